@@ -90,7 +90,7 @@ mssm_status mssm_add_rmsnorm_q8(const mssm_norm_problem* p, const void* x, const
 
 size_t mssm_linear_workspace_bytes(const mssm_linear_problem* p) {
     if (check_linear(p) != MSSM_OK) return 0;
-    return mssm::plan_linear(p->rows, p->in_dim, p->out_dim, p->dtype, device_cus()).ws_bytes;
+    return mssm::plan_linear(p->rows, p->in_dim, p->out_dim, p->dtype, p->out_dtype, device_cus()).ws_bytes;
 }
 
 mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float* x_scale, const void* w,
@@ -102,7 +102,7 @@ mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float
     if (p->dtype == MSSM_F8 ? (!x_scale || !w_scale) : (x_scale || w_scale)) return MSSM_ERR_NULL;
     st = check_align({x, x_scale, w, w_scale, bias, residual, y, workspace});
     if (st != MSSM_OK) return st;
-    const mssm::LinearPlan plan = mssm::plan_linear(p->rows, p->in_dim, p->out_dim, p->dtype, device_cus());
+    const mssm::LinearPlan plan = mssm::plan_linear(p->rows, p->in_dim, p->out_dim, p->dtype, p->out_dtype, device_cus());
     if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes)) return MSSM_ERR_WORKSPACE;
     const mssm::LinearArgs a{p->rows, p->in_dim, p->out_dim, p->dtype, p->out_dtype, p->activation, x, x_scale, w,
                              w_scale, bias, residual, y, plan.splits > 1 ? static_cast<float*>(workspace) : nullptr};

@@ -3,6 +3,8 @@
 #include "block.h"
 #include "device_common.h"
 
+#include <type_traits>
+
 namespace mssm {
 namespace {
 
@@ -26,11 +28,6 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
     if constexpr (DT == MSSM_BF16) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc,
                                                        0, 0, 0);
-    } else if constexpr (DT == MSSM_F8) {
-        typedef int64_t i64x2 __attribute__((ext_vector_type(2)));
-        const i64x2 p = __builtin_bit_cast(i64x2, a), q = __builtin_bit_cast(i64x2, b);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(p[0], q[0], acc, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(p[1], q[1], acc, 0, 0, 0);
     } else {
         const f32x4 p = __builtin_bit_cast(f32x4, a), q = __builtin_bit_cast(f32x4, b);
 #pragma unroll
@@ -49,100 +46,203 @@ struct LinearKernelArgs {
     void* y;
     int64_t M, K, N;
     int act;
+    // tiles [0, full) are one workgroup each; each of the `rest` others is
+    // `splits` workgroups that leave their sums of a part of k in `partial`
+    int64_t full, rest;
+    int splits;
+    float* partial;
 };
 
-__device__ __forceinline__ float activate(float v, int act) {
-    if (act == MSSM_ACT_RELU) return v > 0.0f ? v : 0.0f;
-    if (act == MSSM_ACT_SILU) return v / (1.0f + expf(-v));
-    if (act == MSSM_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+    if constexpr (ACT == MSSM_ACT_RELU) return v > 0.0f || v != v ? v : 0.0f;  // NaN stays
+    if constexpr (ACT == MSSM_ACT_SILU) return silu(v);
+    if constexpr (ACT == MSSM_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     return v;
 }
 
-// Four neighbouring outputs of row m from column n on.
-template <int DT, typename O>
-__device__ __forceinline__ void store_outputs(const LinearKernelArgs& a, int64_t m, int64_t n, f32x4 v, float xs) {
-    const int64_t o = m * a.N + n;
-    if ((a.N & 3) == 0) {  // whole vectors, aligned
-        if (n >= a.N) return;
-        if constexpr (DT == MSSM_F8) v *= xs * *reinterpret_cast<const f32x4*>(a.ws + n);
-        if (a.bias) v += *reinterpret_cast<const f32x4*>(a.bias + n);
+// f(std::integral_constant<int, activation>): the epilogue's loops are compiled
+// once for each activation, a test in each element would multiply their code.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+    if (act == MSSM_ACT_NONE) f(std::integral_constant<int, MSSM_ACT_NONE>{});
+    else if (act == MSSM_ACT_RELU) f(std::integral_constant<int, MSSM_ACT_RELU>{});
+    else if (act == MSSM_ACT_SILU) f(std::integral_constant<int, MSSM_ACT_SILU>{});
+    else f(std::integral_constant<int, MSSM_ACT_GELU>{});
+}
+
+// `C` neighbouring values of a float32 row (C a multiple of 4, 16-byte aligned).
+template <int C>
+__device__ __forceinline__ void load_columns(const float* p, float (&v)[C]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
-        if constexpr (sizeof(O) == 4) {
-            if (a.res) v += *reinterpret_cast<const f32x4*>(static_cast<const O*>(a.res) + o);
-            *reinterpret_cast<f32x4*>(static_cast<O*>(a.y) + o) = v;
-        } else {
-            if (a.res) {
-                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const O*>(a.res) + o);
-                v += f32x4{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
-            }
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<bf16x4*>(static_cast<O*>(a.y) + o) = __builtin_convertvector(v, bf16x4);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (n + i >= a.N) return;
-            float u = v[i];
-            if constexpr (DT == MSSM_F8) u *= xs * a.ws[n + i];
-            if (a.bias) u += a.bias[n + i];
-            u = activate(u, a.act);
-            if (a.res) u += load_act(static_cast<const O*>(a.res), o + i);
-            store_act(static_cast<O*>(a.y), o + i, u);
-        }
+    for (int c = 0; c < C; c += 4) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(p + c);
+        v[c] = q[0]; v[c + 1] = q[1]; v[c + 2] = q[2]; v[c + 3] = q[3];
     }
 }
 
-// 64 x 64 outputs a workgroup of 4 waves, k in steps of 64 bytes through LDS,
-// loaded byte group by byte group with bounds checks (zeros outside).
+template <typename O> struct OutVec;  // 16 bytes of outputs
+template <> struct OutVec<float> {
+    typedef f32x4 Raw;
+    static constexpr int kCols = 4;
+    __device__ static float get(const Raw& r, int c) { return r[c]; }
+    __device__ static void set(Raw& r, int c, float v) { r[c] = v; }
+};
+template <> struct OutVec<uint16_t> {
+    typedef bf16x8 Raw;
+    static constexpr int kCols = 8;
+    __device__ static float get(const Raw& r, int c) { return static_cast<float>(r[c]); }
+    __device__ static void set(Raw& r, int c, float v) { r[c] = static_cast<__bf16>(v); }
+};
+
+// A wave's 64 x 64 float32 block, staged in 16 KB of LDS, as finished outputs.
+// The accumulators hold four columns of a row in each lane; stored from there
+// a row's 128 bytes would leave in 32-byte pieces.  Through LDS (16-byte
+// chunk c of row i at place c ^ i % 16: no bank is hit twice) every store is
+// 16 bytes a lane and whole rows, past the caches: an 8-bit in-projection of
+// 16,384 x 2,560 x 10,240 takes 396 us with it, 430 us without the streaming
+// stores and 456 us storing from the accumulators.  The residual is read
+// ahead of the stores, behind which it would have to wait.
 template <int DT, typename O>
-__global__ __launch_bounds__(256) void linear_kernel(LinearKernelArgs a) {
-    constexpr int E = Elem<DT>::kBytes, KB = 64, PITCH = KB + 16;
-    __shared__ __align__(16) uint8_t sx[64 * PITCH], sw[64 * PITCH];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 64, n0 = static_cast<int64_t>(blockIdx.x) * 64;
-    const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
-    const int64_t kbytes = a.K * E;
-    f32x4 acc[4] = {};
-    for (int64_t k0 = 0; k0 < kbytes; k0 += KB) {
-        for (int i = threadIdx.x; i < 64 * KB / E; i += 256) {
-            const int row = i / (KB / E), kb = i % (KB / E) * E;
-            const bool in_k = k0 + kb < kbytes;
-            const bool in_x = in_k && m0 + row < a.M, in_w = in_k && n0 + row < a.N;
-            const int64_t ox = (m0 + row) * kbytes + k0 + kb, ow = (n0 + row) * kbytes + k0 + kb;
-            if constexpr (E == 4) {
-                *reinterpret_cast<uint32_t*>(sx + row * PITCH + kb) = in_x ? *reinterpret_cast<const uint32_t*>(a.x + ox) : 0;
-                *reinterpret_cast<uint32_t*>(sw + row * PITCH + kb) = in_w ? *reinterpret_cast<const uint32_t*>(a.w + ow) : 0;
-            } else if constexpr (E == 2) {
-                *reinterpret_cast<uint16_t*>(sx + row * PITCH + kb) = in_x ? *reinterpret_cast<const uint16_t*>(a.x + ox) : 0;
-                *reinterpret_cast<uint16_t*>(sw + row * PITCH + kb) = in_w ? *reinterpret_cast<const uint16_t*>(a.w + ow) : 0;
-            } else {
-                sx[row * PITCH + kb] = in_x ? a.x[ox] : 0;
-                sw[row * PITCH + kb] = in_w ? a.w[ow] : 0;
-            }
-        }
-        __syncthreads();
-        const u32x4 wf = *reinterpret_cast<const u32x4*>(sw + (wave * 16 + r) * PITCH + g * 16);
+struct BlockOut {
+    static constexpr int CPL = OutVec<O>::kCols, LPR = 64 / CPL, RPI = 64 / LPR, STEPS = 64 / RPI;
+    typedef typename OutVec<O>::Raw Raw;
+    Raw res[STEPS];
+
+    __device__ __forceinline__ static bool whole(const LinearKernelArgs& a) { return a.N % CPL == 0; }
+
+    __device__ __forceinline__ void load_residual(const LinearKernelArgs& a, int64_t m0, int64_t n0, int lane) {
+        const int64_t n = n0 + lane % LPR * CPL;
+        if (!a.res || !whole(a)) return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[j] = mma<DT>(wf, *reinterpret_cast<const u32x4*>(sx + (j * 16 + r) * PITCH + g * 16), acc[j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + j * 16 + r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t n = n0 + wave * 16 + g * 4 + i;
-            if (m < a.M && n < a.N) {
-                float v = acc[j][i];
-                if constexpr (DT == MSSM_F8) v *= a.xs[m] * a.ws[n];
-                if (a.bias) v += a.bias[n];
-                v = activate(v, a.act);
-                if (a.res) v += load_act(static_cast<const O*>(a.res), m * a.N + n);
-                store_act(static_cast<O*>(a.y), m * a.N + n, v);
-            }
+        for (int q = 0; q < STEPS; ++q) {
+            const int64_t m = m0 + q * RPI + lane / LPR;
+            if (m < a.M && n < a.N) res[q] = *reinterpret_cast<const Raw*>(static_cast<const O*>(a.res) + m * a.N + n);
         }
     }
+
+    __device__ __forceinline__ void stage(uint8_t* lds, int row, int col4, f32x4 v) const {
+        *reinterpret_cast<f32x4*>(lds + row * 256 + ((col4 ^ (row & 15)) * 16)) = v;
+    }
+
+    template <int ACT>
+    __device__ __forceinline__ void store_rows(const LinearKernelArgs& a, const uint8_t* lds, int64_t m0, int64_t n0, int lane) const {
+        const int64_t n = n0 + lane % LPR * CPL;
+        if (n >= a.N) return;
+        float ws[CPL], bias[CPL] = {}, xs[STEPS];
+        if constexpr (DT == MSSM_F8) load_columns<CPL>(a.ws + n, ws);
+        if (a.bias) load_columns<CPL>(a.bias + n, bias);
+        if constexpr (DT == MSSM_F8) {
+#pragma unroll
+            for (int q = 0; q < STEPS; ++q) xs[q] = a.xs[imin64(m0 + q * RPI + lane / LPR, a.M - 1)];
+        }
+#pragma unroll
+        for (int q = 0; q < STEPS; ++q) {
+            const int row = q * RPI + lane / LPR;
+            const int64_t m = m0 + row;
+            Raw out;
+#pragma unroll
+            for (int c4 = 0; c4 < CPL / 4; ++c4) {
+                const f32x4 v =
+                    *reinterpret_cast<const f32x4*>(lds + row * 256 + (((lane % LPR * (CPL / 4) + c4) ^ (row & 15)) * 16));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float u = v[c];
+                    if constexpr (DT == MSSM_F8) u *= xs[q] * ws[c4 * 4 + c];
+                    u = activate<ACT>(u + bias[c4 * 4 + c]);
+                    if (a.res) u += OutVec<O>::get(res[q], c4 * 4 + c);
+                    OutVec<O>::set(out, c4 * 4 + c, u);
+                }
+            }
+            if (m < a.M) __builtin_nontemporal_store(out, reinterpret_cast<Raw*>(static_cast<O*>(a.y) + m * a.N + n));
+        }
+    }
+
+    // Rows that start off a 16-byte boundary: a column a lane.
+    template <int ACT>
+    __device__ __forceinline__ void store_columns(const LinearKernelArgs& a, const uint8_t* lds, int64_t m0, int64_t n0, int lane) const {
+        const int64_t n = n0 + lane;
+        if (n >= a.N) return;
+        const float ws = DT == MSSM_F8 ? a.ws[n] : 1.0f, bias = a.bias ? a.bias[n] : 0.0f;
+        constexpr int BATCH = 8;
+        for (int r0 = 0; r0 < 64 && m0 + r0 < a.M; r0 += BATCH) {
+            float xs[BATCH], add[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int64_t m = imin64(m0 + r0 + i, a.M - 1);
+                xs[i] = DT == MSSM_F8 ? a.xs[m] * ws : 1.0f;
+                add[i] = a.res ? load_act(static_cast<const O*>(a.res), m * a.N + n) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int row = r0 + i;
+                float u = *reinterpret_cast<const float*>(lds + row * 256 + (((lane >> 2) ^ (row & 15)) * 16) + (lane & 3) * 4);
+                if constexpr (DT == MSSM_F8) u *= xs[i];
+                u = activate<ACT>(u + bias) + add[i];
+                if (m0 + row < a.M) store_act(static_cast<O*>(a.y), (m0 + row) * a.N + n, u);
+            }
+        }
+    }
+
+    __device__ __forceinline__ static void store_sums(const uint8_t* lds, float* to, int pitch, int64_t rows, int lane) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int row = q * 4 + (lane >> 4);
+            if (row < rows)
+                *reinterpret_cast<f32x4*>(to + row * pitch + (lane & 15) * 4) =
+                    *reinterpret_cast<const f32x4*>(lds + row * 256 + (((lane & 15) ^ (row & 15)) * 16));
+        }
+    }
+
+    __device__ __forceinline__ void store(const LinearKernelArgs& a, const uint8_t* lds, int64_t m0, int64_t n0, int lane) const {
+        with_activation(a.act, [&](auto act) {
+            if (whole(a)) store_rows<act>(a, lds, m0, n0, lane);
+            else store_columns<act>(a, lds, m0, n0, lane);
+        });
+    }
+};
+
+// ---- operand rows ------------------------------------------------------------
+
+constexpr int kTileBytes = 128;             // k bytes of a step's row: eight 16-byte chunks
+constexpr uint32_t kOutside = 0x7fff0000u;  // beyond any slab's range (below 2^30 bytes)
+
+// Some rows of an operand: reads outside them give zeros.
+struct Slab {
+    const uint8_t* base;
+    uint32_t bytes;
+    __amdgpu_buffer_rsrc_t rsrc;
+    __device__ __forceinline__ Slab(const uint8_t* p, int64_t row, int64_t rows, int64_t end, int64_t kbytes)
+        : base(uniform_ptr(p + row * kbytes)), bytes(static_cast<uint32_t>(imin64(rows, end - row) * kbytes)),
+          rsrc(make_rsrc(base, __builtin_amdgcn_readfirstlane(bytes))) {}
+};
+
+// The 16 bytes at k byte `k` of slab row `row`, zeros beyond the row's kbytes,
+// of rows that are multiples of 16 bytes long.
+__device__ __forceinline__ u32x4 load_even(const Slab& s, uint32_t row, uint32_t k, uint32_t kbytes) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s.rsrc, k < kbytes ? row * kbytes + k : kOutside, 0, 0));
+}
+
+// The same of rows of any length, whose chunks start anywhere: five aligned
+// words around the chunk, shifted into place.  Only for k + 20 <= kbytes: the
+// fifth word then lies in the row as well (rows outside the slab hold anything,
+// as do the outputs that they go to).
+__device__ __forceinline__ u32x4 load_inside(const Slab& s, uint32_t row, uint32_t k, uint32_t kbytes) {
+    const uint32_t off = row * kbytes + k, at = off & ~3u, shift = off & 3u;
+    const u32x4 q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s.rsrc, at, 0, 0));
+    const uint32_t e = __builtin_amdgcn_raw_buffer_load_b32(s.rsrc, at + 16, 0, 0);
+    return u32x4{__builtin_amdgcn_alignbyte(q[1], q[0], shift), __builtin_amdgcn_alignbyte(q[2], q[1], shift),
+                 __builtin_amdgcn_alignbyte(q[3], q[2], shift), __builtin_amdgcn_alignbyte(e, q[3], shift)};
+}
+
+// The same near the end of a row: byte by byte.
+__device__ __forceinline__ u32x4 load_end(const Slab& s, uint32_t row, uint32_t k, uint32_t kbytes) {
+    u32x4 v = {0, 0, 0, 0};
+    const uint32_t off = row * kbytes + k, n = k < kbytes && off < s.bytes ? (kbytes - k < 16 ? kbytes - k : 16) : 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i)
+        v[i / 4] |= static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b8(s.rsrc, i < n ? off + i : kOutside, 0, 0)) << (8 * (i & 3));
+    return v;
 }
 
 // ---- the tile kernel ---------------------------------------------------------
@@ -171,128 +271,504 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, i32x4 rsrc, uint32_t v
 // The tile that was being loaded is in LDS and nobody reads the other one any more.
 __device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Workgroup -> tile: the hardware deals workgroups to the 8 XCDs in turn, so
-// each XCD gets one contiguous range of tiles, walked in bands of 4 tile rows:
-// its 32 CUs then share 4 + 8 operand slabs in their L2.
+// Tile number -> place: tiles are walked in bands of 4 tile rows, so that
+// neighbours in number share 4 + 8 operand slabs of 32 tiles.
 struct TileAt { int64_t m, n; };
-__device__ __forceinline__ TileAt tile_of(uint32_t id, int64_t tm, int64_t tn) {
-    const int64_t T = tm * tn, xcd = id & 7, i = id >> 3, q = T >> 3, rem = T & 7;
-    const int64_t t = xcd * q + (xcd < rem ? xcd : rem) + i;
+__device__ __forceinline__ TileAt tile_at(int64_t t, int64_t tm, int64_t tn) {
     const int64_t band = t / (4 * tn), m0 = band * 4, rows = tm - m0 < 4 ? tm - m0 : 4, in = t - band * 4 * tn;
     return {m0 + in % rows, in / rows};
 }
 
-constexpr int kTileBytes = 128;             // k bytes of a tile row: eight 16-byte chunks
-constexpr uint32_t kOutside = 0x7fff0000u;  // beyond any tile's range (below 2^30 bytes)
-
-// Products over a tile row's two 64-byte halves.
-template <int DT>
-__device__ __forceinline__ f32x4 mma2(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x4 acc) {
-    if constexpr (DT == MSSM_F8) {
-        typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-        const i32x8 p = __builtin_bit_cast(i32x8, __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        const i32x8 q = __builtin_bit_cast(i32x8, __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, acc, 0, 0, 0, 0, 0, 0);
-    } else {
-        return mma<DT>(a[1], b[1], mma<DT>(a[0], b[0], acc));
+// A fragment as the matrix instructions take it: two 16-byte chunks of a row,
+// 64 bytes of k apart.  The 8-bit instructions drop the low bits of their
+// products (the sum of 2,560 normal ones is 1.5e-5 off, relative; with the
+// operands widened to bfloat16, which is exact, 3e-7 and half the rate).  A
+// bfloat16 output (2^-8) does not show it, a float32 one would: WIDE is that.
+template <int DT, bool WIDE>
+struct Frag {
+    u32x4 h[2];
+    __device__ __forceinline__ void set(u32x4 a, u32x4 b) { h[0] = a, h[1] = b; }
+    __device__ __forceinline__ static f32x4 mma(const Frag& p, const Frag& q, f32x4 acc) {
+        if constexpr (DT == MSSM_F8) {
+            typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+            const i32x8 u = __builtin_bit_cast(i32x8, __builtin_shufflevector(p.h[0], p.h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            const i32x8 v = __builtin_bit_cast(i32x8, __builtin_shufflevector(q.h[0], q.h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, acc, 0, 0, 0, 0, 0, 0);
+        } else {
+            return mssm::mma<DT>(p.h[1], q.h[1], mssm::mma<DT>(p.h[0], q.h[0], acc));
+        }
     }
-}
+};
+template <>
+struct Frag<MSSM_F8, true> {
+    bf16x8 v[4];
+    __device__ __forceinline__ void set(u32x4 a, u32x4 b) {
+        widen(a, v[0], v[1]);
+        widen(b, v[2], v[3]);
+    }
+    __device__ __forceinline__ static void widen(u32x4 c, bf16x8& lo, bf16x8& hi) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        bf16x2 p[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false);
+            p[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true);
+        }
+        lo = bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+        hi = bf16x8{p[4][0], p[4][1], p[5][0], p[5][1], p[6][0], p[6][1], p[7][0], p[7][1]};
+    }
+    __device__ __forceinline__ static f32x4 mma(const Frag& p, const Frag& q, f32x4 acc) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p.v[i], q.v[i], acc, 0, 0, 0);
+        return acc;
+    }
+};
 
-template <int DT, typename O, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearKernelArgs a) {
+template <int DT, typename O, int BM, int BN, int WM, int WN, bool EVEN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(LinearKernelArgs a) {
     constexpr int E = Elem<DT>::kBytes, WAVES = WM * WN;
     constexpr int XB = BM * kTileBytes, WB = BN * kTileBytes, STAGE = XB + WB;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16-row fragments of a wave
     constexpr int LX = BM / (8 * WAVES), LW = BN / (8 * WAVES);
     __shared__ __align__(1024) uint8_t lds[2 * STAGE];
-    const TileAt at = tile_of(blockIdx.x, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN);
+    // The hardware deals workgroups to the 8 XCDs in turn: each XCD gets one
+    // contiguous range of the whole tiles (full is a multiple of 8, or all).
+    const int64_t id = blockIdx.x, whole = a.full;
+    const bool split = id >= whole;
+    const int64_t t_id = split ? whole + (id - whole) % a.rest
+                               : (id & 7) * (whole >> 3) + ((id & 7) < (whole & 7) ? (id & 7) : (whole & 7)) + (id >> 3);
+    const int part = split ? static_cast<int>((id - whole) / a.rest) : 0;
+    const TileAt at = tile_at(t_id, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN);
     const int64_t m0 = at.m * BM, n0 = at.n * BN, kbytes = a.K * E;
     const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
-    const i32x4 rx = buffer_words(a.x + m0 * kbytes, static_cast<uint32_t>(imin64(BM, a.M - m0) * kbytes));
-    const i32x4 rw = buffer_words(a.w + n0 * kbytes, static_cast<uint32_t>(imin64(BN, a.N - n0) * kbytes));
-
     // Row `row` of a tile keeps its chunk c at place c ^ (row / 2 % 8): the 16
     // rows that a fragment read touches lie in 16 different bank groups.  The
     // loads write LDS linearly, so the lane fetches the chunk of its place.
     const int lrow = wave * 8 + (lane >> 3), lchunk = (lane & 7) ^ ((lrow >> 1) & 7);
-    const uint32_t base = lrow * static_cast<uint32_t>(kbytes) + lchunk * 16;
     const int64_t tiles = (kbytes + kTileBytes - 1) / kTileBytes;
+    const int64_t first = split ? tiles * part / a.splits : 0, last = split ? tiles * (part + 1) / a.splits : tiles;
+    const Slab sx(a.x, m0, BM, a.M, kbytes), sw(a.w, n0, BN, a.N, kbytes);
+    // EVEN rows go from memory to LDS by themselves; others through registers,
+    // loaded a step ahead and written when their buffer is free.
+    const i32x4 rx = buffer_words(sx.base, sx.bytes), rw = buffer_words(sw.base, sw.bytes);
+    const uint32_t base = lrow * static_cast<uint32_t>(kbytes) + lchunk * 16;
     const bool tail_out = (tiles - 1) * kTileBytes + lchunk * 16 >= kbytes;
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+    u32x4 held[EVEN ? 1 : LX + LW];
     auto load = [&](int64_t t) {
-        const uint32_t soff = static_cast<uint32_t>(t * kTileBytes);
-        const bool out = t == tiles - 1 && tail_out;
-        const uint32_t to = lds0 + static_cast<uint32_t>(t & 1) * STAGE + wave * 1024;
+        if constexpr (EVEN) {
+            const uint32_t soff = static_cast<uint32_t>(t * kTileBytes);
+            const bool out = t == tiles - 1 && tail_out;
+            const uint32_t to = lds0 + static_cast<uint32_t>(t & 1) * STAGE + wave * 1024;
 #pragma unroll
-        for (int i = 0; i < LX; ++i)
-            load_to_lds(to + i * WAVES * 1024, rx, out ? kOutside : base + i * WAVES * 8 * static_cast<uint32_t>(kbytes), soff);
+            for (int i = 0; i < LX; ++i)
+                load_to_lds(to + i * WAVES * 1024, rx, out ? kOutside : base + i * WAVES * 8 * static_cast<uint32_t>(kbytes), soff);
 #pragma unroll
-        for (int i = 0; i < LW; ++i)
-            load_to_lds(to + XB + i * WAVES * 1024, rw, out ? kOutside : base + i * WAVES * 8 * static_cast<uint32_t>(kbytes), soff);
+            for (int i = 0; i < LW; ++i)
+                load_to_lds(to + XB + i * WAVES * 1024, rw, out ? kOutside : base + i * WAVES * 8 * static_cast<uint32_t>(kbytes), soff);
+        } else {
+            const uint32_t k = static_cast<uint32_t>(t * kTileBytes) + lchunk * 16, kb = static_cast<uint32_t>(kbytes);
+            if ((t + 1) * kTileBytes + 4 <= kbytes) {
+#pragma unroll
+                for (int i = 0; i < LX + LW; ++i)
+                    held[i] = load_inside(i < LX ? sx : sw, lrow + (i < LX ? i : i - LX) * WAVES * 8, k, kb);
+            } else {
+#pragma unroll
+                for (int i = 0; i < LX + LW; ++i)
+                    held[i] = load_end(i < LX ? sx : sw, lrow + (i < LX ? i : i - LX) * WAVES * 8, k, kb);
+            }
+        }
+    };
+    auto keep = [&](int64_t t) {
+        if constexpr (!EVEN) {
+            uint8_t* to = lds + (t & 1) * STAGE + wave * 1024 + lane * 16;
+#pragma unroll
+            for (int i = 0; i < LX + LW; ++i)
+                *reinterpret_cast<u32x4*>(to + (i < LX ? i * WAVES * 1024 : XB + (i - LX) * WAVES * 1024)) = held[i];
+        }
     };
 
     f32x4 acc[FM][FN] = {};
     const int place = ((g ^ (r >> 1)) & 7) * 16;
     const int xo = (wm * (BM / WM) + r) * kTileBytes + place, wo = XB + (wn * (BN / WN) + r) * kTileBytes + place;
-    load(0);
-    for (int64_t t = 0; t < tiles; ++t) {
+    load(first);
+    keep(first);
+    for (int64_t t = first; t < last; ++t) {
         tile_barrier();
-        if (t + 1 < tiles) load(t + 1);
+        if (t + 1 < last) load(t + 1);
         const uint8_t* st = lds + (t & 1) * STAGE;
-        u32x4 wf[FN][2], xf[2];
+        auto at_lds = [&](int o) { return *reinterpret_cast<const u32x4*>(st + o); };
+        typedef Frag<DT, sizeof(O) == 4> F;
+        F wf[FN], xf;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            wf[j][0] = *reinterpret_cast<const u32x4*>(st + wo + j * 16 * kTileBytes);
-            wf[j][1] = *reinterpret_cast<const u32x4*>(st + (wo ^ 64) + j * 16 * kTileBytes);
-        }
+        for (int j = 0; j < FN; ++j) wf[j].set(at_lds(wo + j * 16 * kTileBytes), at_lds((wo ^ 64) + j * 16 * kTileBytes));
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            xf[0] = *reinterpret_cast<const u32x4*>(st + xo + i * 16 * kTileBytes);
-            xf[1] = *reinterpret_cast<const u32x4*>(st + (xo ^ 64) + i * 16 * kTileBytes);
+            xf.set(at_lds(xo + i * 16 * kTileBytes), at_lds((xo ^ 64) + i * 16 * kTileBytes));
 #pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = mma2<DT>(wf[j], xf, acc[i][j]);
+            for (int j = 0; j < FN; ++j) acc[i][j] = F::mma(wf[j], xf, acc[i][j]);
         }
+        if (t + 1 < last) keep(t + 1);
     }
+    static_assert(BN / WN == 64 && FM % 4 == 0 && WAVES * 16384 <= 2 * STAGE, "64-column waves, 16 KB of LDS each");
+    BlockOut<DT, O> out;
+    uint8_t* mine = lds + wave * 16384;
+    const int64_t mw = m0 + wm * (BM / WM), nw = n0 + wn * 64;
+    auto stage = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int64_t m = m0 + wm * (BM / WM) + i * 16 + r;
-        if (m >= a.M) continue;
-        float xs = 1.0f;
-        if constexpr (DT == MSSM_F8) xs = a.xs[m];
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-            store_outputs<DT, O>(a, m, n0 + wn * (BN / WN) + j * 16 + g * 4, acc[i][j], xs);
-    }
-}
-
-template <int DT, typename O>
-void launch_t(const LinearArgs& a, hipStream_t s) {
-    const LinearKernelArgs k{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.w), a.x_scale, a.w_scale,
-                             a.bias, a.residual, a.y, a.M, a.K, a.N, a.act};
-    if (a.K * Elem<DT>::kBytes % 16 == 0) {
-        if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= 256) {
-            linear_tile_kernel<DT, O, 256, 256, 2, 4><<<dim3(static_cast<uint32_t>(((a.M + 255) / 256) * ((a.N + 255) / 256))), 512, 0, s>>>(k);
-        } else {
-            linear_tile_kernel<DT, O, 128, 128, 2, 2><<<dim3(static_cast<uint32_t>(((a.M + 127) / 128) * ((a.N + 127) / 128))), 256, 0, s>>>(k);
+            for (int j = 0; j < FN; ++j) out.stage(mine, i * 16 + r, j * 4 + g, acc[h * 4 + i][j]);
+    };
+    if (split) {
+        float* sums = a.partial + ((part * a.rest + t_id - whole) * BM + wm * (BM / WM)) * BN + wn * 64;
+        tile_barrier();  // the last step's reads are done
+#pragma unroll
+        for (int h = 0; h < FM / 4; ++h) {
+            stage(h);
+            out.store_sums(mine, sums + h * 64 * BN, BN, a.M - mw - h * 64, lane);
         }
         return;
     }
-    const dim3 grid(static_cast<uint32_t>((a.N + 63) / 64), static_cast<uint32_t>((a.M + 63) / 64));
-    linear_kernel<DT, O><<<grid, 256, 0, s>>>(k);
+    out.load_residual(a, mw, nw, lane);
+    tile_barrier();
+#pragma unroll
+    for (int h = 0; h < FM / 4; ++h) {
+        stage(h);
+        out.store(a, mine, mw + h * 64, nw, lane);
+        if (h + 1 < FM / 4) out.load_residual(a, mw + (h + 1) * 64, nw, lane);
+    }
+}
+
+// ---- few rows ------------------------------------------------------------------
+
+// Four neighbouring outputs of one row from the accumulators.
+template <int DT, typename O, int ACT>
+__device__ __forceinline__ void store_four(const LinearKernelArgs& a, int64_t m, int64_t n, f32x4 v) {
+    if (m >= a.M || n >= a.N) return;
+    const int64_t o = m * a.N + n;
+    O* y = static_cast<O*>(a.y) + o;
+    const O* res = a.res ? static_cast<const O*>(a.res) + o : nullptr;
+    const float xs = DT == MSSM_F8 ? a.xs[m] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int64_t nc = imin64(n + c, a.N - 1);
+        if constexpr (DT == MSSM_F8) v[c] *= xs * a.ws[nc];
+        v[c] = activate<ACT>(v[c] + (a.bias ? a.bias[nc] : 0.0f));
+    }
+    if (a.N % 4 == 0) {
+        if constexpr (sizeof(O) == 4) {
+            if (res) v += *reinterpret_cast<const f32x4*>(res);
+            *reinterpret_cast<f32x4*>(y) = v;
+        } else {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            if (res) v += __builtin_convertvector(*reinterpret_cast<const bf16x4*>(res), f32x4);
+            *reinterpret_cast<bf16x4*>(y) = __builtin_convertvector(v, bf16x4);
+        }
+    } else {
+        float add[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) add[c] = res && n + c < a.N ? load_act(res, c) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (n + c < a.N) store_act(y, c, v[c] + add[c]);
+    }
+}
+
+// At most 16 MF rows: the weight is read once, straight into registers as
+// matrix operands, 16 of its rows a workgroup.  The 8 waves take the 128-byte
+// steps of k in turn, U of them in flight each, and add their sums through LDS
+// in the order of the waves.
+template <int DT, typename O, int MF, bool EVEN>
+__global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
+    constexpr int WAVES = 8, U = MF == 1 ? 4 : 2;
+    __shared__ __align__(16) f32x4 part[WAVES][MF][64];
+    const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const uint32_t kbytes = static_cast<uint32_t>(a.K * Elem<DT>::kBytes);
+    const Slab sw(a.w, n0, 16, a.N, kbytes), sx(a.x, 0, 16 * MF, a.M, kbytes);
+    typedef Frag<DT, sizeof(O) == 4> F;
+    f32x4 acc[MF] = {};
+    auto steps = [&](uint32_t k0, auto chunk) {
+        u32x4 wf[U][2], xf[U][MF][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t k = k0 + u * WAVES * kTileBytes + h * 64 + g * 16;
+                wf[u][h] = chunk(sw, r, k, kbytes);
+#pragma unroll
+                for (int i = 0; i < MF; ++i) xf[u][i][h] = chunk(sx, i * 16 + r, k, kbytes);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                F p, q;
+                p.set(wf[u][0], wf[u][1]);
+                q.set(xf[u][i][0], xf[u][i][1]);
+                acc[i] = F::mma(p, q, acc[i]);
+            }
+    };
+    for (uint32_t k0 = wave * kTileBytes; k0 < kbytes; k0 += WAVES * U * kTileBytes) {
+        if constexpr (EVEN)
+            steps(k0, load_even);
+        else if (k0 + ((U - 1) * WAVES + 1) * kTileBytes + 4 <= kbytes)
+            steps(k0, load_inside);
+        else
+            for (int u = 0; u < U; ++u) {
+                const uint32_t ku = k0 + u * WAVES * kTileBytes;
+                if (ku >= kbytes) break;
+                F p, q;
+                const bool inside = ku + kTileBytes + 4 <= kbytes;
+                auto chunk = [&](const Slab& s, uint32_t row, uint32_t k) {
+                    return inside ? load_inside(s, row, k, kbytes) : load_end(s, row, k, kbytes);
+                };
+                p.set(chunk(sw, r, ku + g * 16), chunk(sw, r, ku + 64 + g * 16));
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    q.set(chunk(sx, i * 16 + r, ku + g * 16), chunk(sx, i * 16 + r, ku + 64 + g * 16));
+                    acc[i] = F::mma(p, q, acc[i]);
+                }
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave >= MF) return;
+    f32x4 v = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += part[w][wave][lane];
+    with_activation(a.act, [&](auto act) { store_four<DT, O, act>(a, wave * 16 + r, n0 + g * 4, v); });
+}
+
+// ---- few columns ---------------------------------------------------------------
+
+// At most 16 FN columns: a workgroup of 8 waves computes all of them for 64
+// rows, so that x is read once.  Waves 0-3 take 16 rows each and the first 64
+// bytes of every k step, waves 4-7 the second 64 bytes (two waves a SIMD, one
+// fetches while the other multiplies); their sums are added through LDS.  Steps
+// arrive in four LDS stages, three of them in flight.
+template <int DT, typename O, int FN>
+__global__ __launch_bounds__(512) void linear_columns_kernel(LinearKernelArgs a) {
+    constexpr int STAGES = 4, LOADS = FN <= 4 ? 2 : 3;  // 64-row loads of all the waves: x, then w (padded)
+    constexpr int STAGE = LOADS * 64 * kTileBytes;
+    __shared__ __align__(1024) uint8_t lds[STAGES * STAGE];
+    const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64, kbytes = a.K * Elem<DT>::kBytes;
+    const Slab sx(a.x, m0, 64, a.M, kbytes), sw(a.w, 0, 16 * FN, a.N, kbytes);
+    const i32x4 rx = buffer_words(sx.base, sx.bytes), rw = buffer_words(sw.base, sw.bytes);
+    const int lrow = wave * 8 + (lane >> 3), lchunk = (lane & 7) ^ ((lrow >> 1) & 7);
+    const int tiles = static_cast<int>((kbytes + kTileBytes - 1) / kTileBytes);
+    const uint32_t base = lrow * static_cast<uint32_t>(kbytes) + lchunk * 16;
+    const bool tail_out = static_cast<int64_t>(tiles - 1) * kTileBytes + lchunk * 16 >= kbytes;
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+    auto load = [&](int t) {
+        const uint32_t soff = static_cast<uint32_t>(t) * kTileBytes, to = lds0 + (t % STAGES) * STAGE + wave * 1024;
+        const bool out = t == tiles - 1 && tail_out;
+        load_to_lds(to, rx, out ? kOutside : base, soff);
+#pragma unroll
+        for (int i = 0; i + 1 < LOADS; ++i)
+            load_to_lds(to + (i + 1) * 8192, rw, out ? kOutside : base + i * 64 * static_cast<uint32_t>(kbytes), soff);
+    };
+    const int half = wave >> 2, xrow = (wave & 3) * 16 + r;
+    const int place = ((half * 4 + g) ^ (r >> 1)) * 16;
+    f32x4 acc[FN] = {};
+    for (int t = 0; t < STAGES - 1 && t < tiles; ++t) load(t);
+    for (int t = 0; t < tiles; ++t) {
+        // step t is here when at most the two later steps are under way
+        if (t + STAGES - 2 < tiles)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(2 * LOADS) : "memory");
+        else
+            tile_barrier();
+        if (t + STAGES - 1 < tiles) load(t + STAGES - 1);
+        const uint8_t* st = lds + (t % STAGES) * STAGE;
+        const u32x4 xf = *reinterpret_cast<const u32x4*>(st + xrow * kTileBytes + place);
+        if constexpr (DT == MSSM_F8) {  // few columns never wait for the matrix cores: widened for both outputs
+            typedef Frag<MSSM_F8, true> F;
+            bf16x8 x0, x1, w0, w1;
+            F::widen(xf, x0, x1);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                F::widen(*reinterpret_cast<const u32x4*>(st + (64 + j * 16 + r) * kTileBytes + place), w0, w1);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x0, acc[j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x1, acc[j], 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[j] = mma<DT>(*reinterpret_cast<const u32x4*>(st + (64 + j * 16 + r) * kTileBytes + place), xf, acc[j]);
+        }
+    }
+    tile_barrier();
+    f32x4* part = reinterpret_cast<f32x4*>(lds) + ((wave & 3) * FN) * 64 + lane;
+    if (half) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) part[j * 64] = acc[j];
+    }
+    __syncthreads();
+    if (half) return;
+    with_activation(a.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) store_four<DT, O, act>(a, m0 + xrow, j * 16 + g * 4, acc[j] + part[j * 64]);
+    });
+}
+
+// The split tiles' parts added in order, and the epilogue: 16 rows of a tile a
+// workgroup, four columns a lane.
+template <int DT, typename O, int BM, int BN>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearKernelArgs a) {
+    constexpr int LPR = BN / 4, ROWS = 256 / LPR;  // lanes a row, rows at a time
+    const int64_t q = blockIdx.x / (BM / 16), r0 = blockIdx.x % (BM / 16) * 16;
+    const TileAt at = tile_at(a.full + q, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN);
+    const int64_t n = at.n * BN + threadIdx.x % LPR * 4;
+    if (n >= a.N) return;
+    const bool whole = a.N % 4 == 0;
+    f32x4 ws = {1, 1, 1, 1}, bias = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int64_t nc = imin64(n + c, a.N - 1);
+        if constexpr (DT == MSSM_F8) ws[c] = a.ws[nc];
+        if (a.bias) bias[c] = a.bias[nc];
+    }
+    with_activation(a.act, [&](auto act) {
+        for (int i = threadIdx.x / LPR; i < 16; i += ROWS) {
+            const int64_t m = at.m * BM + r0 + i;
+            if (m >= a.M) break;
+            const float* p = a.partial + (q * BM + r0 + i) * BN + threadIdx.x % LPR * 4;
+            f32x4 v = *reinterpret_cast<const f32x4*>(p);
+            for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * a.rest * (BM * BN));
+            float xs = 1.0f;
+            if constexpr (DT == MSSM_F8) xs = a.xs[m];
+            const int64_t o = m * a.N + n;
+            O* y = static_cast<O*>(a.y) + o;
+            const O* res = a.res ? static_cast<const O*>(a.res) + o : nullptr;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (DT == MSSM_F8) v[c] *= xs * ws[c];
+                v[c] = activate<act>(v[c] + bias[c]);
+            }
+            if (whole) {
+                if constexpr (sizeof(O) == 4) {
+                    if (res) v += *reinterpret_cast<const f32x4*>(res);
+                    *reinterpret_cast<f32x4*>(y) = v;
+                } else {
+                    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                    if (res) v += __builtin_convertvector(*reinterpret_cast<const bf16x4*>(res), f32x4);
+                    *reinterpret_cast<bf16x4*>(y) = __builtin_convertvector(v, bf16x4);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n + c < a.N) store_act(y, c, v[c] + (res ? load_act(res, c) : 0.0f));
+            }
+        }
+    });
+}
+
+// ---- schedule ----------------------------------------------------------------
+
+template <int DT, typename O, int B, int WM, int WN, bool EVEN>
+void launch_tiles(const LinearKernelArgs& k, const LinearPlan& p, hipStream_t s) {
+    const uint32_t groups = static_cast<uint32_t>(p.full + p.rest * p.splits);
+    linear_tile_kernel<DT, O, B, B, WM, WN, EVEN><<<dim3(groups), 64 * WM * WN, 0, s>>>(k);
+    if (p.splits > 1) linear_join_kernel<DT, O, B, B><<<dim3(static_cast<uint32_t>(p.rest * (B / 16))), 256, 0, s>>>(k);
+}
+
+template <int DT, typename O, int MF>
+void launch_rows(const LinearKernelArgs& k, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>((k.N + 15) / 16));
+    if (k.K * Elem<DT>::kBytes % 16 == 0)
+        linear_rows_kernel<DT, O, MF, true><<<grid, 512, 0, s>>>(k);
+    else
+        linear_rows_kernel<DT, O, MF, false><<<grid, 512, 0, s>>>(k);
+}
+
+template <int DT, typename O, int FN>
+void launch_columns(const LinearKernelArgs& k, hipStream_t s) {
+    linear_columns_kernel<DT, O, FN><<<dim3(static_cast<uint32_t>((k.M + 63) / 64)), 512, 0, s>>>(k);
+}
+
+template <int DT, typename O>
+void launch_t(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {
+    const LinearKernelArgs k{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.w), a.x_scale, a.w_scale,
+                             a.bias, a.residual, a.y, a.M, a.K, a.N, a.act, p.full, p.rest, p.splits, a.partial};
+    const bool even = a.K * Elem<DT>::kBytes % 16 == 0;
+    switch (p.path) {
+        case LinearPath::kTile256:
+            if constexpr (DT != MSSM_F8 || sizeof(O) == 2) launch_tiles<DT, O, 256, 2, 4, true>(k, p, s);
+            break;
+        case LinearPath::kTile128:
+            even ? launch_tiles<DT, O, 128, 2, 2, true>(k, p, s) : launch_tiles<DT, O, 128, 2, 2, false>(k, p, s);
+            break;
+        case LinearPath::kRows:
+            switch ((a.M + 15) / 16) {
+                case 1: launch_rows<DT, O, 1>(k, s); break;
+                case 2: launch_rows<DT, O, 2>(k, s); break;
+                default: launch_rows<DT, O, 4>(k, s); break;
+            }
+            break;
+        case LinearPath::kColumns:
+            switch ((a.N + 15) / 16) {
+                case 1: launch_columns<DT, O, 1>(k, s); break;
+                case 2: launch_columns<DT, O, 2>(k, s); break;
+                case 3: launch_columns<DT, O, 3>(k, s); break;
+                case 4: launch_columns<DT, O, 4>(k, s); break;
+                case 5: launch_columns<DT, O, 5>(k, s); break;
+                case 6: launch_columns<DT, O, 6>(k, s); break;
+                default: launch_columns<DT, O, 8>(k, s); break;
+            }
+            break;
+    }
+}
+
+// Time of T tiles (us): a round of all the slots takes `depth` k steps of
+// `step` us and `ends` us around them; a last round of few tiles is cut along k
+// into `splits` when that saves more than its partial sums' traffic (written and
+// read at about 4 TB/s) and second pass cost.
+struct Schedule { int64_t full, rest; int splits; double us; };
+Schedule schedule(int64_t T, int64_t depth, int64_t slots, double step, double ends, double tile_mb) {
+    const int64_t rest = T % slots, full = T - rest;
+    const double round = depth * step + ends;
+    Schedule best{T, 0, 1, static_cast<double>((T + slots - 1) / slots) * round};
+    if (rest == 0) return best;
+    for (int64_t s = 2; s <= slots / rest && s * 4 <= depth; ++s) {
+        const double us = full / slots * round + (depth + s - 1) / s * step + ends + 5.0 + 2.0 * rest * s * tile_mb / 4.0;
+        if (us < best.us) best = {full, rest, static_cast<int>(s), us};
+    }
+    return best;
 }
 
 }  // namespace
 
-LinearPlan plan_linear(int64_t, int64_t, int64_t, int, int64_t) { return {1, 0}; }
+// The variant and its cut.  Step times are measured on whole rounds at 16,384 x
+// 2,560 x 10,240: a 256 x 256 tile takes 1.65 us a 128-byte k step (float32
+// 7 us), two 128 x 128 tiles on a CU 1.1 us together (float32 3.5 us).  The large
+// tile moves half the operand bytes, the small one fills the CUs with four
+// times fewer outputs.
+LinearPlan plan_linear(int64_t M, int64_t K, int64_t N, int dtype, int out_dtype, int64_t cus) {
+    const int64_t kbytes = K * (dtype == MSSM_F32 ? 4 : dtype == MSSM_BF16 ? 2 : 1), depth = (kbytes + kTileBytes - 1) / kTileBytes;
+    if (M <= 16 || (M <= 64 && (N + 15) / 16 * M * kbytes <= int64_t{48} << 20)) return {LinearPath::kRows, 0, 0, 1, 0};
+    const bool even = kbytes % 16 == 0;
+    if (even && N <= 128 && M >= 64 * cus / 2) return {LinearPath::kColumns, 0, 0, 1, 0};
+    const bool f32 = dtype == MSSM_F32;
+    const Schedule big = schedule(((M + 255) / 256) * ((N + 255) / 256), depth, cus, f32 ? 7.0 : 1.65, 8.0, 0.262);
+    const Schedule small = schedule(((M + 127) / 128) * ((N + 127) / 128), depth, 2 * cus, f32 ? 3.5 : 1.1, 5.0, 0.066);
+    const bool wide = dtype == MSSM_F8 && out_dtype == MSSM_F32;  // twice the fragment registers
+    const Schedule& s = even && !wide && big.us < small.us ? big : small;
+    const int64_t tile = &s == &big ? 256 : 128;
+    return {tile == 256 ? LinearPath::kTile256 : LinearPath::kTile128, s.full, s.rest, s.splits,
+         s.splits > 1 ? static_cast<size_t>(s.splits) * s.rest * tile * tile * sizeof(float) : 0};
+}
 
-hipError_t launch_linear(const LinearArgs& a, const LinearPlan&, hipStream_t s) {
+hipError_t launch_linear(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {
     if (a.dtype == MSSM_F32)
-        launch_t<MSSM_F32, float>(a, s);
+        launch_t<MSSM_F32, float>(a, p, s);
     else if (a.dtype == MSSM_BF16)
-        a.out_dtype == MSSM_F32 ? launch_t<MSSM_BF16, float>(a, s) : launch_t<MSSM_BF16, uint16_t>(a, s);
+        a.out_dtype == MSSM_F32 ? launch_t<MSSM_BF16, float>(a, p, s) : launch_t<MSSM_BF16, uint16_t>(a, p, s);
     else
-        a.out_dtype == MSSM_F32 ? launch_t<MSSM_F8, float>(a, s) : launch_t<MSSM_F8, uint16_t>(a, s);
+        a.out_dtype == MSSM_F32 ? launch_t<MSSM_F8, float>(a, p, s) : launch_t<MSSM_F8, uint16_t>(a, p, s);
     return hipGetLastError();
 }
 
