@@ -1,16 +1,22 @@
 """ctypes binding of the operators around the scan (C ABI in include/mssm_block.h).
 
-As binding.py: argument marshalling only, on torch's current HIP stream.
+As binding.py: argument marshalling only, on torch's current HIP stream.  A
+decode step makes these calls once a layer, with kernels of a few microseconds,
+so the marshalling is kept short: problem descriptors and workspace sizes are
+remembered by the sizes they follow from.
 """
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
-from .binding import MSSM_BF16, MSSM_F32, MssmError, _check, _dtype_code, _opt, _ptr, _req, _stream, _workspace, lib
+from .binding import MSSM_BF16, MSSM_F32, MssmError, _dtype_code, _workspace, lib
+from . import binding
 
 MSSM_F8 = 2
+_CODES = {torch.float32: MSSM_F32, torch.bfloat16: MSSM_BF16, torch.float8_e4m3fn: MSSM_F8}
 MAX_BEAMS = 16
 MAX_BEAM_STATES = 16
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
@@ -55,24 +61,68 @@ def _declare():
 _declare()
 
 
+def _req(t, name, shape, dtype):
+    """binding._req, which says what is wrong, for a tensor that is not right at first sight."""
+    if t is None or not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        binding._req(t, name, shape, dtype)
+
+
+def _opt(t, name, shape, dtype):
+    if t is not None:
+        _req(t, name, shape, dtype)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle by the call that torch's own code generators use; the public one builds an object each time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _run(status: int):
+    if status != 0:
+        raise MssmError(status, lib)
+
+
+@lru_cache(maxsize=1024)
+def _norm_problem(rows, dim, code, rcode, eps):
+    p = NormProblem(rows, dim, code, rcode, eps)
+    return ctypes.byref(p), p
+
+
+@lru_cache(maxsize=1024)
+def _linear_problem(rows, k, n, code, ocode, act, device):
+    p = LinearProblem(rows, k, n, code, ocode, act)
+    with torch.cuda.device(device):
+        return ctypes.byref(p), int(lib.mssm_linear_workspace_bytes(ctypes.byref(p))), p
+
+
+@lru_cache(maxsize=1024)
+def _beam_problem(batch, beams, vocab, code, end):
+    p = BeamProblem(batch, beams, vocab, code, end)
+    return ctypes.byref(p), int(lib.mssm_beam_select_workspace_bytes(ctypes.byref(p))), p
+
+
 def _norm_args(x, weight, residual, residual_out, eps):
-    if x is None or x.dim() < 1:
+    shape = () if x is None else x.shape
+    if not shape:
         raise ValueError("x must have at least one dimension")
-    D = x.shape[-1]
-    _req(x, "x", x.shape, x.dtype)
+    D = shape[-1]
     code = _dtype_code(x)
+    _req(x, "x", shape, x.dtype)
     _req(weight, "weight", (D,), torch.float32)
     kept = residual if residual is not None else residual_out
     rcode = _dtype_code(kept) if kept is not None else code
     if residual is not None:
-        _req(residual, "residual", x.shape, residual.dtype)
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
+        _req(residual, "residual", shape, residual.dtype)
     if residual_out is not None:
-        _req(residual_out, "residual_out", x.shape, kept.dtype)
+        _req(residual_out, "residual_out", shape, kept.dtype)
+    elif residual is not None:
+        residual_out = torch.empty_like(residual)
     if not eps >= 0.0:
         raise ValueError(f"eps = {eps} must not be negative")
-    return NormProblem(x.numel() // D if D else 0, D, code, rcode, eps), residual_out
+    return _norm_problem(x.numel() // D if D else 0, D, code, rcode, eps)[0], residual_out
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None):
@@ -85,9 +135,10 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None):
     prob, residual_out = _norm_args(x, weight, residual, residual_out, eps)
     if y is None:
         y = torch.empty_like(x)
-    _req(y, "y", x.shape, x.dtype)
-    _check(lib.mssm_add_rmsnorm(ctypes.byref(prob), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y),
-                                _ptr(residual_out), _stream(x.device)))
+    else:
+        _req(y, "y", x.shape, x.dtype)
+    _run(lib.mssm_add_rmsnorm(prob, x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), _ptr(residual_out),
+                              _raw_stream(x.get_device())))
     return y, residual_out
 
 
@@ -98,13 +149,15 @@ def add_rmsnorm_q8(x, weight, residual=None, eps=1e-5, q=None, scale=None, resid
     x_scale."""
     prob, residual_out = _norm_args(x, weight, residual, residual_out, eps)
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    _req(q, "q", x.shape, torch.float8_e4m3fn)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    else:
+        _req(q, "q", x.shape, torch.float8_e4m3fn)
     if scale is None:
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _req(scale, "scale", x.shape[:-1], torch.float32)
-    _check(lib.mssm_add_rmsnorm_q8(ctypes.byref(prob), _ptr(x), _ptr(residual), _ptr(weight), _ptr(q), _ptr(scale),
-                                   _ptr(residual_out), _stream(x.device)))
+    else:
+        _req(scale, "scale", x.shape[:-1], torch.float32)
+    _run(lib.mssm_add_rmsnorm_q8(prob, x.data_ptr(), _ptr(residual), weight.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                 _ptr(residual_out), _raw_stream(x.get_device())))
     return q, scale, residual_out
 
 
@@ -117,21 +170,22 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     "silu" or "gelu" (by erf); residual (..., N) in the output's type.
     out_dtype: float32, or bfloat16 (not with float32 operands); x's type by
     default, bfloat16 with 8-bit operands.  y may be residual."""
-    codes = {torch.float32: MSSM_F32, torch.bfloat16: MSSM_BF16, torch.float8_e4m3fn: MSSM_F8}
     if x is None or w is None or x.dim() < 1 or w.dim() != 2:
         raise ValueError("x must be (..., K) and w (N, K)")
-    if x.dtype not in codes:
+    act = x.dtype
+    if act not in _CODES:
         raise TypeError(f"x must be float32, bfloat16 or float8_e4m3fn, got {x.dtype}")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation {activation!r} is not one of {sorted(k for k in ACTIVATIONS if k)}")
-    lead, K, N = x.shape[:-1], x.shape[-1], w.shape[0]
-    _req(x, "x", x.shape, x.dtype)
-    _req(w, "w", (N, K), x.dtype)
+    shape, N = x.shape, w.shape[0]
+    lead, K = shape[:-1], shape[-1]
+    _req(x, "x", shape, act)
+    _req(w, "w", (N, K), act)
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if x.dtype == torch.float8_e4m3fn else x.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16) or (x.dtype == torch.float32 and out_dtype != torch.float32):
-        raise TypeError(f"out_dtype {out_dtype} is not available for {x.dtype} operands")
-    if x.dtype == torch.float8_e4m3fn:
+        out_dtype = torch.bfloat16 if act == torch.float8_e4m3fn else act
+    if out_dtype not in (torch.float32, torch.bfloat16) or (act == torch.float32 and out_dtype != torch.float32):
+        raise TypeError(f"out_dtype {out_dtype} is not available for {act} operands")
+    if act == torch.float8_e4m3fn:
         _req(x_scale, "x_scale", lead, torch.float32)
         _req(w_scale, "w_scale", (N,), torch.float32)
     elif x_scale is not None or w_scale is not None:
@@ -140,13 +194,14 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     _opt(residual, "residual", (*lead, N), out_dtype)
     if y is None:
         y = torch.empty((*lead, N), dtype=out_dtype, device=x.device)
-    _req(y, "y", (*lead, N), out_dtype)
-    prob = LinearProblem(x.numel() // K if K else 0, K, N, codes[x.dtype], MSSM_F32 if out_dtype == torch.float32 else MSSM_BF16,
-                         ACTIVATIONS[activation])
-    nbytes = int(lib.mssm_linear_workspace_bytes(ctypes.byref(prob)))
+    else:
+        _req(y, "y", (*lead, N), out_dtype)
+    dev = x.get_device()
+    prob, nbytes, _ = _linear_problem(x.numel() // K if K else 0, K, N, _CODES[act], _CODES[out_dtype],
+                                      ACTIVATIONS[activation], dev)
     ws = _workspace(nbytes, x.device, workspace)
-    _check(lib.mssm_linear(ctypes.byref(prob), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
-                           _ptr(residual), _ptr(y), _ptr(ws), nbytes, _stream(x.device)))
+    _run(lib.mssm_linear(prob, x.data_ptr(), _ptr(x_scale), w.data_ptr(), _ptr(w_scale), _ptr(bias), _ptr(residual),
+                         y.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev)))
     return y
 
 
@@ -177,20 +232,22 @@ def beam_select(logits, scores, finished=None, end_token=None, scores_out=None, 
             finished_out = torch.empty((B, K), dtype=torch.bool, device=logits.device)
     _opt(finished_out, "finished_out", (B, K), torch.bool)
     if scores_out is None:
-        scores_out = torch.empty((B, K), dtype=torch.float32, device=logits.device)
-    _req(scores_out, "scores_out", (B, K), torch.float32)
+        scores_out = torch.empty_like(scores)
+    else:
+        _req(scores_out, "scores_out", (B, K), torch.float32)
     if parent is None:
-        parent = torch.empty((B, K), dtype=torch.int32, device=logits.device)
-    _req(parent, "parent", (B, K), torch.int32)
+        parent = torch.empty_like(scores, dtype=torch.int32)
+    else:
+        _req(parent, "parent", (B, K), torch.int32)
     if token is None:
-        token = torch.empty((B, K), dtype=torch.int32, device=logits.device)
-    _req(token, "token", (B, K), torch.int32)
-    prob = BeamProblem(B, K, V, code, -1 if end_token is None else end_token)
-    nbytes = int(lib.mssm_beam_select_workspace_bytes(ctypes.byref(prob)))
+        token = torch.empty_like(parent)
+    else:
+        _req(token, "token", (B, K), torch.int32)
+    prob, nbytes, _ = _beam_problem(B, K, V, code, -1 if end_token is None else end_token)
     ws = _workspace(nbytes, logits.device, workspace)
-    _check(lib.mssm_beam_select(ctypes.byref(prob), _ptr(logits), _ptr(scores), _ptr(finished), _ptr(scores_out),
-                                _ptr(parent), _ptr(token), _ptr(finished_out), _ptr(ws), nbytes,
-                                _stream(logits.device)))
+    _run(lib.mssm_beam_select(prob, logits.data_ptr(), scores.data_ptr(), _ptr(finished), scores_out.data_ptr(),
+                              parent.data_ptr(), token.data_ptr(), _ptr(finished_out), _ptr(ws), nbytes,
+                              _raw_stream(logits.get_device())))
     return scores_out, parent, token, finished_out
 
 
@@ -215,6 +272,7 @@ def beam_reorder(parent, states):
         _req(t, f"states[{i}]", t.shape, t.dtype)
         if t.numel() == 0:
             raise MssmError(-2, lib)
-        entries[i] = BeamState(t.data_ptr(), t.shape[0], t[0, 0].numel() * t.element_size())
-    _check(lib.mssm_beam_reorder(B, K, _ptr(parent), len(each), entries, _stream(parent.device)))
+        e = entries[i]
+        e.data, e.layers, e.bytes = t.data_ptr(), t.shape[0], t.numel() // (t.shape[0] * B * K) * t.element_size()
+    _run(lib.mssm_beam_reorder(B, K, parent.data_ptr(), len(each), entries, _raw_stream(parent.get_device())))
     return states
