@@ -3,6 +3,7 @@
 #include "block.h"
 #include "device_common.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace mssm {
@@ -235,13 +236,26 @@ __device__ __forceinline__ u32x4 load_inside(const Slab& s, uint32_t row, uint32
                  __builtin_amdgcn_alignbyte(q[3], q[2], shift), __builtin_amdgcn_alignbyte(e, q[3], shift)};
 }
 
-// The same near the end of a row: byte by byte.
+// The same near the end of a row: words that end inside the slab, the bytes of
+// the slab's last word if that is cut off, zeros for what is not in the row.
 __device__ __forceinline__ u32x4 load_end(const Slab& s, uint32_t row, uint32_t k, uint32_t kbytes) {
-    u32x4 v = {0, 0, 0, 0};
-    const uint32_t off = row * kbytes + k, n = k < kbytes && off < s.bytes ? (kbytes - k < 16 ? kbytes - k : 16) : 0;
+    const uint32_t off = row * kbytes + k, at = off & ~3u, shift = off & 3u, cut = s.bytes & ~3u;
+    const uint32_t left = k < kbytes && off < s.bytes ? kbytes - k : 0;  // bytes of the row from here on
+    uint32_t w[5], last = 0;
 #pragma unroll
-    for (uint32_t i = 0; i < 16; ++i)
-        v[i / 4] |= static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b8(s.rsrc, i < n ? off + i : kOutside, 0, 0)) << (8 * (i & 3));
+    for (uint32_t d = 0; d < 5; ++d)
+        w[d] = __builtin_amdgcn_raw_buffer_load_b32(s.rsrc, left && at + 4 * d < cut ? at + 4 * d : kOutside, 0, 0);
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i)
+        last |= static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b8(s.rsrc, left && cut + i < s.bytes ? cut + i : kOutside, 0, 0)) << (8 * i);
+#pragma unroll
+    for (uint32_t d = 0; d < 5; ++d) w[d] = at + 4 * d == cut ? last : w[d];
+    u32x4 v;
+#pragma unroll
+    for (uint32_t d = 0; d < 4; ++d) {
+        v[d] = __builtin_amdgcn_alignbyte(w[d + 1], w[d], shift);
+        v[d] = left >= 4 * d + 4 ? v[d] : left <= 4 * d ? 0 : v[d] & ((1u << (8 * (left - 4 * d))) - 1);
+    }
     return v;
 }
 
@@ -476,10 +490,12 @@ __device__ __forceinline__ void store_four(const LinearKernelArgs& a, int64_t m,
     }
 }
 
-// At most 16 MF rows: the weight is read once, straight into registers as
-// matrix operands, 16 of its rows a workgroup.  The 8 waves take the 128-byte
+// Few outputs: 16 MF rows by 16 columns a workgroup, both operands straight from
+// memory into registers as matrix operands.  The 8 waves take the 128-byte
 // steps of k in turn, U of them in flight each, and add their sums through LDS
-// in the order of the waves.
+// in the order of the waves: one launch, and every wave of a decode step's
+// product has its part of the weight under way at once.  1 x 2,560 x 10,240
+// bfloat16 takes 13 us (4.0 TB/s), by split tiles and a second pass 20 us.
 template <int DT, typename O, int MF, bool EVEN>
 __global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
     constexpr int WAVES = 8, U = MF == 1 ? 4 : 2;
@@ -487,13 +503,15 @@ __global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
     const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
     const uint32_t kbytes = static_cast<uint32_t>(a.K * Elem<DT>::kBytes);
-    const Slab sw(a.w, n0, 16, a.N, kbytes), sx(a.x, 0, 16 * MF, a.M, kbytes);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MF);
+    const Slab sw(a.w, n0, 16, a.N, kbytes), sx(a.x, m0, 16 * MF, a.M, kbytes);
     typedef Frag<DT, sizeof(O) == 4> F;
     f32x4 acc[MF] = {};
-    auto steps = [&](uint32_t k0, auto chunk) {
-        u32x4 wf[U][2], xf[U][MF][2];
+    auto steps = [&](auto count, uint32_t k0, auto chunk) {
+        constexpr int C = decltype(count)::value;
+        u32x4 wf[C][2], xf[C][MF][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < C; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t k = k0 + u * WAVES * kTileBytes + h * 64 + g * 16;
@@ -502,7 +520,7 @@ __global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
                 for (int i = 0; i < MF; ++i) xf[u][i][h] = chunk(sx, i * 16 + r, k, kbytes);
             }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < C; ++u)
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
                 F p, q;
@@ -511,27 +529,16 @@ __global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
                 acc[i] = F::mma(p, q, acc[i]);
             }
     };
+    constexpr std::integral_constant<int, U> all;
+    constexpr std::integral_constant<int, 1> one;
     for (uint32_t k0 = wave * kTileBytes; k0 < kbytes; k0 += WAVES * U * kTileBytes) {
         if constexpr (EVEN)
-            steps(k0, load_even);
+            steps(all, k0, load_even);
         else if (k0 + ((U - 1) * WAVES + 1) * kTileBytes + 4 <= kbytes)
-            steps(k0, load_inside);
+            steps(all, k0, load_inside);
         else
-            for (int u = 0; u < U; ++u) {
-                const uint32_t ku = k0 + u * WAVES * kTileBytes;
-                if (ku >= kbytes) break;
-                F p, q;
-                const bool inside = ku + kTileBytes + 4 <= kbytes;
-                auto chunk = [&](const Slab& s, uint32_t row, uint32_t k) {
-                    return inside ? load_inside(s, row, k, kbytes) : load_end(s, row, k, kbytes);
-                };
-                p.set(chunk(sw, r, ku + g * 16), chunk(sw, r, ku + 64 + g * 16));
-#pragma unroll
-                for (int i = 0; i < MF; ++i) {
-                    q.set(chunk(sx, i * 16 + r, ku + g * 16), chunk(sx, i * 16 + r, ku + 64 + g * 16));
-                    acc[i] = F::mma(p, q, acc[i]);
-                }
-            }
+            for (uint32_t k = k0; k < kbytes && k < k0 + WAVES * U * kTileBytes; k += WAVES * kTileBytes)
+                k + kTileBytes + 4 <= kbytes ? steps(one, k, load_inside) : steps(one, k, load_end);
     }
 #pragma unroll
     for (int i = 0; i < MF; ++i) part[wave][i][lane] = acc[i];
@@ -540,24 +547,24 @@ __global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
     f32x4 v = part[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += part[w][wave][lane];
-    with_activation(a.act, [&](auto act) { store_four<DT, O, act>(a, wave * 16 + r, n0 + g * 4, v); });
+    with_activation(a.act, [&](auto act) { store_four<DT, O, act>(a, m0 + wave * 16 + r, n0 + g * 4, v); });
 }
 
 // ---- few columns ---------------------------------------------------------------
 
-// At most 16 FN columns: a workgroup of 8 waves computes all of them for 64
-// rows, so that x is read once.  Waves 0-3 take 16 rows each and the first 64
-// bytes of every k step, waves 4-7 the second 64 bytes (two waves a SIMD, one
+// At most 16 FN columns: a workgroup computes all of them for 16 RG rows, so
+// that x is read once.  The first RG waves take 16 rows each and the first 64
+// bytes of every k step, the others the second 64 bytes (two waves a SIMD, one
 // fetches while the other multiplies); their sums are added through LDS.  Steps
 // arrive in four LDS stages, three of them in flight.
-template <int DT, typename O, int FN>
-__global__ __launch_bounds__(512) void linear_columns_kernel(LinearKernelArgs a) {
-    constexpr int STAGES = 4, LOADS = FN <= 4 ? 2 : 3;  // 64-row loads of all the waves: x, then w (padded)
-    constexpr int STAGE = LOADS * 64 * kTileBytes;
+template <int DT, typename O, int FN, int RG>
+__global__ __launch_bounds__(128 * RG, 2) void linear_columns_kernel(LinearKernelArgs a) {
+    constexpr int STAGES = 4, WL = (FN + RG - 1) / RG, LOADS = 1 + WL;  // 16 RG rows a load of all the waves: x, then w
+    constexpr int ROUND = 16 * RG * kTileBytes, STAGE = LOADS * ROUND;
     __shared__ __align__(1024) uint8_t lds[STAGES * STAGE];
     const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64, kbytes = a.K * Elem<DT>::kBytes;
-    const Slab sx(a.x, m0, 64, a.M, kbytes), sw(a.w, 0, 16 * FN, a.N, kbytes);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * (16 * RG), kbytes = a.K * Elem<DT>::kBytes;
+    const Slab sx(a.x, m0, 16 * RG, a.M, kbytes), sw(a.w, 0, 16 * FN, a.N, kbytes);
     const i32x4 rx = buffer_words(sx.base, sx.bytes), rw = buffer_words(sw.base, sw.bytes);
     const int lrow = wave * 8 + (lane >> 3), lchunk = (lane & 7) ^ ((lrow >> 1) & 7);
     const int tiles = static_cast<int>((kbytes + kTileBytes - 1) / kTileBytes);
@@ -569,10 +576,10 @@ __global__ __launch_bounds__(512) void linear_columns_kernel(LinearKernelArgs a)
         const bool out = t == tiles - 1 && tail_out;
         load_to_lds(to, rx, out ? kOutside : base, soff);
 #pragma unroll
-        for (int i = 0; i + 1 < LOADS; ++i)
-            load_to_lds(to + (i + 1) * 8192, rw, out ? kOutside : base + i * 64 * static_cast<uint32_t>(kbytes), soff);
+        for (int i = 0; i < WL; ++i)
+            load_to_lds(to + (i + 1) * ROUND, rw, out ? kOutside : base + i * 16 * RG * static_cast<uint32_t>(kbytes), soff);
     };
-    const int half = wave >> 2, xrow = (wave & 3) * 16 + r;
+    const int half = wave / RG, xrow = wave % RG * 16 + r;
     const int place = ((half * 4 + g) ^ (r >> 1)) * 16;
     f32x4 acc[FN] = {};
     for (int t = 0; t < STAGES - 1 && t < tiles; ++t) load(t);
@@ -591,18 +598,18 @@ __global__ __launch_bounds__(512) void linear_columns_kernel(LinearKernelArgs a)
             F::widen(xf, x0, x1);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                F::widen(*reinterpret_cast<const u32x4*>(st + (64 + j * 16 + r) * kTileBytes + place), w0, w1);
+                F::widen(*reinterpret_cast<const u32x4*>(st + (16 * RG + j * 16 + r) * kTileBytes + place), w0, w1);
                 acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x0, acc[j], 0, 0, 0);
                 acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x1, acc[j], 0, 0, 0);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                acc[j] = mma<DT>(*reinterpret_cast<const u32x4*>(st + (64 + j * 16 + r) * kTileBytes + place), xf, acc[j]);
+                acc[j] = mma<DT>(*reinterpret_cast<const u32x4*>(st + (16 * RG + j * 16 + r) * kTileBytes + place), xf, acc[j]);
         }
     }
     tile_barrier();
-    f32x4* part = reinterpret_cast<f32x4*>(lds) + ((wave & 3) * FN) * 64 + lane;
+    f32x4* part = reinterpret_cast<f32x4*>(lds) + wave % RG * FN * 64 + lane;
     if (half) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) part[j * 64] = acc[j];
@@ -678,7 +685,7 @@ void launch_tiles(const LinearKernelArgs& k, const LinearPlan& p, hipStream_t s)
 
 template <int DT, typename O, int MF>
 void launch_rows(const LinearKernelArgs& k, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>((k.N + 15) / 16));
+    const dim3 grid(static_cast<uint32_t>((k.N + 15) / 16), static_cast<uint32_t>((k.M + 16 * MF - 1) / (16 * MF)));
     if (k.K * Elem<DT>::kBytes % 16 == 0)
         linear_rows_kernel<DT, O, MF, true><<<grid, 512, 0, s>>>(k);
     else
@@ -687,7 +694,8 @@ void launch_rows(const LinearKernelArgs& k, hipStream_t s) {
 
 template <int DT, typename O, int FN>
 void launch_columns(const LinearKernelArgs& k, hipStream_t s) {
-    linear_columns_kernel<DT, O, FN><<<dim3(static_cast<uint32_t>((k.M + 63) / 64)), 512, 0, s>>>(k);
+    constexpr int RG = 4;  // 16 or 32 rows take 1.8 and 1.04 times as long at 16,384 x 1,536 x 80
+    linear_columns_kernel<DT, O, FN, RG><<<dim3(static_cast<uint32_t>((k.M + 16 * RG - 1) / (16 * RG))), 128 * RG, 0, s>>>(k);
 }
 
 template <int DT, typename O>
@@ -725,8 +733,8 @@ void launch_t(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {
 
 // Time of T tiles (us): a round of all the slots takes `depth` k steps of
 // `step` us and `ends` us around them; a last round of few tiles is cut along k
-// into `splits` when that saves more than its partial sums' traffic (written and
-// read at about 4 TB/s) and second pass cost.
+// into `splits` when that saves more than a second pass (5 us) and the partial
+// sums' traffic (written and read at about 4.5 TB/s, `tile_mb` each) cost.
 struct Schedule { int64_t full, rest; int splits; double us; };
 Schedule schedule(int64_t T, int64_t depth, int64_t slots, double step, double ends, double tile_mb) {
     const int64_t rest = T % slots, full = T - rest;
@@ -734,7 +742,7 @@ Schedule schedule(int64_t T, int64_t depth, int64_t slots, double step, double e
     Schedule best{T, 0, 1, static_cast<double>((T + slots - 1) / slots) * round};
     if (rest == 0) return best;
     for (int64_t s = 2; s <= slots / rest && s * 4 <= depth; ++s) {
-        const double us = full / slots * round + (depth + s - 1) / s * step + ends + 5.0 + 2.0 * rest * s * tile_mb / 4.0;
+        const double us = full / slots * round + (depth + s - 1) / s * step + ends + 5.0 + 2.0 * rest * s * tile_mb / 4.5;
         if (us < best.us) best = {full, rest, static_cast<int>(s), us};
     }
     return best;
@@ -742,24 +750,36 @@ Schedule schedule(int64_t T, int64_t depth, int64_t slots, double step, double e
 
 }  // namespace
 
-// The variant and its cut.  Step times are measured on whole rounds at 16,384 x
-// 2,560 x 10,240: a 256 x 256 tile takes 1.65 us a 128-byte k step (float32
-// 7 us), two 128 x 128 tiles on a CU 1.1 us together (float32 3.5 us).  The large
-// tile moves half the operand bytes, the small one fills the CUs with four
-// times fewer outputs.
+// The variant and its cut, by estimated times (us) from measured step times.
+// Tiles, on whole rounds at 16,384 x 2,560 x 10,240: a 256 x 256 tile takes 1.65
+// us a 128-byte k step (float32 7 us), two 128 x 128 tiles on a CU 1.1 us
+// together (float32 3.5 us); the large tile moves half the operand bytes, the
+// small one fills the CUs with four times fewer outputs.  Few columns: 0.38 us
+// a step of a round of 64-row workgroups (float32 0.22 + 0.11 for each 16
+// columns, its matrix rate).  Few outputs: what they read, the operands once for
+// each block of the other, comes at 6 TB/s, mostly from L2.
 LinearPlan plan_linear(int64_t M, int64_t K, int64_t N, int dtype, int out_dtype, int64_t cus) {
     const int64_t kbytes = K * (dtype == MSSM_F32 ? 4 : dtype == MSSM_BF16 ? 2 : 1), depth = (kbytes + kTileBytes - 1) / kTileBytes;
-    if (M <= 16 || (M <= 64 && (N + 15) / 16 * M * kbytes <= int64_t{48} << 20)) return {LinearPath::kRows, 0, 0, 1, 0};
-    const bool even = kbytes % 16 == 0;
-    if (even && N <= 128 && M >= 64 * cus / 2) return {LinearPath::kColumns, 0, 0, 1, 0};
-    const bool f32 = dtype == MSSM_F32;
-    const Schedule big = schedule(((M + 255) / 256) * ((N + 255) / 256), depth, cus, f32 ? 7.0 : 1.65, 8.0, 0.262);
-    const Schedule small = schedule(((M + 127) / 128) * ((N + 127) / 128), depth, 2 * cus, f32 ? 3.5 : 1.1, 5.0, 0.066);
-    const bool wide = dtype == MSSM_F8 && out_dtype == MSSM_F32;  // twice the fragment registers
-    const Schedule& s = even && !wide && big.us < small.us ? big : small;
-    const int64_t tile = &s == &big ? 256 : 128;
+    const bool f32 = dtype == MSSM_F32, even = kbytes % 16 == 0;
+    const bool wide = dtype == MSSM_F8 && out_dtype == MSSM_F32;  // twice the fragment registers: no large tile
+    auto mb = [&](int64_t t) { return 4e-6 * std::min(M, t) * std::min(N, t); };
+    const Schedule big = schedule(((M + 255) / 256) * ((N + 255) / 256), depth, cus, f32 ? 7.0 : 1.65, 8.0, mb(256));
+    const Schedule small = schedule(((M + 127) / 128) * ((N + 127) / 128), depth, 2 * cus, f32 ? 3.5 : even ? 1.1 : 1.7, 4.0, mb(128));
+    const bool large = even && !wide && big.us < small.us;
+    const Schedule& s = large ? big : small;
+    const int64_t tile = large ? 256 : 128;
+
+    const int64_t block = M <= 16 ? 16 : M <= 32 ? 32 : 64, blocks_m = (M + block - 1) / block, blocks_n = (N + 15) / 16;
+    const double read = static_cast<double>(blocks_n * M + blocks_m * N) * kbytes * 1e-6;
+    const double flops = 2e-6 * blocks_m * block * blocks_n * 16 * K;
+    const double rows = 4.0 + std::max(read / 6.0, flops / (f32 ? 100.0 : 500.0));
+    const int64_t fn = (N + 15) / 16;
+    const double columns = even && N <= 128
+                               ? 3.0 + (M + 64 * cus - 1) / (64 * cus) * depth * (f32 ? 0.22 + 0.11 * fn : 0.38) : 1e30;
+    if (blocks_m < 65536 && rows <= columns && rows <= s.us) return {LinearPath::kRows, 0, 0, 1, 0};
+    if (columns <= s.us) return {LinearPath::kColumns, 0, 0, 1, 0};
     return {tile == 256 ? LinearPath::kTile256 : LinearPath::kTile128, s.full, s.rest, s.splits,
-         s.splits > 1 ? static_cast<size_t>(s.splits) * s.rest * tile * tile * sizeof(float) : 0};
+            s.splits > 1 ? static_cast<size_t>(s.splits) * s.rest * tile * tile * sizeof(float) : 0};
 }
 
 hipError_t launch_linear(const LinearArgs& a, const LinearPlan& p, hipStream_t s) {

@@ -169,3 +169,34 @@ def test_bitwise_repeats_on_another_stream(mssm):
             ys = [mssm.linear(x, w, activation="gelu") for _ in range(3)]
         st.synchronize()
         assert all(torch.equal(y, t) for t in ys)
+
+
+@pytest.mark.parametrize("dtype,out", PAIRS)
+@pytest.mark.parametrize("M,K,N", [(8200, 96, 17), (8300, 200, 128), (16400, 64, 33), (16385, 48, 80), (9000, 416, 100), (16384, 16, 16)])
+def test_few_columns(mssm, M, K, N, dtype, out):
+    run_exact(mssm, M, K, N, dtype, out)
+
+
+@pytest.mark.parametrize("dtype,out", PAIRS)
+@pytest.mark.parametrize("K", [1921, 2049, 2111, 2113, 3071, 4090])
+def test_uneven_rows_end_anywhere_in_a_wave_s_steps(mssm, K, dtype, out):
+    run_exact(mssm, 5, K, 37, dtype, out)      # few outputs
+    run_exact(mssm, 70, K, 50, dtype, out)
+    run_exact(mssm, 600, K, 1300, dtype, out)  # tiles
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f8"])
+def test_large_tiles_with_a_split_tail(mssm, dtype):
+    # 17 x 16 tiles of 256: one round of 256 and a tail that is cut along in_dim
+    run_exact(mssm, 4352, 4096 // {"f32": 4, "bf16": 2, "f8": 1}[dtype], 4096, dtype, "f32" if dtype == "f32" else "bf16")
+
+
+def test_eight_bit_sums_keep_float32_accuracy(mssm):
+    # a float32 output shows what the 8-bit matrix instructions drop (1.5e-5): below 1e-6 here
+    g = torch.Generator().manual_seed(9)
+    for M, K, N in ((4, 2560, 512), (300, 2560, 512), (1100, 512, 1100), (8300, 512, 64)):
+        x, w = (30 * torch.randn((M, K), generator=g)).to(DT["f8"]), (30 * torch.randn((N, K), generator=g)).to(DT["f8"])
+        one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+        y = mssm.linear(x.cuda(), w.cuda(), x_scale=one(M), w_scale=one(N), out_dtype=torch.float32)
+        want = np64(x) @ np64(w).T
+        assert np.linalg.norm(np64(y) - want) <= 1e-6 * np.linalg.norm(want)
