@@ -456,9 +456,15 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
         };
         a.dtype == MSSM_F32 ? pick(0.0f) : pick(uint16_t{0});
     }
-    beam_merge_kernel<<<dim3(static_cast<uint32_t>(a.B)), 512, 0, s>>>(a.scores, a.finished, a.end_token, a.V, K,
-                                                                      static_cast<int>(p.parts), best, stat, a.scores_out,
-                                                                      a.parent, a.token, a.finished_out);
+    // a launch has fewer than 2^32 threads: 2^22 batch rows at a time
+    constexpr int64_t kBatch = int64_t{1} << 22;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kBatch) {
+        const int64_t r0 = b0 * a.K;
+        beam_merge_kernel<<<dim3(static_cast<uint32_t>(imin64(kBatch, a.B - b0))), 512, 0, s>>>(
+            a.scores + r0, a.finished ? a.finished + r0 : nullptr, a.end_token, a.V, K, static_cast<int>(p.parts),
+            best + r0 * p.parts * a.K, stat + r0 * p.parts, a.scores_out + r0, a.parent + r0, a.token + r0,
+            a.finished_out ? a.finished_out + r0 : nullptr);
+    }
     return hipGetLastError();
 }
 
@@ -473,7 +479,7 @@ hipError_t launch_beam_reorder(int64_t B, int64_t K, const int32_t* parent, int 
         a.st[i] = st[i];
         a.first[i + 1] = a.first[i] + st[i].layers * B * ((st[i].bytes + 16 * kColumns - 1) / (16 * kColumns));
     }
-    const dim3 grid(static_cast<uint32_t>(imin64(a.first[count], int64_t{1} << 30)));
+    const dim3 grid(static_cast<uint32_t>(imin64(a.first[count], int64_t{1} << 23)));  // below 2^32 threads; the kernel strides
     if (K <= 4)
         beam_reorder_kernel<4><<<grid, kColumns, 0, s>>>(a);
     else if (K <= 8)

@@ -774,9 +774,10 @@ LinearPlan plan_linear(int64_t M, int64_t K, int64_t N, int dtype, int out_dtype
     const double flops = 2e-6 * blocks_m * block * blocks_n * 16 * K;
     const double rows = 4.0 + std::max(read / 6.0, flops / (f32 ? 100.0 : 500.0));
     const int64_t fn = (N + 15) / 16;
-    const double columns = even && N <= 128
+    const double columns = even && N <= 128 && M < (int64_t{1} << 28)
                                ? 3.0 + (M + 64 * cus - 1) / (64 * cus) * depth * (f32 ? 0.22 + 0.11 * fn : 0.38) : 1e30;
-    if (blocks_m < 65536 && rows <= columns && rows <= s.us) return {LinearPath::kRows, 0, 0, 1, 0};
+    // (a launch has fewer than 2^32 threads, and 65,535 row blocks)
+    if (blocks_m < 65536 && blocks_n < (int64_t{1} << 22) && rows <= columns && rows <= s.us) return {LinearPath::kRows, 0, 0, 1, 0};
     if (columns <= s.us) return {LinearPath::kColumns, 0, 0, 1, 0};
     return {tile == 256 ? LinearPath::kTile256 : LinearPath::kTile128, s.full, s.rest, s.splits,
             s.splits > 1 ? static_cast<size_t>(s.splits) * s.rest * tile * tile * sizeof(float) : 0};

@@ -300,13 +300,13 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormKernelArgs a) {
 
 template <typename T, typename R, typename Q>
 void launch_q(const NormArgs& a, hipStream_t s) {
-    const NormKernelArgs k{a.x, a.residual, a.weight, a.y, a.scale, a.residual_out, a.rows, a.dim, a.eps};
+    NormKernelArgs k{a.x, a.residual, a.weight, a.y, a.scale, a.residual_out, a.rows, a.dim, a.eps};
     const bool whole = a.dim % VEC == 0;
     // vectors a row covers (others than whole rows: up to VEC - 1 elements earlier)
     const int64_t vectors = (a.dim + (whole ? 0 : VEC - 1) + VEC - 1) / VEC;
     auto run = [&](auto w, auto nv) {
         constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-        const dim3 grid(static_cast<uint32_t>((a.rows + 4 / W - 1) / (4 / W)));
+        const dim3 grid(static_cast<uint32_t>((k.rows + 4 / W - 1) / (4 / W)));
         if (whole)
             norm_kernel<T, R, Q, W, NV, true><<<grid, 256, 0, s>>>(k);
         else
@@ -321,16 +321,30 @@ void launch_q(const NormArgs& a, hipStream_t s) {
     // Four waves a row where rows are few: 4 x 2,560 takes 3.4 us (one wave: 4.1),
     // 2,047 x 1,537 14.4 us (15.5); from 4,096 rows on both take the same.
     const bool few = a.rows < 4096;
-    if (vectors <= 64) run(C1{}, C1{});
-    else if (vectors <= 128 && !few) run(C1{}, C2{});
-    else if (vectors <= 192 && !few) run(C1{}, C3{});
-    else if (vectors <= 320 && !few) run(C1{}, C5{});
-    else if (vectors <= 256) run(C4{}, C1{});
-    else if (vectors <= 512) run(C4{}, C2{});
-    else if (vectors <= 768) run(C4{}, C3{});
-    else if (vectors <= 1024) run(C4{}, C4{});
-    else if (vectors <= 2048) run(C4{}, C8{});
-    else norm_long_kernel<T, R, Q><<<dim3(static_cast<uint32_t>(a.rows)), 256, 0, s>>>(k);
+    auto launch = [&] {
+        if (vectors <= 64) run(C1{}, C1{});
+        else if (vectors <= 128 && !few) run(C1{}, C2{});
+        else if (vectors <= 192 && !few) run(C1{}, C3{});
+        else if (vectors <= 320 && !few) run(C1{}, C5{});
+        else if (vectors <= 256) run(C4{}, C1{});
+        else if (vectors <= 512) run(C4{}, C2{});
+        else if (vectors <= 768) run(C4{}, C3{});
+        else if (vectors <= 1024) run(C4{}, C4{});
+        else if (vectors <= 2048) run(C4{}, C8{});
+        else norm_long_kernel<T, R, Q><<<dim3(static_cast<uint32_t>(k.rows)), 256, 0, s>>>(k);
+    };
+    // a launch has fewer than 2^32 threads: 2^22 rows at a time (whole vectors apart)
+    constexpr int64_t kRows = int64_t{1} << 22;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += kRows) {
+        const int64_t e0 = r0 * a.dim;
+        k.rows = imin64(kRows, a.rows - r0);
+        k.x = static_cast<const T*>(a.x) + e0;
+        k.res = a.residual ? static_cast<const R*>(a.residual) + e0 : nullptr;
+        k.res_out = a.residual_out ? static_cast<R*>(a.residual_out) + e0 : nullptr;
+        k.y = static_cast<Q*>(a.y) + e0;
+        k.scale = a.scale ? a.scale + r0 : nullptr;
+        launch();
+    }
 }
 
 template <typename T, typename R>

@@ -200,3 +200,26 @@ def test_select_and_reorder_in_a_graph(mssm):
         torch.cuda.synchronize()
         assert torch.equal(so, es) and torch.equal(p, ep) and torch.equal(t, et)
         assert torch.equal(state.cpu(), reorder_ref(keep.cpu(), ep.cpu()))
+
+
+def test_more_rows_than_a_grid_dimension_holds(mssm):
+    B, V = 70000, 12
+    x = torch.rand((B, 1, V), device="cuda")
+    s, p, t, _ = mssm.beam_select(x, torch.zeros((B, 1), device="cuda"))
+    assert torch.all(p == 0) and torch.equal(t[:, 0].long(), x[:, 0].argmax(1))
+    want = torch.log_softmax(x.double(), -1).amax(-1)
+    assert torch.all((s.double() - want).abs() <= 2e-5)
+
+
+def test_long_rows_in_several_spans_a_part(mssm):
+    # 32 parts of several spans, and a part whose candidates overflow (many equal logits at the top)
+    check(mssm, *good_seed(1, 3, 300001, "f32"))
+    x, s = torch.zeros((1, 2, 200000)), torch.zeros((1, 2))
+    x[:, :, 70000:140000] = 1.0
+    s[0, 1] = -1.0
+    _, p, t, _ = mssm.beam_select(x.cuda(), s.cuda())
+    assert p.cpu().tolist() == [[0, 0]] and t.cpu().tolist() == [[70000, 70001]]
+    x, s = torch.zeros((64, 8, 20000)), torch.zeros((64, 8))
+    x[:, :, 11111:] = 2.0
+    _, p, t, _ = mssm.beam_select(x.bfloat16().cuda(), s.cuda())
+    assert torch.all(p == 0) and torch.equal(t.cpu(), (11111 + torch.arange(8)).int().expand(64, 8))

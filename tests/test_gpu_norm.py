@@ -136,3 +136,19 @@ def test_other_stream_and_repeats(mssm):
             q2, s2, h2 = mssm.add_rmsnorm_q8(x, w, res)
     st.synchronize()
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2) and torch.equal(h, h2)
+
+
+def test_more_rows_than_a_launch_holds(mssm):
+    rows, dim = (1 << 22) + 5, 9
+    x = torch.randn((rows, dim), device="cuda").bfloat16()
+    w = torch.rand(dim, device="cuda") + 0.5
+    y, h = mssm.add_rmsnorm(x, w, x)
+    q, s, _ = mssm.add_rmsnorm_q8(x, w, x)
+    tail = slice(rows - 9, rows)
+    y2, h2 = mssm.add_rmsnorm(x[tail].clone(), w, x[tail].clone())
+    q2, s2, _ = mssm.add_rmsnorm_q8(x[tail].clone(), w, x[tail].clone())
+    assert torch.equal(y[tail], y2) and torch.equal(h[tail], h2) and torch.equal(s[tail], s2)
+    assert torch.equal(q[tail].view(torch.uint8), q2.view(torch.uint8))
+    full = (2 * x.float()).double()
+    want = full / torch.sqrt((full * full).mean(1, keepdim=True) + 1e-5) * w.double()
+    assert torch.all((y.double() - want).abs() <= want.abs() * (ref.EPSB + 20 * ref.EPS32) + 1e-38)
