@@ -72,8 +72,8 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[VEC]) {
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(a[i]), v[2 * i + 1] = bf16_hi(a[i]);
 }
 // Stores go past the caches: 16,384 x 2,560 bfloat16 rows with a bfloat16
-// residual take 63 us so and 74 us without (float32 residual, 8-bit output: 87
-// and 89 us).
+// residual take 63 us so and 74 us without (float32 residual, 8-bit output, before
+// its remainders were carried: 87 and 89 us).
 __device__ __forceinline__ void store8(float* p, const float (&v)[VEC]) {
     __builtin_nontemporal_store((f32x4{v[0], v[1], v[2], v[3]}), reinterpret_cast<f32x4*>(p));
     __builtin_nontemporal_store((f32x4{v[4], v[5], v[6], v[7]}), reinterpret_cast<f32x4*>(p + 4));
@@ -140,14 +140,86 @@ __device__ __forceinline__ void load_weight(const float* w, int64_t c, int64_t d
     }
 }
 
+// ---- the 8-bit division ----------------------------------------------------------
+//
+// q = e4m3(y / scale) with y = h r w and scale = max |y| / 448: r cancels, and
+// what is rounded to 4 bits is h w (448 / max |h w|).  One rounding of its
+// float32 factors moves about one value in a million across a rounding
+// boundary, by a step of 6 %, so products and quotient are carried as a float32
+// and its remainder (exact sum, fused products) and rounded once, to e4m3: 2 us
+// of 89 at 16,384 x 2,560, where the vector instructions hide behind memory, and up to 2 us of 8 for a thousand rows.
+
+// a + b = s + the returned remainder, exactly
+__device__ __forceinline__ float sum_rest(float a, float b, float s) {
+#pragma clang fp contract(off)
+    const float t = s - a;
+    return (a - (s - t)) + (b - t);
+}
+// (h + rest) w as a float32 and its remainder, in the places of h and rest
+__device__ __forceinline__ void times_weight(float& h, float& rest, float w) {
+#pragma clang fp contract(off)  // what is rounded where is the point here
+    const float p = h * w;
+    rest = __builtin_fmaf(rest, w, __builtin_fmaf(h, w, -p));
+    h = p;
+}
+// The row's largest magnitude so far, as the bits of a float32 (NaN above
+// infinity above every number) and its remainder.
+struct Largest {
+    uint32_t bits = 0;
+    float rest = 0.0f;
+    __device__ __forceinline__ void take(float p, float e) {
+        const uint32_t b = __float_as_uint(p) & 0x7fffffffu;
+        if (b > bits) bits = b, rest = p < 0.0f ? -e : e;
+    }
+    __device__ __forceinline__ void wave() {
+        const uint32_t top = wave_max(bits);
+        // of the lanes that hold it (mostly one) the largest remainder; remainders compare as ordered bits
+        uint32_t o = __float_as_uint(rest);
+        o ^= o >> 31 ? 0xffffffffu : 0x80000000u;
+        o = wave_max(bits == top ? o : 0u);
+        bits = top;
+        rest = __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xffffffffu));
+    }
+};
+// The scale and the factor of the row's h w, in float32 and remainder.
+struct RowScale {
+    float scale, hi, lo;
+    __device__ __forceinline__ RowScale(uint32_t bits, float rest, float r) {
+#pragma clang fp contract(off)
+        const float top = __uint_as_float(bits), y = top * r;
+        if (y < kScaleFloor) {
+            scale = kScaleFloor / kF8Max;
+            hi = r / scale;
+            lo = 0.0f;
+        } else {  // 448 / (top + rest), with what hi leaves of it
+            scale = y / kF8Max;
+            hi = kF8Max / top;
+            lo = __builtin_fmaf(-hi, rest, __builtin_fmaf(-hi, top, kF8Max)) * (hi / kF8Max);
+        }
+    }
+    // (p + e) times the factor, as a float32 that e4m3 rounds as it would the
+    // exact value: where a remainder is left and the last bit is 0 (as it is on
+    // every rounding boundary), one unit towards it.
+    __device__ __forceinline__ float apply(float p, float e) const {
+#pragma clang fp contract(off)
+        const float a = p * hi;
+        const float rest = __builtin_fmaf(p, hi, -a) + __builtin_fmaf(p, lo, e * hi);
+        const float v = a + rest, left = rest - (v - a);
+        const uint32_t b = __float_as_uint(v);
+        const bool away = (__float_as_uint(left) ^ b) >> 31 == 0;
+        return left != 0.0f && (b & 1u) == 0 && b << 1 != 0 ? __uint_as_float(away ? b + 1 : b - 1) : v;
+    }
+};
+
 // W waves a row (4 / W rows a workgroup), NV vectors a lane held in registers,
 // every load of a row under way at once.  Bound by memory: 16,384 x 2,560
-// bfloat16 with a float32 residual into 8 bits moves 461 MB in 87 us, 5.3 TB/s
-// (a device copy: 5.0 to 5.4 TB/s).
+// bfloat16 with a float32 residual into 8 bits moves 461 MB in 89 us, 5.2 TB/s
+// (a device copy: 5.0 to 5.4 TB/s); into bfloat16 with a bfloat16 residual 336 MB
+// in 63 us.
 template <typename T, typename R, typename Q, int W, int NV, bool WHOLE>
 __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
     constexpr bool Q8 = sizeof(Q) == 1;
-    __shared__ float part[2][4];
+    __shared__ float part[3][4];
     const int lane = threadIdx.x & 63, wave = wave_id(), in_row = wave % W;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / W) + wave / W;
     if (W < 4 && row >= a.rows) return;  // a whole wave, and no barrier below
@@ -155,10 +227,16 @@ __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
     const int64_t head = WHOLE ? 0 : e0 & (VEC - 1);
     const T* x = static_cast<const T*>(a.x) + e0;
     const R* res = static_cast<const R*>(a.res) + e0;
-    float h[NV][VEC], w[NV][VEC];
+    float h[NV][VEC], rest[Q8 ? NV : 1][VEC];
     auto column = [&](int i) { return static_cast<int64_t>((i * W + in_row) * 64 + lane) * VEC - head; };
 #pragma unroll
     for (int i = 0; i < NV; ++i) load_part<WHOLE>(x, column(i), a.dim, h[i]);
+    if constexpr (Q8) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) rest[i][j] = 0.0f;
+    }
     if (a.res) {
         float r[NV][VEC];
 #pragma unroll
@@ -166,10 +244,19 @@ __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) h[i][j] += r[i][j];
+            for (int j = 0; j < VEC; ++j) {
+                const float s = h[i][j] + r[i][j];
+                if constexpr (Q8) rest[i][j] = sum_rest(h[i][j], r[i][j], s);
+                h[i][j] = s;
+            }
     }
+    // The 8-bit form holds two registers an element: its weight comes late, from L1
+    // (16,384 x 2,560: 89 us, with the weight held from the start 102 us).
+    float w[Q8 ? 1 : NV][VEC];
+    if constexpr (!Q8) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load_weight<WHOLE>(a.weight, column(i), a.dim, w[i]);
+        for (int i = 0; i < NV; ++i) load_weight<WHOLE>(a.weight, column(i), a.dim, w[i]);
+    }
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -189,39 +276,37 @@ __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) store_part<WHOLE>(static_cast<R*>(a.res_out) + e0, column(i), a.dim, h[i]);
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i][j] = h[i][j] * r * w[i][j];
     if constexpr (Q8) {
-        // magnitudes compared as their bits: NaN above infinity above every number
-        uint32_t m = 0;
+        Largest top;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            asm volatile("" ::: "memory");  // not before this vector's turn
+            load_weight<WHOLE>(a.weight, column(i), a.dim, w[0]);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const uint32_t b = __float_as_uint(h[i][j]) & 0x7fffffffu;
-                m = b > m ? b : m;
-            }
-        m = wave_max(m);
-        if constexpr (W == 4) {
-            if (lane == 0) part[1][wave] = __uint_as_float(m);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t o = __float_as_uint(part[1][i]);
-                m = o > m ? o : m;
+                times_weight(h[i][j], rest[i][j], w[0][j]);
+                top.take(h[i][j], rest[i][j]);
             }
         }
-        // a NaN among the elements outside the row is none: they are 0 * r * 0, and r
-        // is a number unless the row holds a NaN or an infinity
-        const float top = __uint_as_float(m), scale = (top < kScaleFloor ? kScaleFloor : top) / kF8Max;
-        const float inv = 1.0f / scale;
-        if (lane == 0 && in_row == 0) a.scale[row] = scale;
+        top.wave();
+        if constexpr (W == 4) {
+            if (lane == 0) part[1][wave] = __uint_as_float(top.bits), part[2][wave] = top.rest;
+            __syncthreads();
+            top = Largest{};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top.take(part[1][i], part[2][i]);
+        }
+        const RowScale q(top.bits, top.rest, r);
+        if (lane == 0 && in_row == 0) a.scale[row] = q.scale;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) h[i][j] *= inv;
+            for (int j = 0; j < VEC; ++j) h[i][j] = q.apply(h[i][j], rest[i][j]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) h[i][j] = h[i][j] * r * w[i][j];
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) store_part<WHOLE>(static_cast<Q*>(a.y) + e0, column(i), a.dim, h[i]);
@@ -232,27 +317,31 @@ __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
 template <typename T, typename R, typename Q>
 __global__ __launch_bounds__(256) void norm_long_kernel(NormKernelArgs a) {
     constexpr bool Q8 = sizeof(Q) == 1;
-    __shared__ float part[2][4];
+    __shared__ float part[3][4];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t row = blockIdx.x, e0 = row * a.dim;
     const T* x = static_cast<const T*>(a.x) + e0;
     const R* res = a.res ? static_cast<const R*>(a.res) + e0 : nullptr;
     const int64_t head = e0 & (VEC - 1);
-    auto each = [&](auto f) {
+    auto each = [&](auto f) {  // f(column, h, the remainders of its sums)
         for (int64_t c = static_cast<int64_t>(threadIdx.x) * VEC - head; c < a.dim; c += 256 * VEC) {
-            float h[VEC];
+            float h[VEC], rest[VEC] = {};
             load_part<false>(x, c, a.dim, h);
             if (res) {
                 float r[VEC];
                 load_part<false>(res, c, a.dim, r);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) h[j] += r[j];
+                for (int j = 0; j < VEC; ++j) {
+                    const float s = h[j] + r[j];
+                    rest[j] = sum_rest(h[j], r[j], s);
+                    h[j] = s;
+                }
             }
-            f(c, h);
+            f(c, h, rest);
         }
     };
     float ss = 0.0f;
-    each([&](int64_t, float (&h)[VEC]) {
+    each([&](int64_t, float (&h)[VEC], float (&)[VEC]) {
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) s = __builtin_fmaf(h[j], h[j], s);
@@ -263,37 +352,40 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormKernelArgs a) {
     __syncthreads();
     ss = (part[0][0] + part[0][1]) + (part[0][2] + part[0][3]);
     const float r = 1.0f / __builtin_sqrtf(ss / static_cast<float>(a.dim) + a.eps);
-    float inv = 1.0f;
+    Largest top;
     if constexpr (Q8) {
-        uint32_t m = 0;
-        each([&](int64_t c, float (&h)[VEC]) {
+        each([&](int64_t c, float (&h)[VEC], float (&rest)[VEC]) {
             float w[VEC];
             load_weight<false>(a.weight, c, a.dim, w);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const uint32_t b = __float_as_uint(h[j] * r * w[j]) & 0x7fffffffu;
-                m = b > m ? b : m;
+                times_weight(h[j], rest[j], w[j]);
+                top.take(h[j], rest[j]);
             }
         });
-        m = wave_max(m);
-        if (lane == 0) part[1][wave] = __uint_as_float(m);
+        top.wave();
+        if (lane == 0) part[1][wave] = __uint_as_float(top.bits), part[2][wave] = top.rest;
         __syncthreads();
+        top = Largest{};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t o = __float_as_uint(part[1][i]);
-            m = o > m ? o : m;
-        }
-        const float top = __uint_as_float(m), scale = (top < kScaleFloor ? kScaleFloor : top) / kF8Max;
-        inv = 1.0f / scale;
-        if (threadIdx.x == 0) a.scale[row] = scale;
+        for (int i = 0; i < 4; ++i) top.take(part[1][i], part[2][i]);
     }
+    const RowScale q(top.bits, top.rest, r);
+    if (Q8 && threadIdx.x == 0) a.scale[row] = q.scale;
     // each thread writes the places it has read, after its last read of them
-    each([&](int64_t c, float (&h)[VEC]) {
+    each([&](int64_t c, float (&h)[VEC], float (&rest)[VEC]) {
         float w[VEC];
         load_weight<false>(a.weight, c, a.dim, w);
         if (a.res_out) store_part<false>(static_cast<R*>(a.res_out) + e0, c, a.dim, h);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = Q8 ? h[j] * r * w[j] * inv : h[j] * r * w[j];
+        for (int j = 0; j < VEC; ++j) {
+            if constexpr (Q8) {
+                times_weight(h[j], rest[j], w[j]);
+                h[j] = q.apply(h[j], rest[j]);
+            } else {
+                h[j] = h[j] * r * w[j];
+            }
+        }
         store_part<false>(static_cast<Q*>(a.y) + e0, c, a.dim, h);
     });
 }
@@ -325,6 +417,7 @@ void launch_q(const NormArgs& a, hipStream_t s) {
         if (vectors <= 64) run(C1{}, C1{});
         else if (vectors <= 128 && !few) run(C1{}, C2{});
         else if (vectors <= 192 && !few) run(C1{}, C3{});
+        else if (vectors <= 256 && !few) run(C1{}, C4{});
         else if (vectors <= 320 && !few) run(C1{}, C5{});
         else if (vectors <= 256) run(C4{}, C1{});
         else if (vectors <= 512) run(C4{}, C2{});

@@ -152,3 +152,19 @@ def test_more_rows_than_a_launch_holds(mssm):
     full = (2 * x.float()).double()
     want = full / torch.sqrt((full * full).mean(1, keepdim=True) + 1e-5) * w.double()
     assert torch.all((y.double() - want).abs() <= want.abs() * (ref.EPSB + 20 * ref.EPS32) + 1e-38)
+
+
+@pytest.mark.parametrize("dim", [2560, 1537, 20001])
+@pytest.mark.parametrize("dtype,residual", [("bf16", "f32"), ("f32", "bf16"), ("bf16", None)])
+def test_eight_bit_values_are_the_nearest(mssm, dim, dtype, residual):
+    # h w (448 / max |h w|) is rounded once: every value is the e4m3 nearest to the exact one (r cancels), but
+    # for those within the carried product's error, 2^-40 relative, of a rounding boundary
+    x, res, w = inputs(4000 if dim < 10000 else 100, dim, dtype, residual, seed=3)
+    q, _, _ = mssm.add_rmsnorm_q8(x, w, res)
+    t = (np64(x) + (0 if res is None else np64(res))) * np64(w)
+    v = t * (448.0 / np.abs(t).max(1, keepdims=True))
+    step = ref.f8_step(v)
+    q = np64(q.float())
+    assert np.all(np.abs(q - v) <= 0.5 * step + np.abs(v) * 2.0 ** -40)
+    sure = np.abs(np.abs(np.fmod(v / step, 1.0)) - 0.5) * step > np.abs(v) * 2.0 ** -40
+    assert np.array_equal(q[sure], (np.round(v / step) * step)[sure])
