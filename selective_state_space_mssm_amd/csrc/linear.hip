@@ -503,15 +503,17 @@ __device__ __forceinline__ void store_four(const LinearKernelArgs& a, int64_t m,
     }
 }
 
+constexpr int kRowWaves = 8;
+
 // Few outputs: 16 MF rows by 16 columns a workgroup, both operands straight from
 // memory into registers as matrix operands.  The 8 waves take the 128-byte
 // steps of k in turn, U of them in flight each, and add their sums through LDS
 // in the order of the waves: one launch, and every wave of a decode step's
 // product has its part of the weight under way at once.  1 x 2,560 x 10,240
-// bfloat16 takes 13 us (4.0 TB/s), by split tiles and a second pass 20 us.
-template <int DT, typename O, int MF, bool EVEN>
+// bfloat16 takes 12 us (4.4 TB/s), by split tiles and a second pass 20 us.
+template <int DT, typename O, int MF, bool EVEN, int U>
 __global__ __launch_bounds__(512) void linear_rows_kernel(LinearKernelArgs a) {
-    constexpr int WAVES = 8, U = MF == 1 ? 4 : 2;
+    constexpr int WAVES = kRowWaves;
     __shared__ __align__(16) f32x4 part[WAVES][MF][64];
     const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
@@ -702,10 +704,24 @@ void launch_tiles(const LinearKernelArgs& k, const LinearPlan& p, hipStream_t s)
 template <int DT, typename O, int MF>
 void launch_rows(const LinearKernelArgs& k, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>((k.N + 15) / 16), static_cast<uint32_t>((k.M + 16 * MF - 1) / (16 * MF)));
-    if (k.K * Elem<DT>::kBytes % 16 == 0)
-        linear_rows_kernel<DT, O, MF, true><<<grid, 512, 0, s>>>(k);
-    else
-        linear_rows_kernel<DT, O, MF, false><<<grid, 512, 0, s>>>(k);
+    const int64_t kbytes = k.K * Elem<DT>::kBytes;
+    if (kbytes % 16 != 0) {
+        linear_rows_kernel<DT, O, MF, false, MF == 1 ? 4 : 2><<<grid, 512, 0, s>>>(k);
+    } else if constexpr (MF > 1) {  // more steps in flight: no gain, or up to a third slower by their registers
+        linear_rows_kernel<DT, O, MF, true, 2><<<grid, 512, 0, s>>>(k);
+    } else {
+        // A wave's steps in the fewest turns of at most 5, evenly: 5 steps in one
+        // turn of 5 take 12.0 us where turns of 4 take 13.9; 3 steps in one of 3
+        // 7.3 us, of 4 8.0 us, of 5 8.7 us.
+        const int64_t steps = (kbytes + kTileBytes * kRowWaves - 1) / (kTileBytes * kRowWaves), turns = (steps + 4) / 5;
+        switch ((steps + turns - 1) / turns) {
+            case 1: linear_rows_kernel<DT, O, MF, true, 1><<<grid, 512, 0, s>>>(k); break;
+            case 2: linear_rows_kernel<DT, O, MF, true, 2><<<grid, 512, 0, s>>>(k); break;
+            case 3: linear_rows_kernel<DT, O, MF, true, 3><<<grid, 512, 0, s>>>(k); break;
+            case 4: linear_rows_kernel<DT, O, MF, true, 4><<<grid, 512, 0, s>>>(k); break;
+            default: linear_rows_kernel<DT, O, MF, true, 5><<<grid, 512, 0, s>>>(k); break;
+        }
+    }
 }
 
 template <int DT, typename O, int FN>

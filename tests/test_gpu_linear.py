@@ -200,3 +200,11 @@ def test_eight_bit_sums_keep_float32_accuracy(mssm):
         y = mssm.linear(x.cuda(), w.cuda(), x_scale=one(M), w_scale=one(N), out_dtype=torch.float32)
         want = np64(x) @ np64(w).T
         assert np.linalg.norm(np64(y) - want) <= 1e-6 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("dtype,out", PAIRS)
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7, 11])
+def test_few_rows_any_number_of_steps_a_wave(mssm, steps, dtype, out):
+    size = {"f32": 4, "bf16": 2, "f8": 1}[dtype]
+    for k in (1024 * steps, 1024 * steps - 112):  # bytes: all 8 waves' steps full, and the last cut short
+        run_exact(mssm, 3, k // size, 40, dtype, out)
