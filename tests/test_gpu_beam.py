@@ -223,3 +223,15 @@ def test_long_rows_in_several_spans_a_part(mssm):
     x[:, :, 11111:] = 2.0
     _, p, t, _ = mssm.beam_select(x.bfloat16().cuda(), s.cuda())
     assert torch.all(p == 0) and torch.equal(t.cpu(), (11111 + torch.arange(8)).int().expand(64, 8))
+
+
+@pytest.mark.parametrize("K", [3, 8, 16])
+def test_reorder_states_beyond_the_caches(mssm, K):
+    g = torch.Generator().manual_seed(K)
+    parent = torch.randint(0, K, (2, K), generator=g).int().cuda()
+    rows = (torch.arange(2, device="cuda")[:, None] * K + parent).view(-1)
+    t = torch.randint(0, 2 ** 31, (8, 2 * K, (300 << 20) // (64 * K) // 4 * 4), dtype=torch.int32, device="cuda")
+    odd = torch.randn((2, 2 * K, 77), device="cuda").bfloat16()
+    want, want_odd = t[:, rows], odd[:, rows]
+    mssm.beam_reorder(parent, [t, odd])
+    assert torch.equal(t, want) and torch.equal(odd, want_odd)
