@@ -128,9 +128,12 @@ __device__ __forceinline__ uint64_t best_of(uint64_t (&held)[S], int n, int K, i
             const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(held[0]), j);
             rank += ((static_cast<uint64_t>(hi) << 32) | lo) > held[0] ? 1 : 0;
         }
+        wave_handoff();  // sorted may be where held came from
         if (lane < K) sorted[lane] = 0;
+        wave_handoff();
         if (held[0] && rank < K) sorted[rank] = held[0];
-        return lane < K ? sorted[lane] : 0;  // one wave: its LDS operations are in order
+        wave_handoff();
+        return lane < K ? sorted[lane] : 0;
     }
     uint64_t mine = 0;
     for (int k = 0; k < K; ++k) {
@@ -162,6 +165,7 @@ __device__ __forceinline__ int pick_in_passes(const T* x, int64_t v0, int64_t hi
         if (lane == 0) hits[k] = last;
         if (last == 0) last = 1;  // none left: only zeros follow
     }
+    wave_handoff();
     return K;
 }
 
@@ -242,12 +246,14 @@ __global__ __launch_bounds__(kThreads) void beam_part_kernel(const void* logits,
                 }
             }
         }
+        wave_handoff();
         if (n > kHits || !(floor > -kInf)) n = before + pick_in_passes<T, At>(x, v0, hi, K, hits + before, lane);
         if (n > 64) {  // make room for the next span's
             uint64_t held[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) held[i] = i * 64 + lane < n ? hits[i * 64 + lane] : 0;
             const uint64_t kept = best_of(held, n, K, lane, sorted[wave]);
+            wave_handoff();
             if (lane < K) hits[lane] = kept;
             n = K;
         }
@@ -276,6 +282,7 @@ __global__ __launch_bounds__(kThreads) void beam_part_kernel(const void* logits,
         if (lane < c) all[total + lane] = key;
         total += c;
     }
+    wave_handoff();
     uint64_t held[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) held[i] = i * 64 + lane < total ? all[i * 64 + lane] : 0;

@@ -271,6 +271,15 @@ __device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_
 // silu(z) = z * sigmoid(z)
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 
+// Between stores to LDS and loads of them by other lanes of the same wave (and
+// before the places are written again).  The hardware runs a wave's LDS
+// operations in order; this binds the compiler to the order, and emits nothing.
+__device__ __forceinline__ void wave_handoff() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __host__ __device__ __forceinline__ int64_t imin64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // ---- wave helpers ----------------------------------------------------------
