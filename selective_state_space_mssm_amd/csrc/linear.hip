@@ -443,10 +443,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(LinearKern
     uint8_t* mine = lds + wave * 16384;
     const int64_t mw = m0 + wm * (BM / WM), nw = n0 + wn * 64;
     auto stage = [&](int h) {
+        wave_handoff();  // the block before has been read
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) out.stage(mine, i * 16 + r, j * 4 + g, acc[h * 4 + i][j]);
+        wave_handoff();
     };
     if (split) {
         float* sums = a.partial + ((part * a.rest + t_id - whole) * BM + wm * (BM / WM)) * BN + wn * 64;

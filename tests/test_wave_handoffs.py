@@ -52,3 +52,12 @@ def test_the_fence_binds_compiler_and_wave():
 ])
 def test_beam_candidates(function, first, then):
     assert fenced(body(source("beam.hip"), function), first, then)
+
+
+def test_linear_output_blocks():
+    kernel = body(source("linear.hip"), r"void linear_tile_kernel\(")
+    stage = body(kernel, r"auto stage =")
+    assert re.search(rf"^{{\s*{FENCE}", stage), "the block before may still be read"
+    assert re.search(rf"{FENCE}\s*}}$", stage), "other lanes read the block next"
+    # nothing else writes or reads the blocks: stored by stage(), read by the calls behind it
+    assert len(re.findall(r"out\.stage\(", kernel)) == len(re.findall(r"out\.stage\(", stage)) == 1
