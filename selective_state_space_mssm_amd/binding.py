@@ -169,6 +169,10 @@ def _workspace(nbytes: int, device, workspace=None):
     if nbytes == 0:
         return None
     if workspace is not None:
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError(f"workspace has {workspace.numel() * workspace.element_size()} bytes, needs {nbytes}")
         return workspace
