@@ -8,9 +8,9 @@
 namespace mssm {
 namespace {
 
-// A float32 as an unsigned number of the same order (no NaN).
+// A float32 as an unsigned number of the same order (no NaN; -0 is +0: the two are equal).
 __device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t b = __float_as_uint(v);
+    const uint32_t b = __float_as_uint(v + 0.0f);
     return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float from_ordered(uint32_t u) {
