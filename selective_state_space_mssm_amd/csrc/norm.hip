@@ -187,9 +187,9 @@ struct RowScale {
     __device__ __forceinline__ RowScale(uint32_t bits, float rest, float r) {
 #pragma clang fp contract(off)
         const float top = __uint_as_float(bits), y = top * r;
-        if (y < kScaleFloor) {
+        if (bits == 0 || y < kScaleFloor) {
             scale = kScaleFloor / kF8Max;
-            hi = r / scale;
+            hi = bits ? r / scale : 0.0f;  // a row of zeros: r is infinite with eps = 0
             lo = 0.0f;
         } else {  // 448 / (top + rest), with what hi leaves of it
             scale = y / kF8Max;
