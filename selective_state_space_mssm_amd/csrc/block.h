@@ -8,6 +8,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "linear_plan.h"
 #include "mssm_block.h"
 
 namespace mssm {
@@ -37,15 +38,6 @@ struct LinearArgs {
     void* y;
     float* partial;        // split sums (splits, M, N), null: none
 };
-// How one product is computed and cut; the same rule sizes the workspace and launches.
-enum class LinearPath { kRows, kColumns, kTile128, kTile256 };
-struct LinearPlan {
-    LinearPath path;
-    int64_t full, rest;  // tiles computed whole, and tiles cut along in_dim
-    int splits;          // parts of each of the latter, 1: none and no second pass
-    size_t ws_bytes;
-};
-LinearPlan plan_linear(int64_t M, int64_t K, int64_t N, int dtype, int out_dtype, int64_t cus);
 hipError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, hipStream_t s);
 
 struct BeamArgs {
