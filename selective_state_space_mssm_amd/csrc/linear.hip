@@ -359,7 +359,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(LinearKern
     __shared__ __align__(1024) uint8_t lds[2 * STAGE];
     // The hardware deals workgroups to the 8 XCDs in turn: each XCD gets one
     // contiguous range of the whole tiles (full is a multiple of 8, or all).
-    const int64_t id = blockIdx.x, whole = a.full;
+    const int64_t id = blockIdx.x + static_cast<int64_t>(blockIdx.y) * gridDim.x, whole = a.full;
+    if (id >= whole + a.rest * a.splits) return;  // the grid's last row
     const bool split = id >= whole;
     const int64_t t_id = split ? whole + (id - whole) % a.rest
                                : (id & 7) * (whole >> 3) + ((id & 7) < (whole & 7) ? (id & 7) : (whole & 7)) + (id >> 3);
@@ -698,8 +699,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearKernelArgs a) {
 
 template <int DT, typename O, int B, int WM, int WN, bool EVEN>
 void launch_tiles(const LinearKernelArgs& k, const LinearPlan& p, hipStream_t s) {
-    const uint32_t groups = static_cast<uint32_t>(p.full + p.rest * p.splits);
-    linear_tile_kernel<DT, O, B, B, WM, WN, EVEN><<<dim3(groups), 64 * WM * WN, 0, s>>>(k);
+    const LinearGrid g = linear_grid(p.full + p.rest * p.splits);
+    linear_tile_kernel<DT, O, B, B, WM, WN, EVEN><<<dim3(g.x, g.y), 64 * WM * WN, 0, s>>>(k);
     if (p.splits > 1) linear_join_kernel<DT, O, B, B><<<dim3(static_cast<uint32_t>(p.rest * (B / 16))), 256, 0, s>>>(k);
 }
 

@@ -22,6 +22,15 @@ struct LinearPlan {
     size_t ws_bytes;
 };
 
+// The tile kernel's grid: a launch has fewer than 2^32 threads in a dimension,
+// so 2^22 workgroups go in a row; number x + y * grid.x, those behind the last do
+// nothing.
+struct LinearGrid { uint32_t x, y; };
+inline LinearGrid linear_grid(int64_t groups) {
+    const int64_t x = std::min<int64_t>(groups, int64_t{1} << 22);
+    return {static_cast<uint32_t>(x), static_cast<uint32_t>((groups + x - 1) / x)};
+}
+
 // Time of T tiles (us): a round of all the slots takes `depth` k steps of
 // `step` us and `ends` us around them; a last round of few tiles is cut along k
 // into `splits` when that saves more than a second pass (5 us) and the partial

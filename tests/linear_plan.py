@@ -18,6 +18,10 @@ extern "C" void plan(int64_t M, int64_t K, int64_t N, int dtype, int out, int64_
     const mssm::LinearPlan p = mssm::plan_linear(M, K, N, dtype, out, cus);
     r[0] = static_cast<int64_t>(p.path); r[1] = p.full; r[2] = p.rest; r[3] = p.splits; r[4] = static_cast<int64_t>(p.ws_bytes);
 }
+extern "C" void grid(int64_t groups, int64_t* r) {
+    const mssm::LinearGrid g = mssm::linear_grid(groups);
+    r[0] = g.x; r[1] = g.y;
+}
 """
 
 
@@ -31,7 +35,8 @@ def _lib():
                         "-I", CSRC, src, "-o", so], check=True)
         lib = ctypes.CDLL(so)
     lib.plan.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 2 + [ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
-    lib.plan.restype = None
+    lib.grid.argtypes = [ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
+    lib.plan.restype = lib.grid.restype = None
     return lib
 
 
@@ -40,3 +45,10 @@ def plan(M, K, N, dtype, out, cus=256):
     r = (ctypes.c_int64 * 5)()
     _lib().plan(M, K, N, DTYPES[dtype], DTYPES[out], cus, r)
     return (PATHS[r[0]], *r[1:])
+
+
+def grid(groups):
+    """(x, y) of the tile kernel's grid for so many workgroups"""
+    r = (ctypes.c_int64 * 2)()
+    _lib().grid(groups, r)
+    return r[0], r[1]

@@ -47,3 +47,13 @@ def test_plans_are_whole(dtype, out):
     if (dtype, out) == ("f8", "f32"):
         want -= {("tile256", False), ("tile256", True)}
     assert seen == want
+
+
+def test_tile_grids_stay_within_a_launch():
+    # up to 512 threads a workgroup, fewer than 2^32 threads in a dimension, 65,535 rows
+    largest = linear_plan.plan(2 ** 31 - 1, 1, 1, "bf16", "bf16")[1]
+    assert largest * 256 >= 2 ** 32  # one row of workgroups would not do
+    for n in (1, 2, 255, 256, 2 ** 22 - 1, 2 ** 22, 2 ** 22 + 1, 3 * 2 ** 22, largest, 2 ** 31):
+        x, y = linear_plan.grid(n)
+        assert x * 512 < 2 ** 32 and y < 65536 and n <= x * y < n + x
+        assert y == 1 or n > 2 ** 22
