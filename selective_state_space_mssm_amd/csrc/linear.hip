@@ -66,10 +66,22 @@ struct LinearKernelArgs {
     float* partial;
 };
 
-template <int ACT>
+// v / (1 + exp(-v)) to float32's accuracy: exp2 of the rounded -|v| log2 e alone
+// is off by up to |v| 2^-24, so the remainder of that product is carried.  exp of
+// the negative magnitude does not overflow, and is 0 from -104 on (an infinite
+// remainder otherwise).
+__device__ __forceinline__ float silu_whole(float v) {
+    constexpr float kLog2eRest = 1.925963033500012e-08f;  // log2 e = kLog2e + this
+    const float a = __builtin_fmaxf(-__builtin_fabsf(v), -104.0f), t = a * kLog2e;
+    const float e0 = fast_exp2(t), e = __builtin_fmaf(e0, kLn2 * __builtin_fmaf(a, kLog2eRest, __builtin_fmaf(a, kLog2e, -t)), e0);
+    return (v < 0.0f ? v * e : v) * fast_rcp(1.0f + e);
+}
+
+// A bfloat16 output (2^-8) does not show the short form's error.
+template <int ACT, typename O>
 __device__ __forceinline__ float activate(float v) {
     if constexpr (ACT == MSSM_ACT_RELU) return v > 0.0f || v != v ? v : 0.0f;  // NaN stays
-    if constexpr (ACT == MSSM_ACT_SILU) return silu(v);
+    if constexpr (ACT == MSSM_ACT_SILU) return sizeof(O) == 4 ? silu_whole(v) : silu(v);
     if constexpr (ACT == MSSM_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     return v;
 }
@@ -162,7 +174,7 @@ struct BlockOut {
                 for (int c = 0; c < 4; ++c) {
                     float u = v[c];
                     if constexpr (DT == MSSM_F8) u *= xs[q] * ws[c4 * 4 + c];
-                    u = activate<ACT>(u + bias[c4 * 4 + c]);
+                    u = activate<ACT, O>(u + bias[c4 * 4 + c]);
                     if (a.res) u += OutVec<O>::get(res[q], c4 * 4 + c);
                     OutVec<O>::set(out, c4 * 4 + c, u);
                 }
@@ -191,7 +203,7 @@ struct BlockOut {
                 const int row = r0 + i;
                 float u = *reinterpret_cast<const float*>(lds + row * 256 + (((lane >> 2) ^ (row & 15)) * 16) + (lane & 3) * 4);
                 if constexpr (DT == MSSM_F8) u *= xs[i];
-                u = activate<ACT>(u + bias) + add[i];
+                u = activate<ACT, O>(u + bias) + add[i];
                 if (m0 + row < a.M) store_act(static_cast<O*>(a.y), (m0 + row) * a.N + n, u);
             }
         }
@@ -484,7 +496,7 @@ __device__ __forceinline__ void store_four(const LinearKernelArgs& a, int64_t m,
     for (int c = 0; c < 4; ++c) {
         const int64_t nc = imin64(n + c, a.N - 1);
         if constexpr (DT == MSSM_F8) v[c] *= xs * a.ws[nc];
-        v[c] = activate<ACT>(v[c] + (a.bias ? a.bias[nc] : 0.0f));
+        v[c] = activate<ACT, O>(v[c] + (a.bias ? a.bias[nc] : 0.0f));
     }
     if (a.N % 4 == 0) {
         if constexpr (sizeof(O) == 4) {
@@ -675,7 +687,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearKernelArgs a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 if constexpr (DT == MSSM_F8) v[c] *= xs * ws[c];
-                v[c] = activate<act>(v[c] + bias[c]);
+                v[c] = activate<act, O>(v[c] + bias[c]);
             }
             if (whole) {
                 if constexpr (sizeof(O) == 4) {
