@@ -178,7 +178,10 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     float32, one scale a row.  bias (N) float32; activation None, "relu",
     "silu" or "gelu" (by erf); residual (..., N) in the output's type.
     out_dtype: float32, or bfloat16 (not with float32 operands); x's type by
-    default, bfloat16 with 8-bit operands.  y may be residual."""
+    default, bfloat16 with 8-bit operands.  8-bit operands with a bfloat16
+    output are summed by the 8-bit matrix instructions, within 2^-10 sum |x w|
+    (typically 1.5e-5 of the sum); out_dtype=float32 sums them in float32 at
+    half the rate, for sums that cancel.  y may be residual."""
     if x is None or w is None or x.dim() < 1 or w.dim() != 2:
         raise ValueError("x must be (..., K) and w (N, K)")
     act = x.dtype
