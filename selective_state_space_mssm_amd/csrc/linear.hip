@@ -66,6 +66,10 @@ struct LinearKernelArgs {
     float* partial;
 };
 
+// A sum of 8-bit products with its row's and its column's scale, one after the
+// other: the scales' own product may be out of range.
+__device__ __forceinline__ float scaled(float sum, float xs, float ws) { return sum * xs * ws; }
+
 // v / (1 + exp(-v)) to float32's accuracy: exp2 of the rounded -|v| log2 e alone
 // is off by up to |v| 2^-24, so the remainder of that product is carried.  exp of
 // the negative magnitude does not overflow, and is 0 from -104 on (an infinite
@@ -173,7 +177,7 @@ struct BlockOut {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float u = v[c];
-                    if constexpr (DT == MSSM_F8) u *= xs[q] * ws[c4 * 4 + c];
+                    if constexpr (DT == MSSM_F8) u = scaled(u, xs[q], ws[c4 * 4 + c]);
                     u = activate<ACT, O>(u + bias[c4 * 4 + c]);
                     if (a.res) u += OutVec<O>::get(res[q], c4 * 4 + c);
                     OutVec<O>::set(out, c4 * 4 + c, u);
@@ -195,14 +199,14 @@ struct BlockOut {
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int64_t m = imin64(m0 + r0 + i, a.M - 1);
-                xs[i] = DT == MSSM_F8 ? a.xs[m] * ws : 1.0f;
+                xs[i] = DT == MSSM_F8 ? a.xs[m] : 1.0f;
                 add[i] = a.res ? load_act(static_cast<const O*>(a.res), m * a.N + n) : 0.0f;
             }
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int row = r0 + i;
                 float u = *reinterpret_cast<const float*>(lds + row * 256 + (((lane >> 2) ^ (row & 15)) * 16) + (lane & 3) * 4);
-                if constexpr (DT == MSSM_F8) u *= xs[i];
+                if constexpr (DT == MSSM_F8) u = scaled(u, xs[i], ws);
                 u = activate<ACT, O>(u + bias) + add[i];
                 if (m0 + row < a.M) store_act(static_cast<O*>(a.y), (m0 + row) * a.N + n, u);
             }
@@ -499,7 +503,7 @@ __device__ __forceinline__ void store_four(const LinearKernelArgs& a, int64_t m,
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int64_t nc = imin64(n + c, a.N - 1);
-        if constexpr (DT == MSSM_F8) v[c] *= xs * a.ws[nc];
+        if constexpr (DT == MSSM_F8) v[c] = scaled(v[c], xs, a.ws[nc]);
         v[c] = activate<ACT, O>(v[c] + (a.bias ? a.bias[nc] : 0.0f));
     }
     if (a.N % 4 == 0) {
@@ -690,7 +694,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearKernelArgs a) {
             const O* res = a.res ? static_cast<const O*>(a.res) + o : nullptr;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                if constexpr (DT == MSSM_F8) v[c] *= xs * ws[c];
+                if constexpr (DT == MSSM_F8) v[c] = scaled(v[c], xs, ws[c]);
                 v[c] = activate<act, O>(v[c] + bias[c]);
             }
             if (whole) {
