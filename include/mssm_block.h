@@ -39,7 +39,10 @@ extern "C" {
  *   x, y                    (rows, dim) in p->dtype (MSSM_F32 or MSSM_BF16)
  *   residual, residual_out  (rows, dim) in p->residual_dtype (either type)
  *   weight                  (dim) float32
- * The norm is taken of the float32 sum, not of its rounded copy.  Required: x,
+ * The norm is taken of the float32 sum, not of its rounded copy, and the squares
+ * are float32: a row with |h| beyond about 1e19 gives 0, and with eps = 0 a row
+ * of magnitudes below 1e-19 is not normalised (a row of zeros is 0 / 0, NaN);
+ * 8-bit rows take h * weight within float32's range as well.  Required: x,
  * weight, y.  Optional (NULL): residual; residual_out -> not written.
  * residual_out may be the residual's own buffer, and y may be x's.
  */
@@ -60,7 +63,7 @@ mssm_status mssm_add_rmsnorm(const mssm_norm_problem* p, const void* x, const vo
  *     scale[row] = max(max |y|, 1e-30) / 448,   q = e4m3(y / scale[row])
  *
  *   q (rows, dim) bytes, scale (rows) float32, both required.
- * A row of zeros gives q = 0 and the scale 1e-30 / 448.  A row that holds a NaN
+ * A row of zeros gives q = 0 and the scale 1e-30 / 448, with eps = 0 too.  A row that holds a NaN
  * or an infinity gives NaN in all of q and in its scale.
  */
 mssm_status mssm_add_rmsnorm_q8(const mssm_norm_problem* p, const void* x, const void* residual,

@@ -1,6 +1,8 @@
 """ctypes binding of the operators around the scan (C ABI in include/mssm_block.h).
 
-As binding.py: argument marshalling only, on torch's current HIP stream.  A
+As binding.py: argument marshalling only, on torch's current HIP stream.  These
+are operators of serving: they have no backward, and what they return from
+tensors that require gradients does not.  A
 decode step makes these calls once a layer, with kernels of a few microseconds,
 so the marshalling is kept short: problem descriptors and workspace sizes are
 remembered by the sizes they follow from.
@@ -140,7 +142,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None):
     float32 or bfloat16, residual as x in either type, weight (D) float32.
     Returns (y, residual_out): y in x's type, residual_out = h in the
     residual's (None without a residual, unless given).  residual_out may be
-    residual and y may be x."""
+    residual and y may be x.  Forward only: no gradient is recorded."""
     prob, residual_out = _norm_args(x, weight, residual, residual_out, eps)
     if y is None:
         y = torch.empty_like(x)
@@ -155,7 +157,7 @@ def add_rmsnorm_q8(x, weight, residual=None, eps=1e-5, q=None, scale=None, resid
     """add_rmsnorm with y in 8 bits: q (..., D) float8_e4m3fn and scale (...)
     float32 with y ~ q * scale, scale = max(max|y|, 1e-30) / 448 of each row.
     Returns (q, scale, residual_out); linear() takes q and scale as x and
-    x_scale."""
+    x_scale.  Forward only: no gradient is recorded."""
     prob, residual_out = _norm_args(x, weight, residual, residual_out, eps)
     if q is None:
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
@@ -181,7 +183,8 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     default, bfloat16 with 8-bit operands.  8-bit operands with a bfloat16
     output are summed by the 8-bit matrix instructions, within 2^-10 sum |x w|
     (typically 1.5e-5 of the sum); out_dtype=float32 sums them in float32 at
-    half the rate, for sums that cancel.  y may be residual."""
+    half the rate, for sums that cancel.  y may be residual.  Forward only:
+    no gradient is recorded."""
     if x is None or w is None or x.dim() < 1 or w.dim() != 2:
         raise ValueError("x must be (..., K) and w (N, K)")
     act = x.dtype
@@ -224,7 +227,8 @@ def beam_select(logits, scores, finished=None, end_token=None, scores_out=None, 
     end_token.  Of the K * V continuations scores + log_softmax(logits) of
     every batch row the K best, in descending order, ties to the lowest
     k * V + v.  Returns (scores_out, parent, token, finished_out): parent and
-    token (B, K) int32; finished_out (B, K) bool, None without an end_token."""
+    token (B, K) int32; finished_out (B, K) bool, None without an end_token.
+    Forward only: no gradient is recorded."""
     if logits is None or logits.dim() != 3:
         raise ValueError("logits must be (B, K, V)")
     B, K, V = logits.shape
@@ -267,7 +271,8 @@ def beam_reorder(parent, states):
     """The beams' states follow their parents, in place: for every tensor of
     states, (layers, B * K, ...) of any type, t[l, b * K + k] becomes
     t[l, b * K + parent[b, k]].  parent (B, K) int32, as beam_select returns
-    it.  One state (B * K, ...) goes as state[None].  Returns states."""
+    it.  One state (B * K, ...) goes as state[None].  Returns states.  Forward
+    only: no gradient is recorded."""
     if parent is None or parent.dim() != 2:
         raise ValueError("parent must be (B, K)")
     B, K = parent.shape
