@@ -73,9 +73,11 @@ __device__ __forceinline__ float clean_score(float v) { return v < kInf ? v : -k
 // tokens are known before the softmax sum is, and one pass over the logits
 // gives both: each workgroup leaves its part's K best (logit, token) and its
 // part's maximum and sum.  Every float32 sum is formed in a fixed order.
-// 512 x 50,280 bfloat16 take 24.5 us (2.1 TB/s): about 400 vector instructions a
-// wave and span (conversion, maximum, exponential, comparison) bound it, not
-// memory; 512 x 131,072 float32 with the second launch 56 us (4.8 TB/s).
+// 512 x 50,280 bfloat16 take 24.4 us (2.1 TB/s), bound by neither memory nor the
+// vector units: their 407 instructions a wave and span are busy for 24,800 of
+// the some 55,000 cycles (by counter), and the two waves of a SIMD wait half of
+// their time, at the barrier, the lane reads and the ballots of each span.
+// 512 x 131,072 float32 with the second launch 56 us (4.8 TB/s).
 
 constexpr int kThreads = 256;
 constexpr int kMaxParts = 32;              // of a row; more logits: several spans a part
@@ -355,8 +357,12 @@ constexpr int kColumns = 256;  // 16-byte columns of a workgroup
 // The beams that move (p[k] != k) get their parents' columns, 16 bytes or one
 // at `at`.  One thread holds its column of all the beams: it reads every parent
 // before it writes, so that the states are reordered in place whatever the
-// parents are.  Up to four beams the choice is a few register selects; more go
-// through the thread's own slots of LDS, which can be indexed.
+// parents are.  Up to four beams the choice is a few register selects: 8 x 4
+// beams, 734 MB of states, of which they read and write 1.0 GB, 169 us (6.0
+// TB/s).  More go through the thread's own slots of LDS, which can be indexed, and
+// are slower by it: the same states as 4 x 8 beams 474 us (2.2 TB/s, at 257
+// registers one wave a SIMD), as 2 x 16 beams 289 us (3.7 TB/s); bytes that are no
+// multiple of 16 move at 1.8 to 2.0 TB/s there, at 5.0 with up to four beams.
 template <int MAXK, bool STREAM, typename C>
 __device__ __forceinline__ void move_column(uint8_t* base, int64_t bytes, const int (&p)[MAXK], uint32_t need, int64_t at,
                                             uint8_t* slots) {
@@ -499,7 +505,7 @@ hipError_t launch_beam_reorder(int64_t B, int64_t K, const int32_t* parent, int 
     }
     const dim3 grid(static_cast<uint32_t>(imin64(a.first[count], int64_t{1} << 23)));  // below 2^32 threads; the kernel strides
     // States beyond the 256 MB last-level cache stream past it: 734 MB take 182 us
-    // so and 201 us through it, but 245 MB 73 us so and 61 us through it.
+    // so and 201 us through it, but 245 MB 73 us so and 61 us through it (four beams).
     auto launch = [&](auto stream) {
         constexpr bool S = decltype(stream)::value;
         if (K <= 4)

@@ -327,7 +327,7 @@ __device__ __forceinline__ TileAt tile_at(int64_t t, int64_t tm, int64_t tn) {
 // + v, v = 8 is left and v = 7 is not): the sum of 2,560 normal ones is 1.5e-5
 // off, relative, of positive ones with wide channels in both operands 1.2e-4, and
 // any sum within 7 x 2^-13 of the sum of magnitudes.  With the operands widened to
-// bfloat16, which is exact, 3e-7, at half the rate (few rows: 1 x 2,560 x 10,240
+// bfloat16, which is exact, 5e-8, at half the rate (few rows: 1 x 2,560 x 10,240
 // 8.7 us instead of 7.7).  A bfloat16 output (2^-8) does not show it unless the
 // sum cancels, a float32 one would: WIDE is that.
 template <int DT, bool WIDE>
