@@ -1,6 +1,8 @@
 """ctypes binding of the operators around the scan (C ABI in include/mssm_block.h).
 
-As binding.py: argument marshalling only, on torch's current HIP stream.  These
+As binding.py: argument marshalling only, on the current HIP stream of the
+tensors' device (the library launches on the current device, which is switched
+for the call where it is another one).  These
 are operators of serving: they have no backward, and what they return from
 tensors that require gradients does not.  A
 decode step makes these calls once a layer, with kernels of a few microseconds,
@@ -63,15 +65,17 @@ def _declare():
 _declare()
 
 
-def _req(t, name, shape, dtype):
-    """binding._req, which says what is wrong, for a tensor that is not right at first sight."""
-    if t is None or not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+def _req(t, name, shape, dtype, dev):
+    """binding._req, which says what is wrong, for a tensor that is not right at first sight; dev: the index of
+    the GPU that the call's first tensor is on."""
+    if t is None or not (t.get_device() == dev and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
         binding._req(t, name, shape, dtype)
+        raise ValueError(f"{name} is on device {t.get_device()}, the call's other tensors on {dev}")
 
 
-def _opt(t, name, shape, dtype):
+def _opt(t, name, shape, dtype, dev):
     if t is not None:
-        _req(t, name, shape, dtype)
+        _req(t, name, shape, dtype, dev)
 
 
 def _ptr(t):
@@ -89,6 +93,9 @@ def _new(shape, dtype, device):
     if len(shape) == 2:
         return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
     return torch.empty(shape, dtype=dtype, device=device)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(status: int):
@@ -121,19 +128,23 @@ def _norm_args(x, weight, residual, residual_out, eps):
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
     code = _dtype_code(x)
-    _req(x, "x", shape, x.dtype)
-    _req(weight, "weight", (D,), torch.float32)
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a GPU tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _req(weight, "weight", (D,), torch.float32, dev)
     kept = residual if residual is not None else residual_out
     rcode = _dtype_code(kept) if kept is not None else code
     if residual is not None:
-        _req(residual, "residual", shape, residual.dtype)
+        _req(residual, "residual", shape, residual.dtype, dev)
     if residual_out is not None:
-        _req(residual_out, "residual_out", shape, kept.dtype)
+        _req(residual_out, "residual_out", shape, kept.dtype, dev)
     elif residual is not None:
         residual_out = torch.empty_like(residual)
     if not eps >= 0.0:
         raise ValueError(f"eps = {eps} must not be negative")
-    return _norm_problem(x.numel() // D if D else 0, D, code, rcode, eps)[0], residual_out
+    return _norm_problem(x.numel() // D if D else 0, D, code, rcode, eps)[0], residual_out, dev
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None):
@@ -143,13 +154,16 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None):
     Returns (y, residual_out): y in x's type, residual_out = h in the
     residual's (None without a residual, unless given).  residual_out may be
     residual and y may be x.  Forward only: no gradient is recorded."""
-    prob, residual_out = _norm_args(x, weight, residual, residual_out, eps)
+    prob, residual_out, dev = _norm_args(x, weight, residual, residual_out, eps)
     if y is None:
         y = torch.empty_like(x)
     else:
-        _req(y, "y", x.shape, x.dtype)
+        _req(y, "y", x.shape, x.dtype, dev)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return add_rmsnorm(x, weight, residual, eps, y, residual_out)
     _run(lib.mssm_add_rmsnorm(prob, x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), _ptr(residual_out),
-                              _raw_stream(x.get_device())))
+                              _raw_stream(dev)))
     return y, residual_out
 
 
@@ -158,17 +172,20 @@ def add_rmsnorm_q8(x, weight, residual=None, eps=1e-5, q=None, scale=None, resid
     float32 with y ~ q * scale, scale = max(max|y|, 1e-30) / 448 of each row.
     Returns (q, scale, residual_out); linear() takes q and scale as x and
     x_scale.  Forward only: no gradient is recorded."""
-    prob, residual_out = _norm_args(x, weight, residual, residual_out, eps)
+    prob, residual_out, dev = _norm_args(x, weight, residual, residual_out, eps)
     if q is None:
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:
-        _req(q, "q", x.shape, torch.float8_e4m3fn)
+        _req(q, "q", x.shape, torch.float8_e4m3fn, dev)
     if scale is None:
         scale = _new(x.shape[:-1], torch.float32, x.device)
     else:
-        _req(scale, "scale", x.shape[:-1], torch.float32)
+        _req(scale, "scale", x.shape[:-1], torch.float32, dev)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return add_rmsnorm_q8(x, weight, residual, eps, q, scale, residual_out)
     _run(lib.mssm_add_rmsnorm_q8(prob, x.data_ptr(), _ptr(residual), weight.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                 _ptr(residual_out), _raw_stream(x.get_device())))
+                                 _ptr(residual_out), _raw_stream(dev)))
     return q, scale, residual_out
 
 
@@ -194,27 +211,33 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
         raise ValueError(f"activation {activation!r} is not one of {sorted(k for k in ACTIVATIONS if k)}")
     shape, N = x.shape, w.shape[0]
     lead, K = shape[:-1], shape[-1]
-    _req(x, "x", shape, act)
-    _req(w, "w", (N, K), act)
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a GPU tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _req(w, "w", (N, K), act, dev)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if act == torch.float8_e4m3fn else act
     if out_dtype not in (torch.float32, torch.bfloat16) or (act == torch.float32 and out_dtype != torch.float32):
         raise TypeError(f"out_dtype {out_dtype} is not available for {act} operands")
     if act == torch.float8_e4m3fn:
-        _req(x_scale, "x_scale", lead, torch.float32)
-        _req(w_scale, "w_scale", (N,), torch.float32)
+        _req(x_scale, "x_scale", lead, torch.float32, dev)
+        _req(w_scale, "w_scale", (N,), torch.float32, dev)
     elif x_scale is not None or w_scale is not None:
         raise ValueError("x_scale and w_scale belong to 8-bit operands")
-    _opt(bias, "bias", (N,), torch.float32)
-    _opt(residual, "residual", (*lead, N), out_dtype)
+    _opt(bias, "bias", (N,), torch.float32, dev)
+    _opt(residual, "residual", (*lead, N), out_dtype, dev)
     if y is None:
         y = _new((*lead, N), out_dtype, x.device)
     else:
-        _req(y, "y", (*lead, N), out_dtype)
-    dev = x.get_device()
+        _req(y, "y", (*lead, N), out_dtype, dev)
     prob, nbytes, _ = _linear_problem(x.numel() // K if K else 0, K, N, _CODES[act], _CODES[out_dtype],
                                       ACTIVATIONS[activation], dev)
     ws = _workspace(nbytes, x.device, workspace)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return linear(x, w, bias, residual, activation, x_scale, w_scale, out_dtype, y, ws)
     _run(lib.mssm_linear(prob, x.data_ptr(), _ptr(x_scale), w.data_ptr(), _ptr(w_scale), _ptr(bias), _ptr(residual),
                          y.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev)))
     return y
@@ -232,12 +255,16 @@ def beam_select(logits, scores, finished=None, end_token=None, scores_out=None, 
     if logits is None or logits.dim() != 3:
         raise ValueError("logits must be (B, K, V)")
     B, K, V = logits.shape
-    _req(logits, "logits", (B, K, V), logits.dtype)
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("logits must be a GPU tensor")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
     code = _dtype_code(logits)
     if K > MAX_BEAMS:
         raise ValueError(f"{K} beams: at most {MAX_BEAMS}")
-    _req(scores, "scores", (B, K), torch.float32)
-    _opt(finished, "finished", (B, K), torch.bool)
+    _req(scores, "scores", (B, K), torch.float32, dev)
+    _opt(finished, "finished", (B, K), torch.bool, dev)
     if end_token is None:
         if finished is not None or finished_out is not None:
             raise ValueError("finished beams need an end_token")
@@ -246,24 +273,26 @@ def beam_select(logits, scores, finished=None, end_token=None, scores_out=None, 
             raise ValueError(f"end_token {end_token} is not in 0..{V - 1}")
         if finished_out is None:
             finished_out = _new((B, K), torch.bool, logits.device)
-    _opt(finished_out, "finished_out", (B, K), torch.bool)
+    _opt(finished_out, "finished_out", (B, K), torch.bool, dev)
     if scores_out is None:
         scores_out = torch.empty_like(scores)
     else:
-        _req(scores_out, "scores_out", (B, K), torch.float32)
+        _req(scores_out, "scores_out", (B, K), torch.float32, dev)
     if parent is None:
         parent = torch.empty_like(scores, dtype=torch.int32)
     else:
-        _req(parent, "parent", (B, K), torch.int32)
+        _req(parent, "parent", (B, K), torch.int32, dev)
     if token is None:
         token = torch.empty_like(parent)
     else:
-        _req(token, "token", (B, K), torch.int32)
+        _req(token, "token", (B, K), torch.int32, dev)
     prob, nbytes, _ = _beam_problem(B, K, V, code, -1 if end_token is None else end_token)
     ws = _workspace(nbytes, logits.device, workspace)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return beam_select(logits, scores, finished, end_token, scores_out, parent, token, finished_out, ws)
     _run(lib.mssm_beam_select(prob, logits.data_ptr(), scores.data_ptr(), _ptr(finished), scores_out.data_ptr(),
-                              parent.data_ptr(), token.data_ptr(), _ptr(finished_out), _ptr(ws), nbytes,
-                              _raw_stream(logits.get_device())))
+                              parent.data_ptr(), token.data_ptr(), _ptr(finished_out), _ptr(ws), nbytes, _raw_stream(dev)))
     return scores_out, parent, token, finished_out
 
 
@@ -276,7 +305,10 @@ def beam_reorder(parent, states):
     if parent is None or parent.dim() != 2:
         raise ValueError("parent must be (B, K)")
     B, K = parent.shape
-    _req(parent, "parent", (B, K), torch.int32)
+    dev = parent.get_device()
+    if dev < 0:
+        raise ValueError("parent must be a GPU tensor")
+    _req(parent, "parent", (B, K), torch.int32, dev)
     if K > MAX_BEAMS:
         raise ValueError(f"{K} beams: at most {MAX_BEAMS}")
     each = [states] if isinstance(states, torch.Tensor) else list(states)
@@ -286,10 +318,15 @@ def beam_reorder(parent, states):
     for i, t in enumerate(each):
         if t is None or t.dim() < 2 or t.shape[1] != B * K:
             raise ValueError(f"states[{i}] must be (layers, {B * K}, ...)")
-        _req(t, f"states[{i}]", t.shape, t.dtype)
+        if t.get_device() != dev or not t.is_contiguous():
+            _req(t, f"states[{i}]", t.shape, t.dtype, dev)
         if t.numel() == 0:
             raise MssmError(-2, lib)
         e = entries[i]
         e.data, e.layers, e.bytes = t.data_ptr(), t.shape[0], t.numel() // (t.shape[0] * B * K) * t.element_size()
-    _run(lib.mssm_beam_reorder(B, K, parent.data_ptr(), len(each), entries, _raw_stream(parent.get_device())))
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            beam_reorder(parent, each)
+        return states
+    _run(lib.mssm_beam_reorder(B, K, parent.data_ptr(), len(each), entries, _raw_stream(dev)))
     return states
