@@ -301,12 +301,13 @@ __device__ __forceinline__ i32x4 buffer_words(const uint8_t* base, uint32_t byte
 // offset outside the descriptor's range gives zeros.  Written as one statement
 // without outputs because the compiler orders every LDS read behind every such
 // load it knows of, which would undo the double buffering; the counter wait is
-// in tile_barrier().  (m0 needs one wait state before the load.)
+// in tile_barrier().  (m0 needs one wait state before the load; nothing else in
+// these kernels uses m0, which the compiler keeps reserved.)
 __device__ __forceinline__ void load_to_lds(uint32_t lds, i32x4 rsrc, uint32_t voff, uint32_t soff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory", "m0");
+                 : "memory");
 }
 
 // The tile that was being loaded is in LDS and nobody reads the other one any more.

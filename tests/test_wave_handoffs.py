@@ -61,12 +61,3 @@ def test_linear_output_blocks():
     assert re.search(rf"{FENCE}\s*}}$", stage), "other lanes read the block next"
     # nothing else writes or reads the blocks: stored by stage(), read by the calls behind it
     assert len(re.findall(r"out\.stage\(", kernel)) == len(re.findall(r"out\.stage\(", stage)) == 1
-
-
-def test_statements_that_write_m0_say_so():
-    text = source("linear.hip")
-    found = re.findall(r"asm volatile\((.*?)\);", text, re.S)
-    assert any("m0" in f for f in found)
-    for f in found:
-        if "s_mov_b32 m0" in f:
-            assert re.search(r':\s*"memory",\s*"m0"\s*$', f)
