@@ -1,0 +1,530 @@
+// gdr_bwd.hip -- the gradients of the gated delta rule (mssm_gdr_bwd_saved,
+// mssm_gdr_bwd), from what the forward keeps (S before every chunk, e, and the
+// matrices N and P with their transposes; gdr_prep.hip has the equations).
+//
+// With L the adjoint of the state behind a chunk, b_C its whole log decay and
+// k, q scaled, D = exp(b_C - b):
+//
+//     du = Pᵀ dy + D (L k)          Z = du + Nᵀ (beta du)        dr = beta Z = dv
+//     L' = exp(b_C) L + sum_t scale exp(b_t) dy_t q_tᵀ - exp(b_t) dr_t k_tᵀ
+//
+// is the chain, backwards over the chunks and, as the forward's, for every value
+// element by itself.  Given L and Z every chunk has its gradients by itself:
+//
+//     dbeta = e . Z                 dP_ij = dy_i . u_j     M_ij = -G_ij dr_i . u_j  (j < i)
+//     dq    = scale exp(b) dy S + (G dP) k
+//     dk    = -exp(b) dr S + M k    where a key is read with (its "row" part, decays exp(b))
+//           + D u L + (G dP)ᵀ q + Mᵀ k    where it is written with (exp(-b))
+//     db    = q . dq + k . dk_row - k . dk_column, and for the chunk's last token
+//             exp(b_C) <L, S> + sum_t D_t k_t . (L u_t) more;   dg_i = sum_{t >= i} db_t
+#include "gdr_common.h"
+
+namespace mssm {
+namespace {
+
+using namespace gdrk;
+
+struct AdjointArgs {
+    const void *q, *k, *dy;
+    const int32_t* offsets;
+    const uint8_t* mats;
+    const float* dh_final;
+    void* dv;
+    float* dh0;
+    float* adjoints;
+    float* pulls;
+    int64_t T, N, G, H, K, V, parts;
+    int64_t mat_bytes, at_f, at_nt, at_pt;
+};
+
+// The chain: as gdr_fwd_kernel, which see for the columns of a wave and its lanes.
+template <typename T, int KP, int CT>
+__global__ __launch_bounds__(256) void gdr_adjoint_kernel(AdjointArgs a) {
+    constexpr int PL = kPlanes<T>, KS = KP / 32;
+    typedef RowTile<KP> Rows;
+    typedef ColumnTile<KP> Columns;
+    __shared__ __align__(16) uint8_t lds[PL * (Rows::kBytes + 2 * Columns::kBytes)];
+    uint8_t *lds_k = lds, *lds_kt = lds_k + PL * Rows::kBytes, *lds_qt = lds_kt + PL * Columns::kBytes;
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
+    const int64_t part = blockIdx.x % a.parts, head = blockIdx.x / a.parts, h = head % a.H, n = head / a.H;
+    const int64_t hg = h / (a.H / a.G);
+    const int64_t v0 = (part * 4 + w) * 16 * CT;
+    const bool in_v = v0 + c * CT < a.V;
+    const Span sp = span_of(a.offsets, n, a.T, a.N);
+    const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
+
+    f32x4 L[CT][KP / 16];
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int m = 0; m < KP / 16; ++m) {
+            L[t][m] = f32x4{0, 0, 0, 0};
+            if (a.dh_final && in_v && 16 * m < a.K)
+                L[t][m] = *reinterpret_cast<const f32x4*>(a.dh_final + ((n * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g);
+        }
+
+    const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
+    const T* kp = static_cast<const T*>(a.k) + sp.start * qk_stride + hg * a.K;
+    const T* qp = static_cast<const T*>(a.q) + sp.start * qk_stride + hg * a.K;
+    const T* dyp = static_cast<const T*>(a.dy) + sp.start * v_stride + h * a.V + v0;
+    T* dvp = static_cast<T*>(a.dv) + sp.start * v_stride + h * a.V + v0;
+    Patch<T, KP> pk, pq;
+    auto fetch = [&](int64_t chunk) {
+        const int len = static_cast<int>(imin64(kC, sp.len - chunk * kC));
+        pk.load(kp + chunk * kC * qk_stride, qk_stride, len, static_cast<int>(a.K), tid);
+        pq.load(qp + chunk * kC * qk_stride, qk_stride, len, static_cast<int>(a.K), tid);
+    };
+    if (chunks) fetch(chunks - 1);
+    for (int64_t chunk = chunks - 1; chunk >= 0; --chunk) {
+        const int len = static_cast<int>(imin64(kC, sp.len - chunk * kC));
+        const uint8_t* mat = a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes;
+        const float* f = reinterpret_cast<const float*>(mat + a.at_f);
+        const int64_t t0 = chunk * kC;
+        __syncthreads();
+        pk.store(lds_k, lds_kt, tid);
+        pq.store(nullptr, lds_qt, tid);
+        __syncthreads();
+        if (chunk > 0) fetch(chunk - 1);
+        if (v0 >= a.V) continue;
+
+        float dy[16][CT];  // item 4 rt + r: token 16 rt + 4 g + r
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = (i >> 2) * 16 + 4 * g + (i & 3);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) dy[i][j] = 0.0f;
+            if (t < len && in_v) load_values(dyp + (t0 + t) * v_stride + c * CT, dy[i]);
+        }
+        if (in_v) {
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int m = 0; m < KP / 16; ++m)
+                    if (16 * m < a.K)
+                        *reinterpret_cast<f32x4*>(a.adjoints + (((slot0 + chunk) * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g) = L[t][m];
+        }
+        // du = D (L k) + Pᵀ dy
+        f32x4 X[CT][4] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            Planes<3> lt[CT];
+#pragma unroll
+            for (int t = 0; t < CT; ++t) lt[t] = split<3>(L[t][2 * s], L[t][2 * s + 1]);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const Planes<PL> kf = read_tile<Rows, PL>(lds_k, 16 * rt + c, 4 * s + g);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) X[t][rt] = mma(kf, lt[t], X[t][rt]);
+            }
+        }
+        f32x4 beta[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            beta[rt] = *reinterpret_cast<const f32x4*>(f + kC + 16 * rt + 4 * g);
+            const f32x4 ed = *reinterpret_cast<const f32x4*>(f + 2 * kC + 16 * rt + 4 * g);
+#pragma unroll
+            for (int t = 0; t < CT; ++t) X[t][rt] *= ed;
+        }
+        auto rows_of = [&](int rt, int t) { return f32x4{dy[4 * rt][t], dy[4 * rt + 1][t], dy[4 * rt + 2][t], dy[4 * rt + 3][t]}; };
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            Planes<PL> d[CT];
+#pragma unroll
+            for (int t = 0; t < CT; ++t) d[t] = split<PL>(rows_of(2 * s, t), rows_of(2 * s + 1, t));
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                if (block_of<false>(rt, s) < 0) continue;
+                const Planes<3> pb = load_block<3>(mat + a.at_pt, block_of<false>(rt, s), lane);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) X[t][rt] = mma(pb, d[t], X[t][rt]);
+            }
+        }
+        // Z = du + Nᵀ (beta du)
+        Planes<3> m[CT][2];
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) m[t][s] = split<3>(beta[2 * s] * X[t][2 * s], beta[2 * s + 1] * X[t][2 * s + 1]);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (block_of<false>(rt, s) < 0) continue;
+                const Planes<3> nb = load_block<3>(mat + a.at_nt, block_of<false>(rt, s), lane);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) X[t][rt] = mma(nb, m[t][s], X[t][rt]);
+            }
+        float* z = a.pulls + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c * CT;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = (i >> 2) * 16 + 4 * g + (i & 3);
+            float x[CT], dr[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                x[j] = X[j][i >> 2][i & 3];
+                dr[j] = x[j] * beta[i >> 2][i & 3];
+                X[j][i >> 2][i & 3] = dr[j];
+            }
+            if (in_v) store_values(z + t * a.V, x);
+            if (t < len && in_v) store_values(dvp + (t0 + t) * v_stride + c * CT, dr);
+        }
+        // the adjoint of the state before the chunk
+        const float last = f[4 * kC];
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int i = 0; i < KP / 16; ++i) L[t][i] *= last;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            f32x4 ek[2], eq[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ek[i] = -*reinterpret_cast<const f32x4*>(f + 32 * s + 16 * i + 4 * g);
+                eq[i] = *reinterpret_cast<const f32x4*>(f + 3 * kC + 32 * s + 16 * i + 4 * g);
+            }
+            Planes<3> dr[CT], dq[CT];
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                dr[t] = split<3>(ek[0] * X[t][2 * s], ek[1] * X[t][2 * s + 1]);
+                dq[t] = split<3>(eq[0] * rows_of(2 * s, t), eq[1] * rows_of(2 * s + 1, t));
+            }
+#pragma unroll
+            for (int i = 0; i < KP / 16; ++i) {
+                const Planes<PL> kt = read_tile<Columns, PL>(lds_kt, 16 * i + c, 4 * s + g);
+                const Planes<PL> qt = read_tile<Columns, PL>(lds_qt, 16 * i + c, 4 * s + g);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) {
+                    L[t][i] = mma(kt, dr[t], L[t][i]);
+                    L[t][i] = mma(qt, dq[t], L[t][i]);
+                }
+            }
+        }
+    }
+    if (a.dh0 && in_v) {
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int m = 0; m < KP / 16; ++m)
+                if (16 * m < a.K)
+                    *reinterpret_cast<f32x4*>(a.dh0 + ((n * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g) = L[t][m];
+    }
+}
+
+// ---- the chunks' gradients --------------------------------------------------------
+
+struct GradArgs {
+    const void *q, *k, *dy;
+    const float *g, *beta;
+    const int32_t* offsets;
+    const float *states, *misses, *adjoints, *pulls;
+    void *dq, *dk;
+    float *dg, *dbeta;
+    int64_t T, N, G, H, K, V, slot0;
+    float scale;
+    int norm;
+};
+
+constexpr int kPitch = kC + 4;  // floats of a row of a 64 x 64 matrix in LDS
+
+// 32 value elements of a state as planes in LDS, an operand row (64 bytes) for
+// each of KP columns; slot (g, j) is element 8 g + j.
+template <int KP>
+struct StateTile {
+    static constexpr int kBytes = KP * 64;
+    __device__ static __forceinline__ int at(int column, int piece) { return column * 64 + ((piece ^ ((column >> 1) & 3)) * 16); }
+};
+
+__device__ __forceinline__ f32x4 load_four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load_four(const uint16_t* p) {
+    const u32x2 a = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{bf16_lo(a[0]), bf16_hi(a[0]), bf16_lo(a[1]), bf16_hi(a[1])};
+}
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b, float s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __builtin_fmaf(a[i], b[i], s);
+    return s;
+}
+__device__ __forceinline__ float group4_sum(float v) {  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// A workgroup: one chunk and one head of q and k, with all value heads that
+// share it, whose dq and dk are summed in registers.  Wave w has the tokens 16 w
+// .. 16 w + 15 in the columns of its accumulators and the key elements in their
+// rows, so that a lane's factors are one token's and it stores four neighbours.
+template <typename T, int KP>
+__global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
+    constexpr int PL = kPlanes<T>, KM = KP / 16;
+    typedef ColumnTile<KP> Columns;
+    typedef StateTile<KP> State;
+    constexpr int kMatrix = kC * kPitch * 4, kKeys = 2 * PL * Columns::kBytes, kStates = 6 * State::kBytes;
+    __shared__ __align__(16) uint8_t lds[kKeys + 2 * kMatrix > kStates ? kKeys + 2 * kMatrix : kStates];
+    __shared__ float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[kC], s_end[8];
+    uint8_t *lds_s = lds, *lds_l = lds + 3 * State::kBytes;              // while summing over value elements
+    uint8_t *lds_kt = lds, *lds_qt = lds + PL * Columns::kBytes;         // then
+    float *sX = reinterpret_cast<float*>(lds + kKeys), *sM = sX + kC * kPitch;
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
+    const int64_t hg = blockIdx.x % a.G, slot = a.slot0 + blockIdx.x / a.G;
+    const Chunk ch = chunk_of(a.offsets, slot, a.T, a.N);
+    if (ch.len == 0) return;
+    const int K = static_cast<int>(a.K), V = static_cast<int>(a.V);
+    const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
+    const T* kp = static_cast<const T*>(a.k) + ch.start * qk_stride + hg * a.K;
+    const T* qp = static_cast<const T*>(a.q) + ch.start * qk_stride + hg * a.K;
+    const int row = 16 * w + c;  // this lane's token
+    const bool in_t = row < ch.len;
+    float rk = 1.0f, rq = 1.0f;
+    if (a.norm) {
+        float k2 = 0.0f, q2 = 0.0f;
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+            const bool in = in_t && 16 * m < K;
+            const f32x4 zero = {0, 0, 0, 0};
+            const f32x4 k4 = in ? load_four(kp + row * qk_stride + 16 * m + 4 * g) : zero;
+            const f32x4 q4 = in ? load_four(qp + row * qk_stride + 16 * m + 4 * g) : zero;
+            k2 = dot4(k4, k4, k2);
+            q2 = dot4(q4, q4, q2);
+        }
+        rk = 1.0f / __builtin_sqrtf(group4_sum(k2) + kGdrNormEps);
+        rq = 1.0f / __builtin_sqrtf(group4_sum(q2) + kGdrNormEps);
+    }
+    if (g == 0) s_rk[row] = rk, s_rq[row] = rq;
+
+    f32x4 dq_sum[KM] = {}, dk_sum[KM] = {};
+    const int per = static_cast<int>(a.H / a.G);
+    for (int hh = 0; hh < per; ++hh) {
+        const int64_t h = hg * per + hh, cell = slot * a.H + h;
+        __syncthreads();  // the head before is done with LDS
+        if (w == 0) {
+            const double b = decays_since_start(a.g + ch.start * a.H + h, a.H, ch.len, lane);
+            const float hi = static_cast<float>(b);
+            s_hi[lane] = hi;
+            s_lo[lane] = static_cast<float>(b - hi);
+            s_beta[lane] = lane < ch.len ? a.beta[(ch.start + lane) * a.H + h] : 0.0f;
+        }
+        Patch<T, KP> pk, pq;
+        pk.load(kp, qk_stride, ch.len, K, tid);
+        pq.load(qp, qk_stride, ch.len, K, tid);
+        const float *S = a.states + cell * a.V * a.K, *L = a.adjoints + cell * a.V * a.K;
+        const float *e = a.misses + cell * kC * a.V, *z = a.pulls + cell * kC * a.V;
+        const T* dy = static_cast<const T*>(a.dy) + ch.start * v_stride + h * a.V;
+
+        // sums over the value elements
+        f32x4 yS[KM] = {}, zS[KM] = {}, uL[KM] = {}, dP[4] = {}, dA[4] = {};
+        float dbeta = 0.0f, both = 0.0f;
+        for (int vb = 0; vb < V; vb += 32) {
+            __syncthreads();
+            {   // 8 value elements of 2 columns a thread
+                const int o = tid / (KP / 2), kc = tid % (KP / 2) * 2;
+                if (o < 4) {
+                    float s0[8], s1[8], l0[8], l1[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = vb + 8 * o < V && kc < K;
+                        const f32x2 zero = {0, 0};
+                        const f32x2 s2 = in ? *reinterpret_cast<const f32x2*>(S + static_cast<int64_t>(vb + 8 * o + j) * K + kc) : zero;
+                        const f32x2 l2 = in ? *reinterpret_cast<const f32x2*>(L + static_cast<int64_t>(vb + 8 * o + j) * K + kc) : zero;
+                        s0[j] = s2[0]; s1[j] = s2[1]; l0[j] = l2[0]; l1[j] = l2[1];
+                        both = __builtin_fmaf(s2[0], l2[0], __builtin_fmaf(s2[1], l2[1], both));
+                    }
+                    auto put = [&](uint8_t* to, int column, const Planes<3>& p) {
+#pragma unroll
+                        for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x4*>(to + n * State::kBytes + State::at(column, o)) = p.p[n];
+                    };
+                    put(lds_s, kc, split<3>(s0));
+                    put(lds_s, kc + 1, split<3>(s1));
+                    put(lds_l, kc, split<3>(l0));
+                    put(lds_l, kc + 1, split<3>(l1));
+                }
+            }
+            __syncthreads();
+            const int v = vb + 8 * g;
+            const bool in = v < V;
+            auto eight = [&](const float* p, int t, float (&x)[8]) {
+                const f32x4 zero = {0, 0, 0, 0};
+                const f32x4 lo = in ? load_four(p + t * a.V + v) : zero, hi = in ? load_four(p + t * a.V + v + 4) : zero;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
+            };
+            float x[8], zz[8];
+            eight(z, row, zz);
+            eight(e, row, x);
+            const float beta = s_beta[row];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dbeta = __builtin_fmaf(x[i], zz[i], dbeta), x[i] *= beta;
+            const Planes<PL> dyf = load_planes(dy + row * v_stride + v, in && in_t);
+            const Planes<3> zf = split<3>(zz), uf = split<3>(x);
+#pragma unroll
+            for (int m = 0; m < KM; ++m) {
+                const Planes<3> sf = read_tile<State, 3>(lds_s, 16 * m + c, g), lf = read_tile<State, 3>(lds_l, 16 * m + c, g);
+                yS[m] = mma(sf, dyf, yS[m]);
+                zS[m] = mma(sf, zf, zS[m]);
+                uL[m] = mma(lf, uf, uL[m]);
+            }
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb) {  // rows (of the accumulator): token i of this wave; columns: token j
+                if (jb > w) continue;
+                float xj[8];
+                eight(e, 16 * jb + c, xj);
+                const float bj = s_beta[16 * jb + c];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xj[i] *= bj;
+                const Planes<3> uj = split<3>(xj);
+                dP[jb] = mma(dyf, uj, dP[jb]);
+                dA[jb] = mma(zf, uj, dA[jb]);
+            }
+        }
+        __syncthreads();
+        pk.store(nullptr, lds_kt, tid);
+        pq.store(nullptr, lds_qt, tid);
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            const int j = 16 * jb + c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * w + 4 * g + r;
+                float x = 0.0f, mm = 0.0f;
+                if (j <= i) {
+                    const float d = decay_between(s_hi[i], s_lo[i], s_hi[j], s_lo[j]);
+                    x = a.scale * d * dP[jb][r];
+                    mm = j < i ? -d * s_beta[i] * dA[jb][r] : 0.0f;
+                }
+                sX[i * kPitch + j] = x;
+                sM[i * kPitch + j] = mm;
+            }
+        }
+        dbeta = group4_sum(dbeta);
+        if (g == 0 && in_t) a.dbeta[(ch.start + row) * a.H + h] = dbeta;
+        both = group_sum<16>(both);
+        both = group4_sum(both);
+        if (lane == 0) s_end[w] = both;
+        __syncthreads();
+
+        const float in_chunk = whole_exp(static_cast<double>(s_hi[row]) + s_lo[row]);
+        const double end = static_cast<double>(s_hi[kC - 1]) + s_lo[kC - 1];
+        const float to_end = whole_exp(end - (static_cast<double>(s_hi[row]) + s_lo[row]));
+        const float fy = a.scale * in_chunk, fz = -in_chunk * s_beta[row];
+        f32x4 dq[KM], dkr[KM], dkc[KM], k4[KM], q4[KM];
+        float wrote = 0.0f;
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+            const bool in = in_t && 16 * m < K;
+            const f32x4 zero = {0, 0, 0, 0};
+            k4[m] = in ? rk * load_four(kp + row * qk_stride + 16 * m + 4 * g) : zero;
+            q4[m] = in ? rq * load_four(qp + row * qk_stride + 16 * m + 4 * g) : zero;
+            dq[m] = fy * yS[m];
+            dkr[m] = fz * zS[m];
+            dkc[m] = to_end * uL[m];
+            wrote = dot4(k4[m], dkc[m], wrote);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            // the tokens summed over: 32 s + slot; this lane's row of X and M, and its column
+            float xr[8], mr[8], xc[8], mc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = 32 * s + 4 * g + (i & 3) + (i >> 2) * 16;
+                const float rkt = s_rk[t];
+                xr[i] = sX[row * kPitch + t] * rkt;
+                mr[i] = sM[row * kPitch + t] * rkt;
+                xc[i] = sX[t * kPitch + row] * s_rq[t];
+                mc[i] = sM[t * kPitch + row] * rkt;
+            }
+            const Planes<3> xrf = split<3>(xr), mrf = split<3>(mr), xcf = split<3>(xc), mcf = split<3>(mc);
+#pragma unroll
+            for (int m = 0; m < KM; ++m) {
+                const Planes<PL> kt = read_tile<Columns, PL>(lds_kt, 16 * m + c, 4 * s + g);
+                const Planes<PL> qt = read_tile<Columns, PL>(lds_qt, 16 * m + c, 4 * s + g);
+                dq[m] = mma(kt, xrf, dq[m]);
+                dkr[m] = mma(kt, mrf, dkr[m]);
+                dkc[m] = mma(kt, mcf, dkc[m]);
+                dkc[m] = mma(qt, xcf, dkc[m]);
+            }
+        }
+        float db = 0.0f;
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+            db = dot4(q4[m], dq[m], db);
+            db = dot4(k4[m], dkr[m] - dkc[m], db);
+            dq_sum[m] += dq[m];
+            dk_sum[m] += dkr[m] + dkc[m];
+        }
+        db = group4_sum(db);
+        if (g == 0) s_db[row] = db;
+        wrote = group4_sum(wrote);
+        wrote = group_sum<16>(wrote);
+        if (lane == 0) s_end[4 + w] = wrote;
+        __syncthreads();
+        if (w == 0) {
+            double v = s_db[lane];
+            if (lane == kC - 1)
+                v += static_cast<double>(whole_exp(end)) * ((static_cast<double>(s_end[0]) + s_end[1]) + (static_cast<double>(s_end[2]) + s_end[3])) +
+                     ((static_cast<double>(s_end[4]) + s_end[5]) + (static_cast<double>(s_end[6]) + s_end[7]));
+#pragma unroll
+            for (int d = 1; d < kC; d *= 2) {  // from the last token on
+                const double o = __shfl_down(v, d);
+                if (lane + d < kC) v += o;
+            }
+            if (lane < ch.len) a.dg[(ch.start + lane) * a.H + h] = static_cast<float>(v);
+        }
+    }
+    // through the division by their lengths
+    float qd = 0.0f, kd = 0.0f;
+    f32x4 k4[KM], q4[KM];
+#pragma unroll
+    for (int m = 0; m < KM; ++m) {
+        const bool in = in_t && 16 * m < K;
+        const f32x4 zero = {0, 0, 0, 0};
+        k4[m] = in && a.norm ? rk * load_four(kp + row * qk_stride + 16 * m + 4 * g) : zero;
+        q4[m] = in && a.norm ? rq * load_four(qp + row * qk_stride + 16 * m + 4 * g) : zero;
+        qd = dot4(q4[m], dq_sum[m], qd);
+        kd = dot4(k4[m], dk_sum[m], kd);
+    }
+    qd = group4_sum(qd);
+    kd = group4_sum(kd);
+    T* dqp = static_cast<T*>(a.dq) + (ch.start + row) * qk_stride + hg * a.K + 4 * g;
+    T* dkp = static_cast<T*>(a.dk) + (ch.start + row) * qk_stride + hg * a.K + 4 * g;
+#pragma unroll
+    for (int m = 0; m < KM; ++m) {
+        if (!in_t || 16 * m >= K) continue;
+        const f32x4 x = rq * (dq_sum[m] - qd * q4[m]), y = rk * (dk_sum[m] - kd * k4[m]);
+        const float xs[4] = {x[0], x[1], x[2], x[3]}, ys[4] = {y[0], y[1], y[2], y[3]};
+        store_row(dqp + 16 * m, xs);
+        store_row(dkp + 16 * m, ys);
+    }
+}
+
+template <typename T, int KP, int CT>
+hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
+    const GdrLayout l(a.dtype, true);
+    const int64_t parts = (a.V + 64 * CT - 1) / (64 * CT);
+    const AdjointArgs k{a.q, a.k, a.dy, a.offsets, a.mats, a.dh_final, a.dv, a.dh0, a.adjoints, a.pulls,
+                        a.T, a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.factors, l.nt, l.pt};
+    gdr_adjoint_kernel<T, KP, CT><<<static_cast<uint32_t>(a.N * a.H * parts), 256, 0, s>>>(k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const GradArgs d{a.q, a.k, a.dy, a.g, a.beta, a.offsets, a.states, a.misses, a.adjoints, a.pulls, a.dq, a.dk, a.dg, a.dbeta,
+                     a.T, a.N, a.G, a.H, a.K, a.V, 0, a.scale, a.norm};
+    gdr_grad_kernel<T, KP><<<static_cast<uint32_t>(gdr_slots(a.T, a.N) * a.G), 256, 0, s>>>(d);
+    return hipGetLastError();
+}
+template <typename T, int KP>
+hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
+    if constexpr (sizeof(T) == 2 || KP == 64) {  // float32 planes of 128 columns leave no registers for a second tile
+        if (a.N * a.H >= 128 && a.V > 64) return launch_c<T, KP, 2>(a, s);
+    }
+    return launch_c<T, KP, 1>(a, s);
+}
+template <typename T>
+hipError_t launch_t(const GdrArgs& a, hipStream_t s) {
+    return a.K <= 64 ? launch_k<T, 64>(a, s) : launch_k<T, 128>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_gdr_bwd(const GdrArgs& a, hipStream_t s) {
+    return a.dtype == MSSM_F32 ? launch_t<float>(a, s) : launch_t<uint16_t>(a, s);
+}
+
+}  // namespace mssm
