@@ -30,12 +30,12 @@ constexpr int kGdrBlockBytes = 1024;
 constexpr int kGdrFactors = 5;
 struct GdrLayout {
     int p_planes;      // of P for the forward: 2 where y is bfloat16, else 3
-    int64_t n, pm, factors, nt, pt, bytes;
+    int64_t pm, n, factors, nt, pt, bytes;
     GdrLayout(int dtype, bool train) {
         p_planes = dtype == MSSM_BF16 ? 2 : 3;
-        n = 0;
-        pm = n + 3 * kGdrBlocks * kGdrBlockBytes;
-        factors = pm + p_planes * kGdrBlocks * kGdrBlockBytes;
+        pm = 0;  // the forward's P, N and factors and the backward's factors and transposes lie together
+        n = pm + p_planes * kGdrBlocks * kGdrBlockBytes;
+        factors = n + 3 * kGdrBlocks * kGdrBlockBytes;
         nt = factors + kGdrFactors * kGdrChunk * 4;
         pt = nt + (train ? 3 * kGdrBlocks * kGdrBlockBytes : 0);
         bytes = pt + (train ? 3 * kGdrBlocks * kGdrBlockBytes : 0);

@@ -37,143 +37,141 @@ struct AdjointArgs {
     int64_t mat_bytes, at_f, at_nt, at_pt;
 };
 
-// The chain: as gdr_fwd_kernel, which see for the columns of a wave and its lanes.
-template <typename T, int KP, int CT>
-__global__ __launch_bounds__(256) void gdr_adjoint_kernel(AdjointArgs a) {
-    constexpr int PL = kPlanes<T>, KS = KP / 32;
-    typedef RowTile<KP> Rows;
-    typedef ColumnTile<KP> Columns;
-    __shared__ __align__(16) uint8_t lds[PL * (Rows::kBytes + 2 * Columns::kBytes)];
-    uint8_t *lds_k = lds, *lds_kt = lds_k + PL * Rows::kBytes, *lds_qt = lds_kt + PL * Columns::kBytes;
+// The chain: as gdr_fwd_kernel, which see for its waves, LDS and lanes; Pᵀ comes from memory.
+template <typename T, int KP, int NW>
+__global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
+    constexpr bool B16 = sizeof(T) == 2;
+    constexpr int PL = kPlanes<T>, KS = KP / 32, KM = KP / 16, VC = NW * 16;
+    typedef Tile<KP> Keys;
+    typedef Tile<VC> Values;
+    constexpr int kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4, kMats = kF + kN;
+    constexpr int kKeys = 2 * PL * Keys::kBytes;
+    constexpr int kPart = B16 ? kKeys + Values::kBytes + kMats : kMats;
+    __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
+    static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const int64_t part = blockIdx.x % a.parts, head = blockIdx.x / a.parts, h = head % a.H, n = head / a.H;
     const int64_t hg = h / (a.H / a.G);
-    const int64_t v0 = (part * 4 + w) * 16 * CT;
-    const bool in_v = v0 + c * CT < a.V;
+    const int64_t vw = part * VC, v0 = vw + w * 16;
+    const bool in_v = v0 < a.V;
     const Span sp = span_of(a.offsets, n, a.T, a.N);
     const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
+    const int K = static_cast<int>(a.K);
 
-    f32x4 L[CT][KP / 16];
+    f32x4 L[KM];
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int m = 0; m < KP / 16; ++m) {
-            L[t][m] = f32x4{0, 0, 0, 0};
-            if (a.dh_final && in_v && 16 * m < a.K)
-                L[t][m] = *reinterpret_cast<const f32x4*>(a.dh_final + ((n * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g);
-        }
+    for (int m = 0; m < KM; ++m) {
+        L[m] = f32x4{0, 0, 0, 0};
+        if (a.dh_final && in_v && 16 * m < K)
+            L[m] = *reinterpret_cast<const f32x4*>(a.dh_final + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g);
+    }
 
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
     const T* kp = static_cast<const T*>(a.k) + sp.start * qk_stride + hg * a.K;
     const T* qp = static_cast<const T*>(a.q) + sp.start * qk_stride + hg * a.K;
-    const T* dyp = static_cast<const T*>(a.dy) + sp.start * v_stride + h * a.V + v0;
-    T* dvp = static_cast<T*>(a.dv) + sp.start * v_stride + h * a.V + v0;
-    Patch<T, KP> pk, pq;
-    auto fetch = [&](int64_t chunk) {
-        const int len = static_cast<int>(imin64(kC, sp.len - chunk * kC));
-        pk.load(kp + chunk * kC * qk_stride, qk_stride, len, static_cast<int>(a.K), tid);
-        pq.load(qp + chunk * kC * qk_stride, qk_stride, len, static_cast<int>(a.K), tid);
-    };
-    if (chunks) fetch(chunks - 1);
-    for (int64_t chunk = chunks - 1; chunk >= 0; --chunk) {
-        const int len = static_cast<int>(imin64(kC, sp.len - chunk * kC));
-        const uint8_t* mat = a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes;
-        const float* f = reinterpret_cast<const float*>(mat + a.at_f);
-        const int64_t t0 = chunk * kC;
-        __syncthreads();
-        pk.store(lds_k, lds_kt, tid);
-        pq.store(nullptr, lds_qt, tid);
-        __syncthreads();
-        if (chunk > 0) fetch(chunk - 1);
-        if (v0 >= a.V) continue;
-
-        float dy[16][CT];  // item 4 rt + r: token 16 rt + 4 g + r
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = (i >> 2) * 16 + 4 * g + (i & 3);
-#pragma unroll
-            for (int j = 0; j < CT; ++j) dy[i][j] = 0.0f;
-            if (t < len && in_v) load_values(dyp + (t0 + t) * v_stride + c * CT, dy[i]);
+    const T* dyp = static_cast<const T*>(a.dy) + sp.start * v_stride + h * a.V;
+    T* dvp = static_cast<T*>(a.dv) + sp.start * v_stride + h * a.V + v0 + c;
+    auto length = [&](int64_t chunk) { return static_cast<int>(imin64(kC, sp.len - chunk * kC)); };
+    auto mats_of = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes; };
+    FloatRows<KP, NW * 64> fk, fq;
+    auto fetch = [&](int64_t chunk, int half) {
+        const int len = length(chunk);
+        uint8_t* to = lds + half * kPart;
+        if constexpr (B16) {
+            rows_to_lds<KP, NW>(lds_offset(to), kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
+            rows_to_lds<KP, NW>(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
+            rows_to_lds<VC, NW>(lds_offset(to) + kKeys, dyp + vw + chunk * kC * v_stride, static_cast<uint32_t>(v_stride), len,
+                                static_cast<int>(a.V - vw), w, lane);
+            bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_f, w, lane);
+        } else {
+            bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_f, w, lane);
+            fk.load(kp + chunk * kC * qk_stride, qk_stride, len, K, tid);
+            fq.load(qp + chunk * kC * qk_stride, qk_stride, len, K, tid);
         }
+    };
+    if (chunks) fetch(chunks - 1, (chunks - 1) & 1);
+    for (int64_t chunk = chunks - 1; chunk >= 0; --chunk) {
+        const int half = static_cast<int>(chunk & 1), len = length(chunk);
+        const uint8_t* in = lds + half * kPart;
+        const uint8_t *lds_k = B16 ? in : lds + 2 * kPart, *lds_q = lds_k + PL * Keys::kBytes, *lds_dy = in + kKeys;
+        const uint8_t* lds_f = B16 ? lds_dy + Values::kBytes : in;
+        const uint8_t* lds_n = lds_f + kF;
+        const float* f = reinterpret_cast<const float*>(lds_f);
+        tile_barrier();  // this half is whole, nobody reads the other one
+        if constexpr (!B16) {
+            fk.store(lds + 2 * kPart, tid);
+            fq.store(lds + 2 * kPart + PL * Keys::kBytes, tid);
+            __syncthreads();
+        }
+        const uint8_t* pt = mats_of(chunk) + a.at_pt;
+        f32x4 dy[4];  // item r of tile rt: token 16 rt + 4 g + r of this lane's column
+        f32x4 X[4] = {};
         if (in_v) {
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
+            for (int rt = 0; rt < 4; ++rt) {
+                if constexpr (B16) {
+                    const u32x2 x = Values::four(lds_dy, rt, w, c, g);
+                    dy[rt] = f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
+                } else {
 #pragma unroll
-                for (int m = 0; m < KP / 16; ++m)
-                    if (16 * m < a.K)
-                        *reinterpret_cast<f32x4*>(a.adjoints + (((slot0 + chunk) * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g) = L[t][m];
+                    for (int r = 0; r < 4; ++r) {
+                        const int t = 16 * rt + 4 * g + r;
+                        dy[rt][r] = t < len ? dyp[(chunk * kC + t) * v_stride + v0 + c] : 0.0f;
+                    }
+                }
+            }
+            // Pᵀ dy first: it waits for memory, and for nothing that the chunk before leaves
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Planes<PL> d = split<PL>(dy[2 * s], dy[2 * s + 1]);
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt)
+                    if (block_of<false>(rt, s) >= 0) X[rt] = mma(load_block<3>(pt, block_of<false>(rt, s), lane), d, X[rt]);
+            }
+        }
+        if (chunk > 0) fetch(chunk - 1, half ^ 1);
+        if (!in_v) continue;
+
+        {
+            float* to = a.adjoints + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K + 4 * g;
+#pragma unroll
+            for (int m = 0; m < KM; ++m)
+                if (16 * m < K) *reinterpret_cast<f32x4*>(to + 16 * m) = L[m];
         }
         // du = D (L k) + Pᵀ dy
-        f32x4 X[CT][4] = {};
+        f32x4 Y[4] = {};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            Planes<3> lt[CT];
+            const Planes<3> lt = split<3>(L[2 * s], L[2 * s + 1]);
 #pragma unroll
-            for (int t = 0; t < CT; ++t) lt[t] = split<3>(L[t][2 * s], L[t][2 * s + 1]);
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                const Planes<PL> kf = read_tile<Rows, PL>(lds_k, 16 * rt + c, 4 * s + g);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) X[t][rt] = mma(kf, lt[t], X[t][rt]);
-            }
+            for (int rt = 0; rt < 4; ++rt) Y[rt] = mma(Keys::template rows<PL>(lds_k, rt, s, c, g), lt, Y[rt]);
         }
         f32x4 beta[4];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             beta[rt] = *reinterpret_cast<const f32x4*>(f + kC + 16 * rt + 4 * g);
-            const f32x4 ed = *reinterpret_cast<const f32x4*>(f + 2 * kC + 16 * rt + 4 * g);
-#pragma unroll
-            for (int t = 0; t < CT; ++t) X[t][rt] *= ed;
-        }
-        auto rows_of = [&](int rt, int t) { return f32x4{dy[4 * rt][t], dy[4 * rt + 1][t], dy[4 * rt + 2][t], dy[4 * rt + 3][t]}; };
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            Planes<PL> d[CT];
-#pragma unroll
-            for (int t = 0; t < CT; ++t) d[t] = split<PL>(rows_of(2 * s, t), rows_of(2 * s + 1, t));
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                if (block_of<false>(rt, s) < 0) continue;
-                const Planes<3> pb = load_block<3>(mat + a.at_pt, block_of<false>(rt, s), lane);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) X[t][rt] = mma(pb, d[t], X[t][rt]);
-            }
+            X[rt] += *reinterpret_cast<const f32x4*>(f + 2 * kC + 16 * rt + 4 * g) * Y[rt];
         }
         // Z = du + Nᵀ (beta du)
-        Planes<3> m[CT][2];
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) m[t][s] = split<3>(beta[2 * s] * X[t][2 * s], beta[2 * s + 1] * X[t][2 * s + 1]);
+        const Planes<3> mx[2] = {split<3>(beta[0] * X[0], beta[1] * X[1]), split<3>(beta[2] * X[2], beta[3] * X[3])};
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (block_of<false>(rt, s) < 0) continue;
-                const Planes<3> nb = load_block<3>(mat + a.at_nt, block_of<false>(rt, s), lane);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) X[t][rt] = mma(nb, m[t][s], X[t][rt]);
-            }
-        float* z = a.pulls + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c * CT;
+            for (int s = 0; s < 2; ++s)
+                if (block_of<false>(rt, s) >= 0) X[rt] = mma(load_block<3>(lds_n, block_of<false>(rt, s), lane), mx[s], X[rt]);
+        float* z = a.pulls + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int t = (i >> 2) * 16 + 4 * g + (i & 3);
-            float x[CT], dr[CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                x[j] = X[j][i >> 2][i & 3];
-                dr[j] = x[j] * beta[i >> 2][i & 3];
-                X[j][i >> 2][i & 3] = dr[j];
-            }
-            if (in_v) store_values(z + t * a.V, x);
-            if (t < len && in_v) store_values(dvp + (t0 + t) * v_stride + c * CT, dr);
+            const float x = X[i >> 2][i & 3], dr = x * beta[i >> 2][i & 3];
+            X[i >> 2][i & 3] = dr;
+            z[t * a.V] = x;
+            if (t < len) store_act(dvp, (chunk * kC + t) * v_stride, dr);
         }
         // the adjoint of the state before the chunk
         const float last = f[4 * kC];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int i = 0; i < KP / 16; ++i) L[t][i] *= last;
+        for (int i = 0; i < KM; ++i) L[i] *= last;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             f32x4 ek[2], eq[2];
@@ -182,31 +180,18 @@ __global__ __launch_bounds__(256) void gdr_adjoint_kernel(AdjointArgs a) {
                 ek[i] = -*reinterpret_cast<const f32x4*>(f + 32 * s + 16 * i + 4 * g);
                 eq[i] = *reinterpret_cast<const f32x4*>(f + 3 * kC + 32 * s + 16 * i + 4 * g);
             }
-            Planes<3> dr[CT], dq[CT];
+            const Planes<3> dr = split<3>(ek[0] * X[2 * s], ek[1] * X[2 * s + 1]);
+            const Planes<3> dq = split<3>(eq[0] * dy[2 * s], eq[1] * dy[2 * s + 1]);
 #pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                dr[t] = split<3>(ek[0] * X[t][2 * s], ek[1] * X[t][2 * s + 1]);
-                dq[t] = split<3>(eq[0] * rows_of(2 * s, t), eq[1] * rows_of(2 * s + 1, t));
-            }
+            for (int i = 0; i < KM; ++i) L[i] = mma(Keys::template columns<PL>(lds_q, i, s, c, g), dq, L[i]);
 #pragma unroll
-            for (int i = 0; i < KP / 16; ++i) {
-                const Planes<PL> kt = read_tile<Columns, PL>(lds_kt, 16 * i + c, 4 * s + g);
-                const Planes<PL> qt = read_tile<Columns, PL>(lds_qt, 16 * i + c, 4 * s + g);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    L[t][i] = mma(kt, dr[t], L[t][i]);
-                    L[t][i] = mma(qt, dq[t], L[t][i]);
-                }
-            }
+            for (int i = 0; i < KM; ++i) L[i] = mma(Keys::template columns<PL>(lds_k, i, s, c, g), dr, L[i]);
         }
     }
     if (a.dh0 && in_v) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int m = 0; m < KP / 16; ++m)
-                if (16 * m < a.K)
-                    *reinterpret_cast<f32x4*>(a.dh0 + ((n * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g) = L[t][m];
+        for (int m = 0; m < KM; ++m)
+            if (16 * m < K) *reinterpret_cast<f32x4*>(a.dh0 + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g) = L[m];
     }
 }
 
@@ -232,6 +217,12 @@ template <int KP>
 struct StateTile {
     static constexpr int kBytes = KP * 64;
     __device__ static __forceinline__ int at(int column, int piece) { return column * 64 + ((piece ^ ((column >> 1) & 3)) * 16); }
+    __device__ static __forceinline__ Planes<3> read(const uint8_t* lds, int column, int piece) {
+        Planes<3> out;
+#pragma unroll
+        for (int n = 0; n < 3; ++n) out.p[n] = *reinterpret_cast<const u32x4*>(lds + n * kBytes + at(column, piece));
+        return out;
+    }
 };
 
 __device__ __forceinline__ f32x4 load_four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -256,14 +247,14 @@ __device__ __forceinline__ float group4_sum(float v) {  // over the lanes l, l ^
 template <typename T, int KP>
 __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     constexpr int PL = kPlanes<T>, KM = KP / 16;
-    typedef ColumnTile<KP> Columns;
+    typedef Tile<KP> Keys;
     typedef StateTile<KP> State;
-    constexpr int kMatrix = kC * kPitch * 4, kKeys = 2 * PL * Columns::kBytes, kStates = 6 * State::kBytes;
-    __shared__ __align__(16) uint8_t lds[kKeys + 2 * kMatrix > kStates ? kKeys + 2 * kMatrix : kStates];
+    constexpr int kMatrix = kC * kPitch * 4, kKeys = 2 * PL * Keys::kBytes, kStates = 6 * State::kBytes;
+    __shared__ __align__(16) uint8_t lds[kKeys + (2 * kMatrix > kStates ? 2 * kMatrix : kStates)];
     __shared__ float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[kC], s_end[8];
-    uint8_t *lds_s = lds, *lds_l = lds + 3 * State::kBytes;              // while summing over value elements
-    uint8_t *lds_kt = lds, *lds_qt = lds + PL * Columns::kBytes;         // then
-    float *sX = reinterpret_cast<float*>(lds + kKeys), *sM = sX + kC * kPitch;
+    uint8_t *lds_k = lds, *lds_q = lds + PL * Keys::kBytes;
+    uint8_t *lds_s = lds + kKeys, *lds_l = lds_s + 3 * State::kBytes;             // while summing over value elements
+    float *sX = reinterpret_cast<float*>(lds + kKeys), *sM = sX + kC * kPitch;  // then
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const int64_t hg = blockIdx.x % a.G, slot = a.slot0 + blockIdx.x / a.G;
     const Chunk ch = chunk_of(a.offsets, slot, a.T, a.N);
@@ -291,6 +282,17 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     }
     if (g == 0) s_rk[row] = rk, s_rq[row] = rq;
 
+    if constexpr (sizeof(T) == 2) {
+        rows_to_lds<KP, 4>(lds_offset(lds_k), kp, static_cast<uint32_t>(qk_stride), ch.len, K, w, lane);
+        rows_to_lds<KP, 4>(lds_offset(lds_q), qp, static_cast<uint32_t>(qk_stride), ch.len, K, w, lane);
+        tile_barrier();
+    } else {
+        FloatRows<KP, 256> rows;
+        rows.load(kp, qk_stride, ch.len, K, tid);
+        rows.store(lds_k, tid);
+        rows.load(qp, qk_stride, ch.len, K, tid);
+        rows.store(lds_q, tid);
+    }
     f32x4 dq_sum[KM] = {}, dk_sum[KM] = {};
     const int per = static_cast<int>(a.H / a.G);
     for (int hh = 0; hh < per; ++hh) {
@@ -303,9 +305,6 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             s_lo[lane] = static_cast<float>(b - hi);
             s_beta[lane] = lane < ch.len ? a.beta[(ch.start + lane) * a.H + h] : 0.0f;
         }
-        Patch<T, KP> pk, pq;
-        pk.load(kp, qk_stride, ch.len, K, tid);
-        pq.load(qp, qk_stride, ch.len, K, tid);
         const float *S = a.states + cell * a.V * a.K, *L = a.adjoints + cell * a.V * a.K;
         const float *e = a.misses + cell * kC * a.V, *z = a.pulls + cell * kC * a.V;
         const T* dy = static_cast<const T*>(a.dy) + ch.start * v_stride + h * a.V;
@@ -357,7 +356,7 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             const Planes<3> zf = split<3>(zz), uf = split<3>(x);
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
-                const Planes<3> sf = read_tile<State, 3>(lds_s, 16 * m + c, g), lf = read_tile<State, 3>(lds_l, 16 * m + c, g);
+                const Planes<3> sf = State::read(lds_s, 16 * m + c, g), lf = State::read(lds_l, 16 * m + c, g);
                 yS[m] = mma(sf, dyf, yS[m]);
                 zS[m] = mma(sf, zf, zS[m]);
                 uL[m] = mma(lf, uf, uL[m]);
@@ -376,8 +375,6 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             }
         }
         __syncthreads();
-        pk.store(nullptr, lds_kt, tid);
-        pq.store(nullptr, lds_qt, tid);
 #pragma unroll
         for (int jb = 0; jb < 4; ++jb) {
             const int j = 16 * jb + c;
@@ -434,8 +431,8 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             const Planes<3> xrf = split<3>(xr), mrf = split<3>(mr), xcf = split<3>(xc), mcf = split<3>(mc);
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
-                const Planes<PL> kt = read_tile<Columns, PL>(lds_kt, 16 * m + c, 4 * s + g);
-                const Planes<PL> qt = read_tile<Columns, PL>(lds_qt, 16 * m + c, 4 * s + g);
+                const Planes<PL> kt = Keys::template columns<PL>(lds_k, m, s, c, g);
+                const Planes<PL> qt = Keys::template columns<PL>(lds_q, m, s, c, g);
                 dq[m] = mma(kt, xrf, dq[m]);
                 dkr[m] = mma(kt, mrf, dkr[m]);
                 dkc[m] = mma(kt, mcf, dkc[m]);
@@ -495,13 +492,13 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     }
 }
 
-template <typename T, int KP, int CT>
+template <typename T, int KP, int NW>
 hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
     const GdrLayout l(a.dtype, true);
-    const int64_t parts = (a.V + 64 * CT - 1) / (64 * CT);
+    const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const AdjointArgs k{a.q, a.k, a.dy, a.offsets, a.mats, a.dh_final, a.dv, a.dh0, a.adjoints, a.pulls,
                         a.T, a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.factors, l.nt, l.pt};
-    gdr_adjoint_kernel<T, KP, CT><<<static_cast<uint32_t>(a.N * a.H * parts), 256, 0, s>>>(k);
+    gdr_adjoint_kernel<T, KP, NW><<<static_cast<uint32_t>(a.N * a.H * parts), NW * 64, 0, s>>>(k);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const GradArgs d{a.q, a.k, a.dy, a.g, a.beta, a.offsets, a.states, a.misses, a.adjoints, a.pulls, a.dq, a.dk, a.dg, a.dbeta,
@@ -511,10 +508,7 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
 }
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
-    if constexpr (sizeof(T) == 2 || KP == 64) {  // float32 planes of 128 columns leave no registers for a second tile
-        if (a.N * a.H >= 128 && a.V > 64) return launch_c<T, KP, 2>(a, s);
-    }
-    return launch_c<T, KP, 1>(a, s);
+    return a.V > 64 && a.N * a.H >= 128 ? launch_c<T, KP, 8>(a, s) : launch_c<T, KP, 4>(a, s);
 }
 template <typename T>
 hipError_t launch_t(const GdrArgs& a, hipStream_t s) {

@@ -217,107 +217,105 @@ __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_
     return expf((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-// ---- a chunk's q and k in LDS ---------------------------------------------------
+// ---- a chunk's rows in LDS --------------------------------------------------------
 
-// 64 rows of a tensor (tokens) of up to KP columns, as planes in LDS, by rows (for
-// products summed over the columns) or by columns (summed over the tokens), in
-// the folded order of what is summed over.  A lane's operand is one 16-byte piece
-// of a row; piece c of row r lies at place c ^ (r, or r / 2 where a row is 128
-// bytes), so that the 16 rows that a read takes at once spread over the banks.
-template <int KP>
-struct RowTile {
-    static constexpr int kRow = KP * 2, kBytes = kC * kRow;
-    static constexpr int kMask = KP / 8 - 1;
-    __device__ static __forceinline__ int at(int row, int piece) {
-        return row * kRow + ((piece ^ ((KP == 64 ? row >> 1 : row) & kMask)) * 16);
+// 64 rows (tokens) of W columns, as bfloat16 planes.  A row's 16-byte pieces are
+// exchanged among themselves by the row's number, so that the 16 rows that a read
+// takes at once spread over the banks.  Read as operands in the folded order of
+// what is summed over: by rows (summed over the columns) in two 8-byte reads, by
+// columns (summed over the tokens) in two transposing reads: sixteen lanes read
+// four rows of 16 values, 8 bytes a lane, and each gets a column's four.
+template <int W>
+struct Tile {
+    static constexpr int kRow = W * 2, kBytes = kC * kRow, kPieces = W / 8;
+    static_assert(kPieces == 8 || kPieces == 16, "rows of 128 or 256 bytes");
+    __device__ static __forceinline__ int turn(int row) { return kPieces == 16 ? row & 15 : (row >> 1) & 7; }
+    __device__ static __forceinline__ int at(int row, int piece) { return row * kRow + ((piece ^ turn(row)) * 16); }
+
+    template <int N>
+    __device__ static __forceinline__ Planes<N> rows(const uint8_t* lds, int rt, int s, int c, int g) {
+        const uint8_t* p = lds + (g & 1) * 8;
+        const int lo = at(16 * rt + c, 4 * s + (g >> 1)), hi = at(16 * rt + c, 4 * s + 2 + (g >> 1));
+        Planes<N> out;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const u32x2 a = *reinterpret_cast<const u32x2*>(p + n * kBytes + lo), b = *reinterpret_cast<const u32x2*>(p + n * kBytes + hi);
+            out.p[n] = u32x4{a[0], a[1], b[0], b[1]};
+        }
+        return out;
+    }
+    // four rows 16 rt + 4 g .. of column 16 m + c
+    __device__ static __forceinline__ u32x2 four(const uint8_t* lds, int rt, int m, int c, int g) {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        const uint8_t* p = lds + at(16 * rt + 4 * g + (c >> 2), 2 * m + ((c >> 1) & 1)) + (c & 1) * 8;
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(p)));
+    }
+    template <int N>
+    __device__ static __forceinline__ Planes<N> columns(const uint8_t* lds, int m, int s, int c, int g) {
+        Planes<N> out;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const u32x2 a = four(lds + n * kBytes, 2 * s, m, c, g), b = four(lds + n * kBytes, 2 * s + 1, m, c, g);
+            out.p[n] = u32x4{a[0], a[1], b[0], b[1]};
+        }
+        return out;
     }
 };
-template <int KP>
-struct ColumnTile {
-    static constexpr int kRow = kC * 2, kBytes = KP * kRow;
-    __device__ static __forceinline__ int at(int column, int piece) { return column * kRow + ((piece ^ ((column >> 1) & 7)) * 16); }
-};
-template <typename Tile, int N>
-__device__ __forceinline__ Planes<N> read_tile(const uint8_t* lds, int row, int piece) {
-    Planes<N> out;
-#pragma unroll
-    for (int n = 0; n < N; ++n) out.p[n] = *reinterpret_cast<const u32x4*>(lds + n * Tile::kBytes + Tile::at(row, piece));
-    return out;
+
+__device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) const uint8_t*)(p))));
 }
 
-// One thread's share of a tile on its way from memory: 4 tokens of 8 columns.
-// Held as loaded from the loads' issue (load) to the stores to LDS (store).
-template <typename T, int KP>
-struct Patch {
-    static constexpr int kItems = (kC / 4) * (KP / 8);  // 128 or 256 threads have one
-    static constexpr int kWords = sizeof(T) == 2 ? 4 : 8;
-    uint32_t raw[4][kWords];
+// bfloat16 rows from memory straight to a tile, by NW waves; rows from `len` and
+// columns from `width` on become zeros.
+template <int W, int NW>
+__device__ __forceinline__ void rows_to_lds(uint32_t lds, const uint16_t* rows, uint32_t stride, int len, int width, int w, int lane) {
+    constexpr int kPieces = Tile<W>::kPieces, kRows = 64 / kPieces;  // rows of one instruction
+    const i32x4 rsrc = buffer_words(rows, 0x7ffffff0u);
+#pragma unroll
+    for (int i = 0; i < kC / kRows / NW; ++i) {
+        const int first = (i * NW + w) * kRows, row = first + lane / kPieces, piece = lane % kPieces ^ Tile<W>::turn(row);
+        const uint32_t at = row < len && piece * 8 < width ? row * stride + piece * 8 : 0x3fffffffu;
+        load_to_lds(lds + first * Tile<W>::kRow, rsrc, at * 2, 0);
+    }
+}
+// `bytes` (a multiple of 16) from memory straight to LDS, by NW waves.
+template <int NW, int bytes>
+__device__ __forceinline__ void bytes_to_lds(uint32_t lds, const uint8_t* from, int w, int lane) {
+    const i32x4 rsrc = buffer_words(from, bytes);
+#pragma unroll
+    for (int i = 0; i < (bytes + 1024 * NW - 1) / (1024 * NW); ++i) {
+        const int at = (i * NW + w) * 1024;
+        if (at + 1024 <= bytes) load_to_lds(lds + at, rsrc, at + lane * 16, 0);
+        else if (at + lane * 16 < bytes) load_to_lds(lds + at, rsrc, at + lane * 16, 0);  // the lanes of the last piece
+    }
+}
 
-    __device__ static __forceinline__ int quad(int item) { return item % 16; }   // tokens 4 quad ..
-    __device__ static __forceinline__ int octet(int item) { return item / 16; }  // columns 8 octet ..
-
-    // rows: the chunk's first token's row; stride: elements from a token to the next
-    __device__ __forceinline__ void load(const T* rows, int64_t stride, int len, int K, int item) {
-        const int t0 = quad(item) * 4, k0 = octet(item) * 8;
+// float32 rows on their way to a tile's planes: a thread's pieces, held from the loads' issue to the stores.
+template <int W, int THREADS>
+struct FloatRows {
+    static constexpr int kItems = kC * (W / 8) / THREADS;
+    f32x4 lo[kItems], hi[kItems];
+    __device__ __forceinline__ void load(const float* rows, int64_t stride, int len, int width, int tid) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const bool in = item < kItems && t0 + t < len && k0 < K;
-            const u32x4* p = reinterpret_cast<const u32x4*>(rows + (t0 + t) * stride + k0);
-#pragma unroll
-            for (int w = 0; w < kWords; w += 4) {
-                const u32x4 v = in ? p[w / 4] : u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) raw[t][w + i] = v[i];
-            }
+        for (int i = 0; i < kItems; ++i) {
+            const int item = i * THREADS + tid, row = item / (W / 8), piece = item % (W / 8);
+            const bool in = row < len && piece * 8 < width;
+            const float* p = rows + row * stride + piece * 8;
+            const f32x4 zero = {0, 0, 0, 0};
+            lo[i] = in ? *reinterpret_cast<const f32x4*>(p) : zero;
+            hi[i] = in ? *reinterpret_cast<const f32x4*>(p + 4) : zero;
         }
     }
-    // plane n of token t: 4 words of column pairs
-    __device__ __forceinline__ void plane(int n, uint32_t (&out)[4][4]) {
+    __device__ __forceinline__ void store(uint8_t* lds, int tid) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int i = 0; i < kItems; ++i) {
+            const int item = i * THREADS + tid, row = item / (W / 8), piece = item % (W / 8);
+            const Planes<3> p = split<3>(lo[i], hi[i]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 2) {
-                    out[t][i] = raw[t][i];
-                } else {
-                    float a = __uint_as_float(raw[t][2 * i]), b = __uint_as_float(raw[t][2 * i + 1]);
-                    out[t][i] = upper_halves(a, b);
-                    raw[t][2 * i] = __float_as_uint(a - upper_part(a));
-                    raw[t][2 * i + 1] = __float_as_uint(b - upper_part(b));
-                }
-            }
-    }
-    // to the tile by rows and / or by columns (null: not); leaves nothing to store again
-    __device__ __forceinline__ void store(uint8_t* by_row, uint8_t* by_column, int item) {
-        if (item >= kItems) return;
-        const int t0 = quad(item) * 4, o = octet(item);
-#pragma unroll
-        for (int n = 0; n < kPlanes<T>; ++n) {
-            uint32_t x[4][4];
-            plane(n, x);
-            if (by_row) {
-                uint8_t* lds = by_row + n * RowTile<KP>::kBytes;
-                // columns 8 o .. 8 o + 7 of 32 are two quads: slots of groups g and g + 1, lower or upper half
-                const int piece = (o / 4) * 4 + (o % 2) * 2, half = (o % 4) / 2 * 8;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    *reinterpret_cast<u32x2*>(lds + RowTile<KP>::at(t0 + t, piece) + half) = u32x2{x[t][0], x[t][1]};
-                    *reinterpret_cast<u32x2*>(lds + RowTile<KP>::at(t0 + t, piece + 1) + half) = u32x2{x[t][2], x[t][3]};
-                }
-            }
-            if (by_column) {
-                uint8_t* lds = by_column + n * ColumnTile<KP>::kBytes;
-                const int q = quad(item), piece = (q / 8) * 4 + q % 4, half = (q % 8) / 4 * 8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo01 = __builtin_amdgcn_perm(x[1][i], x[0][i], 0x05040100u),
-                                   lo23 = __builtin_amdgcn_perm(x[3][i], x[2][i], 0x05040100u),
-                                   hi01 = __builtin_amdgcn_perm(x[1][i], x[0][i], 0x07060302u),
-                                   hi23 = __builtin_amdgcn_perm(x[3][i], x[2][i], 0x07060302u);
-                    *reinterpret_cast<u32x2*>(lds + ColumnTile<KP>::at(o * 8 + 2 * i, piece) + half) = u32x2{lo01, lo23};
-                    *reinterpret_cast<u32x2*>(lds + ColumnTile<KP>::at(o * 8 + 2 * i + 1, piece) + half) = u32x2{hi01, hi23};
-                }
-            }
+            for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x4*>(lds + n * Tile<W>::kBytes + Tile<W>::at(row, piece)) = p.p[n];
         }
     }
 };

@@ -27,213 +27,193 @@ struct FwdArgs {
     int64_t mat_bytes, at_n, at_p, at_f;
 };
 
-// CT: tiles of 16 columns a wave.  Column l % 16 of tile t is value element CT (l % 16) + t of
-// the wave's 16 CT, so that a lane's columns (and its rows of the transposed y) are neighbours.
-template <typename T, int KP, int CT, bool TRAIN>
-__global__ __launch_bounds__(256) void gdr_fwd_kernel(FwdArgs a) {
-    constexpr int PL = kPlanes<T>, PP = sizeof(T) == 2 ? 2 : 3, KS = KP / 32;
-    typedef RowTile<KP> Rows;
-    typedef ColumnTile<KP> Columns;
-    __shared__ __align__(16) uint8_t lds[PL * (2 * Rows::kBytes + Columns::kBytes)];
-    uint8_t *lds_k = lds, *lds_q = lds_k + PL * Rows::kBytes, *lds_kt = lds_q + PL * Rows::kBytes;
+// NW waves with a tile of 16 columns each.  While a chunk is worked on, the next
+// one's rows and matrices come in: bfloat16 straight into the other half of LDS,
+// one barrier a chunk; float32 through registers, where it is cut into planes,
+// with P from memory (the L2, mostly) as the planes leave no room for it.
+template <typename T, int KP, int NW, bool TRAIN>
+__global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
+    constexpr bool B16 = sizeof(T) == 2;
+    constexpr int PL = kPlanes<T>, PP = B16 ? 2 : 3, KS = KP / 32, KM = KP / 16, VC = NW * 16;
+    typedef Tile<KP> Keys;
+    typedef Tile<VC> Values;
+    constexpr int kPm = PP * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
+    constexpr int kMats = (B16 ? kPm : 0) + kN + kF;
+    constexpr int kKeys = 2 * PL * Keys::kBytes;
+    constexpr int kPart = B16 ? kKeys + Values::kBytes + kMats : kMats;  // of what LDS holds twice
+    __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
+    static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const int64_t part = blockIdx.x % a.parts, head = blockIdx.x / a.parts, h = head % a.H, n = head / a.H;
     const int64_t hg = h / (a.H / a.G);
-    const int64_t v0 = (part * 4 + w) * 16 * CT;  // the wave's first value element
-    const bool in_v = v0 + c * CT < a.V;          // this lane's columns
+    const int64_t vw = part * VC, v0 = vw + w * 16;  // the workgroup's first value element, and the wave's
+    const bool in_v = v0 < a.V;                      // V is a multiple of 16
     const Span sp = span_of(a.offsets, n, a.T, a.N);
     const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
+    const int K = static_cast<int>(a.K);
 
-    f32x4 S[CT][KP / 16];
+    f32x4 S[KM];
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int m = 0; m < KP / 16; ++m) {
-            S[t][m] = f32x4{0, 0, 0, 0};
-            if (a.h0 && in_v && 16 * m < a.K)
-                S[t][m] = *reinterpret_cast<const f32x4*>(a.h0 + ((n * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g);
-        }
+    for (int m = 0; m < KM; ++m) {
+        S[m] = f32x4{0, 0, 0, 0};
+        if (a.h0 && in_v && 16 * m < K) S[m] = *reinterpret_cast<const f32x4*>(a.h0 + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g);
+    }
 
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
     const T* kp = static_cast<const T*>(a.k) + sp.start * qk_stride + hg * a.K;
     const T* qp = static_cast<const T*>(a.q) + sp.start * qk_stride + hg * a.K;
-    const T* vp = static_cast<const T*>(a.v) + sp.start * v_stride + h * a.V + v0;
-    T* yp = static_cast<T*>(a.y) + sp.start * v_stride + h * a.V + v0;
-    Patch<T, KP> pk, pq;
-    auto fetch = [&](int64_t chunk) {
-        const int len = static_cast<int>(imin64(kC, sp.len - chunk * kC));
-        pk.load(kp + chunk * kC * qk_stride, qk_stride, len, static_cast<int>(a.K), tid);
-        pq.load(qp + chunk * kC * qk_stride, qk_stride, len, static_cast<int>(a.K), tid);
+    const T* vp = static_cast<const T*>(a.v) + sp.start * v_stride + h * a.V;
+    T* yp = static_cast<T*>(a.y) + sp.start * v_stride + h * a.V + v0 + 4 * g;
+    auto length = [&](int64_t chunk) { return static_cast<int>(imin64(kC, sp.len - chunk * kC)); };
+    auto mats_of = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes; };
+    FloatRows<KP, NW * 64> fk, fq;
+    auto fetch = [&](int64_t chunk, int half) {
+        const int len = length(chunk);
+        uint8_t* to = lds + half * kPart;
+        if constexpr (B16) {
+            rows_to_lds<KP, NW>(lds_offset(to), kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
+            rows_to_lds<KP, NW>(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
+            rows_to_lds<VC, NW>(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, static_cast<uint32_t>(v_stride), len,
+                                static_cast<int>(a.V - vw), w, lane);
+            bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_p, w, lane);
+        } else {
+            bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_n, w, lane);
+            fk.load(kp + chunk * kC * qk_stride, qk_stride, len, K, tid);
+            fq.load(qp + chunk * kC * qk_stride, qk_stride, len, K, tid);
+        }
     };
-    if (chunks) fetch(0);
+    f32x4 O[4];
+    auto put_y = [&](int64_t chunk) {  // row 4 g + r: value elements; column c of tile rt: token 16 rt + c
+        if (!a.y || !in_v) return;
+        const int len = length(chunk);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const float out[4] = {O[rt][0], O[rt][1], O[rt][2], O[rt][3]};
+            if (16 * rt + c < len) store_row(yp + (chunk * kC + 16 * rt + c) * v_stride, out);
+        }
+    };
+    if (chunks) fetch(0, 0);
     for (int64_t chunk = 0; chunk < chunks; ++chunk) {
-        const int len = static_cast<int>(imin64(kC, sp.len - chunk * kC));
-        const uint8_t* mat = a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes;
-        const float* f = reinterpret_cast<const float*>(mat + a.at_f);
-        const int64_t t0 = chunk * kC;
-        __syncthreads();  // the chunk before is done with
-        pk.store(lds_k, lds_kt, tid);
-        pq.store(lds_q, nullptr, tid);
-        __syncthreads();
-        if (chunk + 1 < chunks) fetch(chunk + 1);
-        if (v0 >= a.V) continue;  // only helps with the loads
-
-        float val[16][CT];  // item 4 rt + r: token 16 rt + 4 g + r
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = (i >> 2) * 16 + 4 * g + (i & 3);
-#pragma unroll
-            for (int j = 0; j < CT; ++j) val[i][j] = 0.0f;
-            if (t < len && in_v) load_values(vp + (t0 + t) * v_stride + c * CT, val[i]);
+        const int half = static_cast<int>(chunk & 1), len = length(chunk);
+        const uint8_t* in = lds + half * kPart;
+        const uint8_t *lds_k = B16 ? in : lds + 2 * kPart, *lds_q = lds_k + PL * Keys::kBytes, *lds_v = in + kKeys;
+        const uint8_t* lds_p = in + kKeys + (B16 ? Values::kBytes : 0);
+        const uint8_t* lds_n = B16 ? lds_p + kPm : in;
+        const float* f = reinterpret_cast<const float*>(lds_n + kN);
+        tile_barrier();  // this half is whole, nobody reads the other one
+        if constexpr (!B16) {
+            fk.store(lds + 2 * kPart, tid);
+            fq.store(lds + 2 * kPart + PL * Keys::kBytes, tid);
+            __syncthreads();
         }
-        if constexpr (TRAIN) {
-            if (in_v) {
-#pragma unroll
-                for (int t = 0; t < CT; ++t)
-#pragma unroll
-                    for (int m = 0; m < KP / 16; ++m)
-                        if (16 * m < a.K)
-                            *reinterpret_cast<f32x4*>(a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g) = S[t][m];
-            }
-        }
+        if (chunk) put_y(chunk - 1);  // here, not when it was ready: the barrier waits for stores too
+        if (chunk + 1 < chunks) fetch(chunk + 1, half ^ 1);
+        if (!in_v) continue;
 
-        // S k (tokens in the rows) and S q (tokens in the columns)
-        f32x4 X[CT][4] = {}, O[CT][4] = {};
+        f32x4 val[4];  // item r of tile rt: token 16 rt + 4 g + r of this lane's column
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            Planes<3> st[CT];
+        for (int rt = 0; rt < 4; ++rt) {
+            if constexpr (B16) {
+                const u32x2 x = Values::four(lds_v, rt, w, c, g);
+                val[rt] = f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
+            } else {
 #pragma unroll
-            for (int t = 0; t < CT; ++t) st[t] = split<3>(S[t][2 * s], S[t][2 * s + 1]);
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                const Planes<PL> kf = read_tile<Rows, PL>(lds_k, 16 * rt + c, 4 * s + g);
-                const Planes<PL> qf = read_tile<Rows, PL>(lds_q, 16 * rt + c, 4 * s + g);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    X[t][rt] = mma(kf, st[t], X[t][rt]);
-                    Planes<PP> so;
-#pragma unroll
-                    for (int i = 0; i < PP; ++i) so.p[i] = st[t].p[i];
-                    O[t][rt] = mma(so, qf, O[t][rt]);
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * rt + 4 * g + r;
+                    val[rt][r] = t < len ? vp[(chunk * kC + t) * v_stride + v0 + c] : 0.0f;
                 }
             }
         }
+        if constexpr (TRAIN) {
+            float* to = a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K + 4 * g;
+#pragma unroll
+            for (int m = 0; m < KM; ++m)
+                if (16 * m < K) *reinterpret_cast<f32x4*>(to + 16 * m) = S[m];
+        }
+        // S k (tokens in the rows) and S q (tokens in the columns)
+        f32x4 X[4] = {};
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) O[rt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const Planes<3> st = split<3>(S[2 * s], S[2 * s + 1]);
+            Planes<PP> so;
+#pragma unroll
+            for (int i = 0; i < PP; ++i) so.p[i] = st.p[i];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) X[rt] = mma(Keys::template rows<PL>(lds_k, rt, s, c, g), st, X[rt]);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) O[rt] = mma(so, Keys::template rows<PL>(lds_q, rt, s, c, g), O[rt]);
+        }
         // e = r + N (beta r)
         f32x4 beta[4];
-        Planes<3> m[CT][2];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             const f32x4 ek = *reinterpret_cast<const f32x4*>(f + 16 * rt + 4 * g);
             beta[rt] = *reinterpret_cast<const f32x4*>(f + kC + 16 * rt + 4 * g);
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) X[t][rt][r] = __builtin_fmaf(-ek[r], X[t][rt][r], val[4 * rt + r][t]);
+            X[rt] = val[rt] - ek * X[rt];
         }
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) m[t][s] = split<3>(beta[2 * s] * X[t][2 * s], beta[2 * s + 1] * X[t][2 * s + 1]);
+        const Planes<3> mx[2] = {split<3>(beta[0] * X[0], beta[1] * X[1]), split<3>(beta[2] * X[2], beta[3] * X[3])};
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (block_of<true>(rt, s) < 0) continue;
-                const Planes<3> nb = load_block<3>(mat + a.at_n, block_of<true>(rt, s), lane);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) X[t][rt] = mma(nb, m[t][s], X[t][rt]);
-            }
+            for (int s = 0; s < 2; ++s)
+                if (block_of<true>(rt, s) >= 0) X[rt] = mma(load_block<3>(lds_n, block_of<true>(rt, s), lane), mx[s], X[rt]);
         if constexpr (TRAIN) {
-            float* e = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c * CT;
-            if (in_v) {
+            float* e = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float x[CT];
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) x[t] = X[t][i >> 2][i & 3];
-                    store_values(e + ((i >> 2) * 16 + 4 * g + (i & 3)) * a.V, x);
-                }
-            }
+            for (int i = 0; i < 16; ++i) e[((i >> 2) * 16 + 4 * g + (i & 3)) * a.V] = X[i >> 2][i & 3];
         }
         // y = scale exp(b) S q + P u, and the state's update
-        const float last = f[4 * kC];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const float eq = f[3 * kC + 16 * rt + c];
-#pragma unroll
-            for (int t = 0; t < CT; ++t) O[t][rt] *= eq, X[t][rt] *= beta[rt];  // X: u
+            O[rt] *= f[3 * kC + 16 * rt + c];
+            X[rt] *= beta[rt];  // u
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            Planes<PP> u[CT];
+            const Planes<PP> u = split<PP>(X[2 * s], X[2 * s + 1]);
 #pragma unroll
-            for (int t = 0; t < CT; ++t) u[t] = split<PP>(X[t][2 * s], X[t][2 * s + 1]);
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                if (block_of<true>(rt, s) < 0) continue;
-                const Planes<PP> pb = load_block<PP>(mat + a.at_p, block_of<true>(rt, s), lane);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) O[t][rt] = mma(u[t], pb, O[t][rt]);
-            }
+            for (int rt = 0; rt < 4; ++rt)
+                if (block_of<true>(rt, s) >= 0)
+                    O[rt] = mma(u, load_block<PP>(B16 ? lds_p : mats_of(chunk) + a.at_p, block_of<true>(rt, s), lane), O[rt]);
         }
+        const float last = f[4 * kC];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int i = 0; i < KP / 16; ++i) S[t][i] *= last;
+        for (int i = 0; i < KM; ++i) S[i] *= last;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const f32x4 d0 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 4 * g),
                         d1 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 16 + 4 * g);
-            Planes<3> u[CT];
+            const Planes<3> u = split<3>(d0 * X[2 * s], d1 * X[2 * s + 1]);
 #pragma unroll
-            for (int t = 0; t < CT; ++t) u[t] = split<3>(d0 * X[t][2 * s], d1 * X[t][2 * s + 1]);
-#pragma unroll
-            for (int i = 0; i < KP / 16; ++i) {
-                const Planes<PL> kt = read_tile<Columns, PL>(lds_kt, 16 * i + c, 4 * s + g);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) S[t][i] = mma(kt, u[t], S[t][i]);
-            }
-        }
-        // row 4 g + r of tile t, column (token) 16 rt + c: value elements v0 + CT (4 g + r) + t
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            float out[4 * CT];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int t = 0; t < CT; ++t) out[r * CT + t] = O[t][rt][r];
-            if (a.y && 16 * rt + c < len && v0 + 4 * CT * g < a.V) store_row(yp + (t0 + 16 * rt + c) * v_stride + 4 * CT * g, out);
+            for (int i = 0; i < KM; ++i) S[i] = mma(Keys::template columns<PL>(lds_k, i, s, c, g), u, S[i]);
         }
     }
+    if (chunks) put_y(chunks - 1);
     if (a.h_final && in_v) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int m = 0; m < KP / 16; ++m)
-                if (16 * m < a.K)
-                    *reinterpret_cast<f32x4*>(a.h_final + ((n * a.H + h) * a.V + v0 + c * CT + t) * a.K + 16 * m + 4 * g) = S[t][m];
+        for (int m = 0; m < KM; ++m)
+            if (16 * m < K) *reinterpret_cast<f32x4*>(a.h_final + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g) = S[m];
     }
 }
 
-template <typename T, int KP, int CT, bool TRAIN>
+template <typename T, int KP, int NW, bool TRAIN>
 hipError_t launch_v(const GdrArgs& a, hipStream_t s) {
     const GdrLayout l(a.dtype, a.train);
-    const int64_t parts = (a.V + 64 * CT - 1) / (64 * CT);
+    const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const FwdArgs k{a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
                     a.T, a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors};
-    gdr_fwd_kernel<T, KP, CT, TRAIN><<<static_cast<uint32_t>(a.N * a.H * parts), 256, 0, s>>>(k);
+    gdr_fwd_kernel<T, KP, NW, TRAIN><<<static_cast<uint32_t>(a.N * a.H * parts), NW * 64, 0, s>>>(k);
     return hipGetLastError();
 }
-template <typename T, int KP, int CT>
+template <typename T, int KP, int NW>
 hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
-    return a.train ? launch_v<T, KP, CT, true>(a, s) : launch_v<T, KP, CT, false>(a, s);
+    return a.train ? launch_v<T, KP, NW, true>(a, s) : launch_v<T, KP, NW, false>(a, s);
 }
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
-    if constexpr (sizeof(T) == 2 || KP == 64) {  // float32 planes of 128 columns leave no registers for a second tile
-        if (a.N * a.H >= 128 && a.V > 64) return launch_c<T, KP, 2>(a, s);
-    }
-    return launch_c<T, KP, 1>(a, s);
+    return a.V > 64 && a.N * a.H >= 128 ? launch_c<T, KP, 8>(a, s) : launch_c<T, KP, 4>(a, s);
 }
 template <typename T>
 hipError_t launch_t(const GdrArgs& a, hipStream_t s) {

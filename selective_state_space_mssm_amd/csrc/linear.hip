@@ -289,30 +289,6 @@ __device__ __forceinline__ u32x4 load_end(const Slab& s, uint32_t row, uint32_t 
 
 // ---- the tile kernel ---------------------------------------------------------
 
-// Four words of a raw buffer descriptor over [base, base + bytes) in scalar registers.
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ i32x4 buffer_words(const uint8_t* base, uint32_t bytes) {
-    const uint64_t p = reinterpret_cast<uint64_t>(uniform_ptr(base));
-    return i32x4{static_cast<int32_t>(p), static_cast<int32_t>((p >> 32) & 0xffff),
-                 static_cast<int32_t>(__builtin_amdgcn_readfirstlane(bytes)), static_cast<int32_t>(kBufferWord3)};
-}
-
-// 16 bytes a lane straight from memory into LDS: lane l's go to lds + 16 l, an
-// offset outside the descriptor's range gives zeros.  Written as one statement
-// without outputs because the compiler orders every LDS read behind every such
-// load it knows of, which would undo the double buffering; the counter wait is
-// in tile_barrier().  (m0 needs one wait state before the load; nothing else in
-// these kernels uses m0, which the compiler keeps reserved.)
-__device__ __forceinline__ void load_to_lds(uint32_t lds, i32x4 rsrc, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
-}
-
-// The tile that was being loaded is in LDS and nobody reads the other one any more.
-__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 // Tile number -> place: tiles are walked in bands of 4 tile rows, so that
 // neighbours in number share 4 + 8 operand slabs of 32 tiles.
 struct TileAt { int64_t m, n; };

@@ -38,12 +38,21 @@ def needed(op: str) -> int:
     return passes + (2 if op.endswith("_f32") else 3)
 
 
+def _adds_to(dst, op, args):
+    """A matrix instruction with the whole result as its addend, which it does not read as an operand: it writes after
+    the result is there, wherever to."""
+    if not op.startswith("v_mfma"):
+        return False
+    parts = [_regs(p) for p in re.split(r",\s*(?![^\[]*\])", args)[:4]]
+    return parts[3:] == [dst] and not any(dst & p for p in parts[1:3])
+
+
 def _interlocked(dst, op, args):
     """A matrix instruction that takes the result as its whole accumulator, and touches it nowhere else in part."""
     if not op.startswith("v_mfma"):
         return False
     parts = [_regs(p) for p in re.split(r",\s*(?![^\[]*\])", args)[:4]]
-    return all(not (dst & p) or (dst == p and i in (0, 3)) for i, p in enumerate(parts))
+    return _adds_to(dst, op, args) or all(not (dst & p) or (dst == p and i == 0) for i, p in enumerate(parts))
 
 
 def _functions(text):
@@ -78,20 +87,24 @@ def check_function(body):
     for i, (op, args) in enumerate(ins):
         if not op.startswith("v_mfma"):
             continue
-        dst = _regs(args.split(",")[0])
-        limit, seen, todo = needed(op), {}, [(i + 1, 0)]
+        dst = frozenset(_regs(args.split(",")[0]))
+        limit, seen, todo = needed(op), {}, [(i + 1, 0, dst)]
         while todo:
-            k, waited = todo.pop()
+            k, waited, dst = todo.pop()
             while k < len(ins) and waited < limit:
-                if seen.get(k, limit) <= waited:
+                if seen.get((k, dst), limit) <= waited:
                     break
-                seen[k] = waited
+                seen[k, dst] = waited
                 o, a = ins[k]
                 if dst & _regs(a) and not _interlocked(dst, o, a):
                     found.append((f"{op} {args}", f"{o} {a}", waited))
                     break
+                if _adds_to(dst, o, a):
+                    dst -= _regs(a.split(",")[0])  # those are its own result from here on
+                    if not dst:
+                        break
                 if o.startswith(("s_cbranch", "s_branch")) and a.split()[-1] in at:
-                    todo.append((at[a.split()[-1]], waited + 1))
+                    todo.append((at[a.split()[-1]], waited + 1, dst))
                 if o in _ENDS:
                     break
                 waited += int(a, 0) + 1 if o == "s_nop" else 1
