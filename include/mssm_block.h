@@ -1,8 +1,8 @@
 /*
  * mssm_block.h -- C ABI of the operators that serve a Mamba block around its
  * scan, in the same library (libmssm.so) as mssm.h: the residual addition with
- * its root-mean-square norm, the projections with their epilogue, and one
- * beam-search step over the logits with the reordering of the recurrent and
+ * its root-mean-square norm, the projections with their epilogue and the low-rank
+ * adapters beside them, and one beam-search step over the logits with the reordering of the recurrent and
  * convolution states.  Forward only: these are the operators of serving.
  *
  * Conventions are those of mssm.h: row-major contiguous tensors, 16-byte
@@ -113,6 +113,45 @@ size_t mssm_linear_workspace_bytes(const mssm_linear_problem* p);
 mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float* x_scale, const void* w,
                         const float* w_scale, const float* bias, const void* residual, void* y,
                         void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: with the
+ * adapter i = index[m] of every row,
+ *
+ *     y[m,n] += scale[i] sum_r (sum_k x[m,k] a[i,r,k]) b[i,n,r]
+ *
+ *   x (rows, in_dim)              in p->dtype: MSSM_F32, MSSM_BF16 or MSSM_F8
+ *   x_scale (rows) float32        required with MSSM_F8 (x[m,k] x_scale[m] in the
+ *                                 place of x[m,k]), NULL otherwise
+ *   a (adapters, rank, in_dim), b (adapters, out_dim, rank)
+ *                                 float32 with MSSM_F32, else bfloat16
+ *   scale (adapters) float32      NULL -> 1
+ *   index (rows) int32            in any order; a row whose index is not in
+ *                                 0 .. adapters - 1 has no adapter: its y stays
+ *   y (rows, out_dim)             in p->out_dtype: MSSM_F32, or MSSM_BF16 (not with
+ *                                 MSSM_F32 operands); read and written in place,
+ *                                 rounded once.  No input's buffer.
+ * The inner sums stay float32 (in the workspace).  Many rows go by tiles, each
+ * computed once for every adapter that its rows name: rows of one adapter are
+ * best neighbours, as the tokens of packed requests are.
+ */
+#define MSSM_MAX_RANK 128
+
+typedef struct {
+    int64_t rows;      /* >= 1, below 2^28 */
+    int64_t in_dim;    /* >= 1, below 2^20 */
+    int64_t out_dim;   /* >= 1, below 2^23 */
+    int64_t rank;      /* 1 .. MSSM_MAX_RANK (else MSSM_ERR_UNSUPPORTED) */
+    int64_t adapters;  /* >= 1, below 2^31 */
+    int32_t dtype;     /* type of x */
+    int32_t out_dtype; /* type of y */
+} mssm_lora_problem;
+
+size_t mssm_lora_workspace_bytes(const mssm_lora_problem* p);
+
+mssm_status mssm_lora(const mssm_lora_problem* p, const void* x, const float* x_scale, const void* a, const void* b,
+                      const float* scale, const int32_t* index, void* y, void* workspace, size_t workspace_bytes,
+                      void* hip_stream);
 
 /*
  * One selection of beam search: of the beams * vocab continuations of every

@@ -23,9 +23,11 @@ MSSM_F8 = 2
 _CODES = {torch.float32: MSSM_F32, torch.bfloat16: MSSM_BF16, torch.float8_e4m3fn: MSSM_F8}
 MAX_BEAMS = 16
 MAX_BEAM_STATES = 16
+MAX_RANK = 128
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 BLOCK_EXPORTS = ["mssm_add_rmsnorm", "mssm_add_rmsnorm_q8", "mssm_linear_workspace_bytes", "mssm_linear",
-                 "mssm_beam_select_workspace_bytes", "mssm_beam_select", "mssm_beam_reorder"]
+                 "mssm_lora_workspace_bytes", "mssm_lora", "mssm_beam_select_workspace_bytes", "mssm_beam_select",
+                 "mssm_beam_reorder"]
 
 
 class NormProblem(ctypes.Structure):
@@ -36,6 +38,12 @@ class NormProblem(ctypes.Structure):
 class LinearProblem(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("in_dim", ctypes.c_int64), ("out_dim", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class LoraProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_dim", ctypes.c_int64), ("out_dim", ctypes.c_int64),
+                ("rank", ctypes.c_int64), ("adapters", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 class BeamProblem(ctypes.Structure):
@@ -55,6 +63,8 @@ def _declare():
             ("mssm_add_rmsnorm_q8", [NP] + [vp] * 7, st),
             ("mssm_linear_workspace_bytes", [LP], sz),
             ("mssm_linear", [LP] + [vp] * 7 + [vp, sz, vp], st),
+            ("mssm_lora_workspace_bytes", [ctypes.POINTER(LoraProblem)], sz),
+            ("mssm_lora", [ctypes.POINTER(LoraProblem)] + [vp] * 7 + [vp, sz, vp], st),
             ("mssm_beam_select_workspace_bytes", [BP], sz),
             ("mssm_beam_select", [BP] + [vp] * 7 + [vp, sz, vp], st),
             ("mssm_beam_reorder", [i64, i64, vp, ctypes.c_int32, ctypes.POINTER(BeamState), vp], st)):
@@ -114,6 +124,12 @@ def _linear_problem(rows, k, n, code, ocode, act, device):
     p = LinearProblem(rows, k, n, code, ocode, act)
     with torch.cuda.device(device):
         return ctypes.byref(p), int(lib.mssm_linear_workspace_bytes(ctypes.byref(p))), p
+
+
+@lru_cache(maxsize=1024)
+def _lora_problem(rows, k, n, rank, adapters, code, ocode):
+    p = LoraProblem(rows, k, n, rank, adapters, code, ocode)
+    return ctypes.byref(p), int(lib.mssm_lora_workspace_bytes(ctypes.byref(p))), p
 
 
 @lru_cache(maxsize=1024)
@@ -240,6 +256,51 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
             return linear(x, w, bias, residual, activation, x_scale, w_scale, out_dtype, y, ws)
     _run(lib.mssm_linear(prob, x.data_ptr(), _ptr(x_scale), w.data_ptr(), _ptr(w_scale), _ptr(bias), _ptr(residual),
                          y.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev)))
+    return y
+
+
+def lora(x, a, b, index, y, scale=None, x_scale=None, workspace=None):
+    """Low-rank adapters beside a shared projection, in place:
+    y[m] += scale[i] (x[m] a[i]ᵀ) b[i]ᵀ with i = index[m], rounded once.
+    x (..., K) float32, bfloat16 or float8_e4m3fn with x_scale (...) float32, one
+    scale a row; a (S, R, K) and b (S, N, R) float32 with float32 x, else
+    bfloat16; index (...) int32 in any order (a row whose index is not in
+    0 .. S - 1 stays as it is); y (..., N) float32, or bfloat16 (not with float32
+    x), as linear() returns it; scale (S) float32.  Returns y.  Forward only: no
+    gradient is recorded."""
+    if x is None or x.dim() < 1 or a is None or a.dim() != 3 or y is None or y.dim() < 1:
+        raise ValueError("x must be (..., K), a (S, R, K) and y (..., N)")
+    act = x.dtype
+    if act not in _CODES:
+        raise TypeError(f"x must be float32, bfloat16 or float8_e4m3fn, got {x.dtype}")
+    lead, K, N = x.shape[:-1], x.shape[-1], y.shape[-1]
+    S, R = a.shape[:2]
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a GPU tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if R > MAX_RANK:
+        raise ValueError(f"rank {R}: at most {MAX_RANK}")
+    weights = torch.float32 if act == torch.float32 else torch.bfloat16
+    _req(a, "a", (S, R, K), weights, dev)
+    _req(b, "b", (S, N, R), weights, dev)
+    _req(index, "index", lead, torch.int32, dev)
+    if y.dtype not in (torch.float32, torch.bfloat16) or (act == torch.float32 and y.dtype != torch.float32):
+        raise TypeError(f"y of {y.dtype} is not available for {act} x")
+    _req(y, "y", (*lead, N), y.dtype, dev)
+    _opt(scale, "scale", (S,), torch.float32, dev)
+    if act == torch.float8_e4m3fn:
+        _req(x_scale, "x_scale", lead, torch.float32, dev)
+    elif x_scale is not None:
+        raise ValueError("x_scale belongs to 8-bit rows")
+    prob, nbytes, _ = _lora_problem(x.numel() // K if K else 0, K, N, R, S, _CODES[act], _CODES[y.dtype])
+    ws = _workspace(nbytes, x.device, workspace)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return lora(x, a, b, index, y, scale, x_scale, ws)
+    _run(lib.mssm_lora(prob, x.data_ptr(), _ptr(x_scale), a.data_ptr(), b.data_ptr(), _ptr(scale), index.data_ptr(),
+                       y.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev)))
     return y
 
 

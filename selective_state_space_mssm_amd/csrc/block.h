@@ -58,4 +58,27 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 hipError_t launch_beam_reorder(int64_t B, int64_t K, const int32_t* parent, int count, const mssm_beam_state* st,
                                hipStream_t s);
 
+// How adapters are computed: rows 1 (each row for itself), or the rows of a tile;
+// `splits` parts of in_dim, `step` long each; the rank padded to whole tiles.
+struct LoraPlan {
+    int rows, splits;
+    int64_t rank, step;
+    size_t ws_bytes;
+};
+LoraPlan plan_lora(int64_t M, int64_t K, int64_t R);
+
+struct LoraArgs {
+    int64_t M, K, N, R, S;
+    int dtype, out_dtype;
+    const void* x;
+    const float* x_scale;  // e4m3 rows only
+    const void* a;
+    const void* b;
+    const float* scale;    // nullable
+    const int32_t* index;
+    void* y;
+    float* inner;          // the workspace
+};
+hipError_t launch_lora(const LoraArgs& a, const LoraPlan& plan, hipStream_t s);
+
 }  // namespace mssm

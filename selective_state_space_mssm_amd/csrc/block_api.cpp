@@ -62,6 +62,19 @@ mssm_status check_beam(const mssm_beam_problem* p) {
     return MSSM_OK;
 }
 
+mssm_status check_lora(const mssm_lora_problem* p) {
+    if (!p) return MSSM_ERR_NULL;
+    if (p->dtype != MSSM_F32 && p->dtype != MSSM_BF16 && p->dtype != MSSM_F8) return MSSM_ERR_DTYPE;
+    if (!f32_or_bf16(p->out_dtype) || (p->dtype == MSSM_F32 && p->out_dtype != MSSM_F32)) return MSSM_ERR_DTYPE;
+    if (p->rows < 1 || p->in_dim < 1 || p->out_dim < 1 || p->rank < 1 || p->adapters < 1) return MSSM_ERR_SHAPE;
+    if (p->rank > MSSM_MAX_RANK) return MSSM_ERR_UNSUPPORTED;
+    // launches: fewer than 2^24 workgroups in a row, 2^16 in a column
+    if (p->rows >= (int64_t{1} << 28) || p->in_dim >= (int64_t{1} << 20) || p->out_dim >= (int64_t{1} << 23) ||
+        p->adapters >= (int64_t{1} << 31))
+        return MSSM_ERR_SHAPE;
+    return MSSM_OK;
+}
+
 mssm_status norm_common(const mssm_norm_problem* p, const void* x, const void* residual, const float* weight, void* y,
                         float* scale, bool q8, void* residual_out, void* hip_stream) {
     mssm_status st = check_norm(p);
@@ -107,6 +120,26 @@ mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float
     const mssm::LinearArgs a{p->rows, p->in_dim, p->out_dim, p->dtype, p->out_dtype, p->activation, x, x_scale, w,
                              w_scale, bias, residual, y, plan.splits > 1 ? static_cast<float*>(workspace) : nullptr};
     return from_hip(mssm::launch_linear(a, plan, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t mssm_lora_workspace_bytes(const mssm_lora_problem* p) {
+    return check_lora(p) == MSSM_OK ? mssm::plan_lora(p->rows, p->in_dim, p->rank).ws_bytes : 0;
+}
+
+mssm_status mssm_lora(const mssm_lora_problem* p, const void* x, const float* x_scale, const void* a, const void* b,
+                      const float* scale, const int32_t* index, void* y, void* workspace, size_t workspace_bytes,
+                      void* hip_stream) {
+    mssm_status st = check_lora(p);
+    if (st != MSSM_OK) return st;
+    if (!x || !a || !b || !index || !y) return MSSM_ERR_NULL;
+    if (p->dtype == MSSM_F8 ? !x_scale : x_scale != nullptr) return MSSM_ERR_NULL;
+    st = check_align({x, x_scale, a, b, scale, index, y, workspace});
+    if (st != MSSM_OK) return st;
+    const mssm::LoraPlan plan = mssm::plan_lora(p->rows, p->in_dim, p->rank);
+    if (!workspace || workspace_bytes < plan.ws_bytes) return MSSM_ERR_WORKSPACE;
+    const mssm::LoraArgs k{p->rows, p->in_dim, p->out_dim, p->rank, p->adapters, p->dtype, p->out_dtype, x, x_scale, a, b,
+                           scale, index, y, static_cast<float*>(workspace)};
+    return from_hip(mssm::launch_lora(k, plan, static_cast<hipStream_t>(hip_stream)));
 }
 
 size_t mssm_beam_select_workspace_bytes(const mssm_beam_problem* p) {
