@@ -35,6 +35,27 @@ __device__ __forceinline__ float wave_sum(float v) {
     for (int i = 0; i < 4; ++i) r[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i * 16));
     return (r[0] + r[1]) + (r[2] + r[3]);
 }
+__device__ __forceinline__ double wave_sum(double v) {
+    auto add_moved = [&](auto moved) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __float_as_uint(moved(__uint_as_float(static_cast<uint32_t>(b)))),
+                       hi = __float_as_uint(moved(__uint_as_float(static_cast<uint32_t>(b >> 32))));
+        v += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    };
+    add_moved([](float x) { return dpp_move<0xB1>(x); });
+    add_moved([](float x) { return dpp_move<0x4E>(x); });
+    add_moved([](float x) { return dpp_move<0x141>(x); });
+    add_moved([](float x) { return dpp_move<0x140>(x); });
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    double r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), i * 16);
+        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), i * 16);
+        r[i] = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    }
+    return (r[0] + r[1]) + (r[2] + r[3]);
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     auto step = [&](float moved) {
         const uint32_t o = __float_as_uint(moved);
@@ -219,7 +240,11 @@ struct RowScale {
 template <typename T, typename R, typename Q, int W, int NV, bool WHOLE>
 __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
     constexpr bool Q8 = sizeof(Q) == 1;
+    // Which lane has which element depends on where a row off vector boundaries starts,
+    // and with it the order of the sum: in float64, so that the norm does not.
+    typedef std::conditional_t<WHOLE, float, double> Sum;
     __shared__ float part[3][4];
+    __shared__ Sum sums[4];
     const int lane = threadIdx.x & 63, wave = wave_id(), in_row = wave % W;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / W) + wave / W;
     if (W < 4 && row >= a.rows) return;  // a whole wave, and no barrier below
@@ -257,21 +282,25 @@ __global__ __launch_bounds__(256) void norm_kernel(NormKernelArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) load_weight<WHOLE>(a.weight, column(i), a.dim, w[i]);
     }
-    float ss = 0.0f;
+    Sum ss = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float s = 0.0f;
+        Sum s = 0;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s = __builtin_fmaf(h[i][j], h[i][j], s);
+        for (int j = 0; j < VEC; ++j) {
+            const Sum v = h[i][j];
+            if constexpr (WHOLE) s = __builtin_fmaf(v, v, s);
+            else s = __builtin_fma(v, v, s);
+        }
         ss += s;
     }
     ss = wave_sum(ss);
     if constexpr (W == 4) {
-        if (lane == 0) part[0][wave] = ss;
+        if (lane == 0) sums[wave] = ss;
         __syncthreads();
-        ss = (part[0][0] + part[0][1]) + (part[0][2] + part[0][3]);
+        ss = (sums[0] + sums[1]) + (sums[2] + sums[3]);
     }
-    const float r = 1.0f / __builtin_sqrtf(ss / static_cast<float>(a.dim) + a.eps);
+    const float r = 1.0f / __builtin_sqrtf(static_cast<float>(ss) / static_cast<float>(a.dim) + a.eps);
     if (a.res_out) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) store_part<WHOLE>(static_cast<R*>(a.res_out) + e0, column(i), a.dim, h[i]);
@@ -318,6 +347,7 @@ template <typename T, typename R, typename Q>
 __global__ __launch_bounds__(256) void norm_long_kernel(NormKernelArgs a) {
     constexpr bool Q8 = sizeof(Q) == 1;
     __shared__ float part[3][4];
+    __shared__ double sums[4];  // as in norm_kernel: the same whatever row it is
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t row = blockIdx.x, e0 = row * a.dim;
     const T* x = static_cast<const T*>(a.x) + e0;
@@ -340,18 +370,18 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormKernelArgs a) {
             f(c, h, rest);
         }
     };
-    float ss = 0.0f;
+    double ss = 0.0;
     each([&](int64_t, float (&h)[VEC], float (&)[VEC]) {
-        float s = 0.0f;
+        double s = 0.0;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s = __builtin_fmaf(h[j], h[j], s);
+        for (int j = 0; j < VEC; ++j) s = __builtin_fma(static_cast<double>(h[j]), static_cast<double>(h[j]), s);
         ss += s;
     });
     ss = wave_sum(ss);
-    if (lane == 0) part[0][wave] = ss;
+    if (lane == 0) sums[wave] = ss;
     __syncthreads();
-    ss = (part[0][0] + part[0][1]) + (part[0][2] + part[0][3]);
-    const float r = 1.0f / __builtin_sqrtf(ss / static_cast<float>(a.dim) + a.eps);
+    ss = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    const float r = 1.0f / __builtin_sqrtf(static_cast<float>(ss) / static_cast<float>(a.dim) + a.eps);
     Largest top;
     if constexpr (Q8) {
         each([&](int64_t c, float (&h)[VEC], float (&rest)[VEC]) {
