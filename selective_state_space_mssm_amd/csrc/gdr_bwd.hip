@@ -33,7 +33,7 @@ struct AdjointArgs {
     float* dh0;
     float* adjoints;
     float* pulls;
-    int64_t T, N, G, H, K, V, parts;
+    int64_t T, N, each, G, H, K, V, parts;
     int64_t mat_bytes, at_f, at_nt, at_pt;
 };
 
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     const int64_t hg = h / (a.H / a.G);
     const int64_t vw = part * VC, v0 = vw + w * 16;
     const bool in_v = v0 < a.V;
-    const Span sp = span_of(a.offsets, n, a.T, a.N);
+    const Span sp = span_of(a.offsets, n, a.T, a.each);
     const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
     const int K = static_cast<int>(a.K);
 
@@ -204,7 +204,7 @@ struct GradArgs {
     const float *states, *misses, *adjoints, *pulls;
     void *dq, *dk;
     float *dg, *dbeta;
-    int64_t T, N, G, H, K, V, slot0;
+    int64_t T, N, each, G, H, K, V, slot0;
     float scale;
     int norm;
 };
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     float *sX = reinterpret_cast<float*>(lds + kKeys), *sM = sX + kC * kPitch;  // then
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const int64_t hg = blockIdx.x % a.G, slot = a.slot0 + blockIdx.x / a.G;
-    const Chunk ch = chunk_of(a.offsets, slot, a.T, a.N);
+    const Chunk ch = chunk_of(a.offsets, slot, a.T, a.N, a.each);
     if (ch.len == 0) return;
     const int K = static_cast<int>(a.K), V = static_cast<int>(a.V);
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
@@ -497,12 +497,12 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
     const GdrLayout l(a.dtype, true);
     const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const AdjointArgs k{a.q, a.k, a.dy, a.offsets, a.mats, a.dh_final, a.dv, a.dh0, a.adjoints, a.pulls,
-                        a.T, a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.factors, l.nt, l.pt};
+                        a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.factors, l.nt, l.pt};
     gdr_adjoint_kernel<T, KP, NW><<<static_cast<uint32_t>(a.N * a.H * parts), NW * 64, 0, s>>>(k);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const GradArgs d{a.q, a.k, a.dy, a.g, a.beta, a.offsets, a.states, a.misses, a.adjoints, a.pulls, a.dq, a.dk, a.dg, a.dbeta,
-                     a.T, a.N, a.G, a.H, a.K, a.V, 0, a.scale, a.norm};
+                     a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, 0, a.scale, a.norm};
     gdr_grad_kernel<T, KP><<<static_cast<uint32_t>(gdr_slots(a.T, a.N) * a.G), 256, 0, s>>>(d);
     return hipGetLastError();
 }

@@ -39,31 +39,31 @@ __device__ __forceinline__ Planes<N> load_block(const uint8_t* mat, int block, i
 struct Span {
     int64_t start, len;
 };
-__device__ __forceinline__ Span span_of(const int32_t* offsets, int64_t n, int64_t T, int64_t N) {
-    if (!offsets) {
-        const int64_t len = T / N;
-        return {n * len, len};
-    }
+// Tokens are fewer than 2^31; of equal lengths, without a division, `each` is T / N.
+__device__ __forceinline__ Span span_of(const int32_t* offsets, int64_t n, int64_t T, int64_t each) {
+    if (!offsets) return {n * each, each};
     int64_t s = offsets[n], e = offsets[n + 1];
     s = s < 0 ? 0 : s > T ? T : s;
     e = e < s ? s : e > T ? T : e;
     return {s, e - s};
 }
-__device__ __forceinline__ int64_t first_slot(const Span& s, int64_t n) { return s.start / kC + n; }
+__device__ __forceinline__ int64_t first_slot(const Span& s, int64_t n) { return (s.start >> 6) + n; }
+static_assert(kC == 64, "first_slot divides by 64");
 
 // The sequence and chunk of a slot; len = 0: the slot is no chunk.
 struct Chunk {
     int64_t seq, start;  // its first token
     int len;             // tokens, up to 64
 };
-__device__ __forceinline__ Chunk chunk_of(const int32_t* offsets, int64_t slot, int64_t T, int64_t N) {
+__device__ __forceinline__ Chunk chunk_of(const int32_t* offsets, int64_t slot, int64_t T, int64_t N, int64_t each) {
     int64_t lo = 0, hi = N;  // the last sequence whose first slot is not behind this one
     while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (first_slot(span_of(offsets, mid, T, N), mid) <= slot) lo = mid;
+        const int64_t mid = (lo + hi) >> 1;
+        const int64_t s = offsets ? imin64(T, offsets[mid] < 0 ? 0 : offsets[mid]) : mid * each;
+        if ((s >> 6) + mid <= slot) lo = mid;
         else hi = mid;
     }
-    const Span s = span_of(offsets, lo, T, N);
+    const Span s = span_of(offsets, lo, T, each);
     const int64_t t = (slot - first_slot(s, lo)) * kC;
     if (t < 0 || t >= s.len) return {lo, 0, 0};
     return {lo, s.start + t, static_cast<int>(imin64(kC, s.len - t))};

@@ -23,7 +23,7 @@ struct FwdArgs {
     float* h_final;
     float* states;
     float* misses;
-    int64_t T, N, G, H, K, V, parts;
+    int64_t T, N, each, G, H, K, V, parts;
     int64_t mat_bytes, at_n, at_p, at_f;
 };
 
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
     const int64_t hg = h / (a.H / a.G);
     const int64_t vw = part * VC, v0 = vw + w * 16;  // the workgroup's first value element, and the wave's
     const bool in_v = v0 < a.V;                      // V is a multiple of 16
-    const Span sp = span_of(a.offsets, n, a.T, a.N);
+    const Span sp = span_of(a.offsets, n, a.T, a.each);
     const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
     const int K = static_cast<int>(a.K);
 
@@ -203,7 +203,7 @@ hipError_t launch_v(const GdrArgs& a, hipStream_t s) {
     const GdrLayout l(a.dtype, a.train);
     const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const FwdArgs k{a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
-                    a.T, a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors};
+                    a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors};
     gdr_fwd_kernel<T, KP, NW, TRAIN><<<static_cast<uint32_t>(a.N * a.H * parts), NW * 64, 0, s>>>(k);
     return hipGetLastError();
 }
