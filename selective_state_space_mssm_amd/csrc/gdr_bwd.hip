@@ -62,8 +62,8 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
         L[m] = f32x4{0, 0, 0, 0};
-        if (a.dh_final && in_v && 16 * m < K)
-            L[m] = *reinterpret_cast<const f32x4*>(a.dh_final + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g);
+        if (a.dh_final && in_v && state_column(m, 4 * g) < K)
+            L[m] = *reinterpret_cast<const f32x4*>(a.dh_final + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g));
     }
 
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
@@ -133,10 +133,10 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
         if (!in_v) continue;
 
         {
-            float* to = a.adjoints + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K + 4 * g;
+            float* to = a.adjoints + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K;
 #pragma unroll
             for (int m = 0; m < KM; ++m)
-                if (16 * m < K) *reinterpret_cast<f32x4*>(to + 16 * m) = L[m];
+                if (state_column(m, 4 * g) < K) *reinterpret_cast<f32x4*>(to + state_column(m, 4 * g)) = L[m];
         }
         // du = D (L k) + Pᵀ dy
         f32x4 Y[4] = {};
@@ -191,7 +191,8 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     if (a.dh0 && in_v) {
 #pragma unroll
         for (int m = 0; m < KM; ++m)
-            if (16 * m < K) *reinterpret_cast<f32x4*>(a.dh0 + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g) = L[m];
+            if (state_column(m, 4 * g) < K)
+                *reinterpret_cast<f32x4*>(a.dh0 + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g)) = L[m];
     }
 }
 
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             const Planes<3> zf = split<3>(zz), uf = split<3>(x);
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
-                const Planes<3> sf = State::read(lds_s, 16 * m + c, g), lf = State::read(lds_l, 16 * m + c, g);
+                const Planes<3> sf = State::read(lds_s, state_column(m, c), g), lf = State::read(lds_l, state_column(m, c), g);
                 yS[m] = mma(sf, dyf, yS[m]);
                 zS[m] = mma(sf, zf, zS[m]);
                 uL[m] = mma(lf, uf, uL[m]);
@@ -406,10 +407,10 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
         float wrote = 0.0f;
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
-            const bool in = in_t && 16 * m < K;
+            const bool in = in_t && state_column(m, 4 * g) < K;
             const f32x4 zero = {0, 0, 0, 0};
-            k4[m] = in ? rk * load_four(kp + row * qk_stride + 16 * m + 4 * g) : zero;
-            q4[m] = in ? rq * load_four(qp + row * qk_stride + 16 * m + 4 * g) : zero;
+            k4[m] = in ? rk * load_four(kp + row * qk_stride + state_column(m, 4 * g)) : zero;
+            q4[m] = in ? rq * load_four(qp + row * qk_stride + state_column(m, 4 * g)) : zero;
             dq[m] = fy * yS[m];
             dkr[m] = fz * zS[m];
             dkc[m] = to_end * uL[m];
@@ -471,24 +472,24 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     f32x4 k4[KM], q4[KM];
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
-        const bool in = in_t && 16 * m < K;
+        const bool in = in_t && state_column(m, 4 * g) < K;
         const f32x4 zero = {0, 0, 0, 0};
-        k4[m] = in && a.norm ? rk * load_four(kp + row * qk_stride + 16 * m + 4 * g) : zero;
-        q4[m] = in && a.norm ? rq * load_four(qp + row * qk_stride + 16 * m + 4 * g) : zero;
+        k4[m] = in && a.norm ? rk * load_four(kp + row * qk_stride + state_column(m, 4 * g)) : zero;
+        q4[m] = in && a.norm ? rq * load_four(qp + row * qk_stride + state_column(m, 4 * g)) : zero;
         qd = dot4(q4[m], dq_sum[m], qd);
         kd = dot4(k4[m], dk_sum[m], kd);
     }
     qd = group4_sum(qd);
     kd = group4_sum(kd);
-    T* dqp = static_cast<T*>(a.dq) + (ch.start + row) * qk_stride + hg * a.K + 4 * g;
-    T* dkp = static_cast<T*>(a.dk) + (ch.start + row) * qk_stride + hg * a.K + 4 * g;
+    T* dqp = static_cast<T*>(a.dq) + (ch.start + row) * qk_stride + hg * a.K;
+    T* dkp = static_cast<T*>(a.dk) + (ch.start + row) * qk_stride + hg * a.K;
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
-        if (!in_t || 16 * m >= K) continue;
+        if (!in_t || state_column(m, 4 * g) >= K) continue;
         const f32x4 x = rq * (dq_sum[m] - qd * q4[m]), y = rk * (dk_sum[m] - kd * k4[m]);
         const float xs[4] = {x[0], x[1], x[2], x[3]}, ys[4] = {y[0], y[1], y[2], y[3]};
-        store_row(dqp + 16 * m, xs);
-        store_row(dkp + 16 * m, ys);
+        store_row(dqp + state_column(m, 4 * g), xs);
+        store_row(dkp + state_column(m, 4 * g), ys);
     }
 }
 
@@ -508,7 +509,10 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
 }
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
-    return a.V > 64 && a.N * a.H >= 128 ? launch_c<T, KP, 8>(a, s) : launch_c<T, KP, 4>(a, s);
+    if constexpr (sizeof(T) == 2 || KP == 64) {  // eight waves have 256 registers each, too few for float32 planes of 128
+        if (a.V > 64 && a.N * a.H >= 128) return launch_c<T, KP, 8>(a, s);
+    }
+    return launch_c<T, KP, 4>(a, s);
 }
 template <typename T>
 hipError_t launch_t(const GdrArgs& a, hipStream_t s) {

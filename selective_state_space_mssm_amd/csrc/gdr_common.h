@@ -155,10 +155,10 @@ __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_
 
 // 64 rows (tokens) of W columns, as bfloat16 planes.  A row's 16-byte pieces are
 // exchanged among themselves by the row's number, so that the 16 rows that a read
-// takes at once spread over the banks.  Read as operands in the folded order of
-// what is summed over: by rows (summed over the columns) in two 8-byte reads, by
-// columns (summed over the tokens) in two transposing reads: sixteen lanes read
-// four rows of 16 values, 8 bytes a lane, and each gets a column's four.
+// takes at once spread over the banks.  Read as operands by rows (summed over the
+// columns) in one 16-byte read, or by columns (summed over the tokens) in two
+// transposing reads: sixteen lanes read four rows of 16 values, 8 bytes a lane,
+// and each gets a column's four.
 template <int W>
 struct Tile {
     static constexpr int kRow = W * 2, kBytes = kC * kRow, kPieces = W / 8;
@@ -166,36 +166,44 @@ struct Tile {
     __device__ static __forceinline__ int turn(int row) { return kPieces == 16 ? row & 15 : (row >> 1) & 7; }
     __device__ static __forceinline__ int at(int row, int piece) { return row * kRow + ((piece ^ turn(row)) * 16); }
 
+    // columns 32 s .. of row 16 rt + c, slots in their own order (state_column below has the accumulators' rows for it)
     template <int N>
     __device__ static __forceinline__ Planes<N> rows(const uint8_t* lds, int rt, int s, int c, int g) {
-        const uint8_t* p = lds + (g & 1) * 8;
-        const int lo = at(16 * rt + c, 4 * s + (g >> 1)), hi = at(16 * rt + c, 4 * s + 2 + (g >> 1));
         Planes<N> out;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const u32x2 a = *reinterpret_cast<const u32x2*>(p + n * kBytes + lo), b = *reinterpret_cast<const u32x2*>(p + n * kBytes + hi);
-            out.p[n] = u32x4{a[0], a[1], b[0], b[1]};
-        }
+        for (int n = 0; n < N; ++n) out.p[n] = *reinterpret_cast<const u32x4*>(lds + n * kBytes + at(16 * rt + c, 4 * s + g));
         return out;
     }
-    // four rows 16 rt + 4 g .. of column 16 m + c
-    __device__ static __forceinline__ u32x2 four(const uint8_t* lds, int rt, int m, int c, int g) {
+    // four rows 16 rt + 4 g .. of the column at a byte offset that this lane helps to read
+    __device__ static __forceinline__ u32x2 four(const uint8_t* lds, int rt, int piece, int byte, int c, int g) {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
-        const uint8_t* p = lds + at(16 * rt + 4 * g + (c >> 2), 2 * m + ((c >> 1) & 1)) + (c & 1) * 8;
+        const uint8_t* p = lds + at(16 * rt + 4 * g + (c >> 2), piece) + byte;
         return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(p)));
     }
+    // ... of column 16 m + c
+    __device__ static __forceinline__ u32x2 four(const uint8_t* lds, int rt, int m, int c, int g) {
+        return four(lds, rt, 2 * m + ((c >> 1) & 1), (c & 1) * 8, c, g);
+    }
+    // rows 32 s .. of column state_column(m, c), folded
     template <int N>
     __device__ static __forceinline__ Planes<N> columns(const uint8_t* lds, int m, int s, int c, int g) {
         Planes<N> out;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const u32x2 a = four(lds + n * kBytes, 2 * s, m, c, g), b = four(lds + n * kBytes, 2 * s + 1, m, c, g);
+            const uint8_t* p = lds + n * kBytes;
+            const u32x2 a = four(p, 2 * s, 4 * (m >> 1) + (c & 3), (m & 1) * 8, c, g),
+                        b = four(p, 2 * s + 1, 4 * (m >> 1) + (c & 3), (m & 1) * 8, c, g);
             out.p[n] = u32x4{a[0], a[1], b[0], b[1]};
         }
         return out;
     }
 };
+
+// The key element of row i of tile m of a state's accumulators: tiles 2 s and 2 s + 1
+// together are an operand whose slot (g, j) is element 32 s + 8 g + j, which is how
+// 16 bytes of a row of q or k lie.
+__device__ __forceinline__ constexpr int state_column(int m, int i) { return 32 * (m >> 1) + 8 * (i >> 2) + 4 * (m & 1) + (i & 3); }
 
 __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
     return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(

@@ -32,7 +32,7 @@ struct FwdArgs {
 // one barrier a chunk; float32 through registers, where it is cut into planes,
 // with P from memory (the L2, mostly) as the planes leave no room for it.
 template <typename T, int KP, int NW, bool TRAIN>
-__global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
+__global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     constexpr bool B16 = sizeof(T) == 2;
     constexpr int PL = kPlanes<T>, PP = B16 ? 2 : 3, KS = KP / 32, KM = KP / 16, VC = NW * 16;
     typedef Tile<KP> Keys;
@@ -56,7 +56,8 @@ __global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
         S[m] = f32x4{0, 0, 0, 0};
-        if (a.h0 && in_v && 16 * m < K) S[m] = *reinterpret_cast<const f32x4*>(a.h0 + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g);
+        if (a.h0 && in_v && state_column(m, 4 * g) < K)
+            S[m] = *reinterpret_cast<const f32x4*>(a.h0 + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g));
     }
 
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
@@ -125,10 +126,10 @@ __global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
             }
         }
         if constexpr (TRAIN) {
-            float* to = a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K + 4 * g;
+            float* to = a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K;
 #pragma unroll
             for (int m = 0; m < KM; ++m)
-                if (16 * m < K) *reinterpret_cast<f32x4*>(to + 16 * m) = S[m];
+                if (state_column(m, 4 * g) < K) *reinterpret_cast<f32x4*>(to + state_column(m, 4 * g)) = S[m];
         }
         // S k (tokens in the rows) and S q (tokens in the columns)
         f32x4 X[4] = {};
@@ -140,12 +141,18 @@ __global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
             Planes<PP> so;
 #pragma unroll
             for (int i = 0; i < PP; ++i) so.p[i] = st.p[i];
+            Planes<PL> kf[4], qf[4];
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) X[rt] = mma(Keys::template rows<PL>(lds_k, rt, s, c, g), st, X[rt]);
+            for (int rt = 0; rt < 4; ++rt) {
+                kf[rt] = Keys::template rows<PL>(lds_k, rt, s, c, g);
+                qf[rt] = Keys::template rows<PL>(lds_q, rt, s, c, g);
+            }
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) O[rt] = mma(so, Keys::template rows<PL>(lds_q, rt, s, c, g), O[rt]);
+            for (int rt = 0; rt < 4; ++rt) X[rt] = mma(kf[rt], st, X[rt]);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) O[rt] = mma(so, qf[rt], O[rt]);
         }
-        // e = r + N (beta r)
+        // e = r + N (beta r) with r = v - exp(b) S k
         f32x4 beta[4];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -155,46 +162,49 @@ __global__ __launch_bounds__(NW * 64) void gdr_fwd_kernel(FwdArgs a) {
         }
         const Planes<3> mx[2] = {split<3>(beta[0] * X[0], beta[1] * X[1]), split<3>(beta[2] * X[2], beta[3] * X[3])};
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int rt = 0; rt < 4; ++rt)
                 if (block_of<true>(rt, s) >= 0) X[rt] = mma(load_block<3>(lds_n, block_of<true>(rt, s), lane), mx[s], X[rt]);
         if constexpr (TRAIN) {
             float* e = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
 #pragma unroll
             for (int i = 0; i < 16; ++i) e[((i >> 2) * 16 + 4 * g + (i & 3)) * a.V] = X[i >> 2][i & 3];
         }
-        // y = scale exp(b) S q + P u, and the state's update
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            O[rt] *= f[3 * kC + 16 * rt + c];
-            X[rt] *= beta[rt];  // u
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const Planes<PP> u = split<PP>(X[2 * s], X[2 * s + 1]);
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt)
-                if (block_of<true>(rt, s) >= 0)
-                    O[rt] = mma(u, load_block<PP>(B16 ? lds_p : mats_of(chunk) + a.at_p, block_of<true>(rt, s), lane), O[rt]);
-        }
+        // u; y = scale exp(b) S q + P u, and the state's update
         const float last = f[4 * kC];
-#pragma unroll
-        for (int i = 0; i < KM; ++i) S[i] *= last;
+        Planes<3> ud[2];
+        Planes<PP> u[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const f32x4 d0 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 4 * g),
                         d1 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 16 + 4 * g);
-            const Planes<3> u = split<3>(d0 * X[2 * s], d1 * X[2 * s + 1]);
-#pragma unroll
-            for (int i = 0; i < KM; ++i) S[i] = mma(Keys::template columns<PL>(lds_k, i, s, c, g), u, S[i]);
+            X[2 * s] *= beta[2 * s];
+            X[2 * s + 1] *= beta[2 * s + 1];
+            ud[s] = split<3>(d0 * X[2 * s], d1 * X[2 * s + 1]);
+            u[s] = split<PP>(X[2 * s], X[2 * s + 1]);
         }
+#pragma unroll
+        for (int i = 0; i < KM; ++i) S[i] *= last;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) O[rt] *= f[3 * kC + 16 * rt + c];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < KM; ++m) S[m] = mma(Keys::template columns<PL>(lds_k, m, s, c, g), ud[s], S[m]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+                if (block_of<true>(rt, s) >= 0)
+                    O[rt] = mma(u[s], load_block<PP>(B16 ? lds_p : mats_of(chunk) + a.at_p, block_of<true>(rt, s), lane), O[rt]);
     }
     if (chunks) put_y(chunks - 1);
     if (a.h_final && in_v) {
 #pragma unroll
         for (int m = 0; m < KM; ++m)
-            if (16 * m < K) *reinterpret_cast<f32x4*>(a.h_final + ((n * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g) = S[m];
+            if (state_column(m, 4 * g) < K)
+                *reinterpret_cast<f32x4*>(a.h_final + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g)) = S[m];
     }
 }
 
@@ -213,7 +223,10 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
 }
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
-    return a.V > 64 && a.N * a.H >= 128 ? launch_c<T, KP, 8>(a, s) : launch_c<T, KP, 4>(a, s);
+    if constexpr (sizeof(T) == 2 || KP == 64) {  // eight waves have 256 registers each, too few for float32 planes of 128
+        if (a.V > 64 && a.N * a.H >= 128) return launch_c<T, KP, 8>(a, s);
+    }
+    return launch_c<T, KP, 4>(a, s);
 }
 template <typename T>
 hipError_t launch_t(const GdrArgs& a, hipStream_t s) {
