@@ -65,7 +65,7 @@ struct LoraPlan {
     int64_t rank, step;
     size_t ws_bytes;
 };
-LoraPlan plan_lora(int64_t M, int64_t K, int64_t R);
+LoraPlan plan_lora(int64_t M, int64_t K, int64_t R, bool f32);
 
 struct LoraArgs {
     int64_t M, K, N, R, S;

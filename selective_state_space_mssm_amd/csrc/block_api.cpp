@@ -72,6 +72,7 @@ mssm_status check_lora(const mssm_lora_problem* p) {
     if (p->rows >= (int64_t{1} << 28) || p->in_dim >= (int64_t{1} << 20) || p->out_dim >= (int64_t{1} << 23) ||
         p->adapters >= (int64_t{1} << 31))
         return MSSM_ERR_SHAPE;
+    if ((p->rows + 31) / 32 * ((p->out_dim + 255) / 256) >= (int64_t{1} << 24)) return MSSM_ERR_SHAPE;  // beyond any memory
     return MSSM_OK;
 }
 
@@ -123,7 +124,7 @@ mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float
 }
 
 size_t mssm_lora_workspace_bytes(const mssm_lora_problem* p) {
-    return check_lora(p) == MSSM_OK ? mssm::plan_lora(p->rows, p->in_dim, p->rank).ws_bytes : 0;
+    return check_lora(p) == MSSM_OK ? mssm::plan_lora(p->rows, p->in_dim, p->rank, p->dtype == MSSM_F32).ws_bytes : 0;
 }
 
 mssm_status mssm_lora(const mssm_lora_problem* p, const void* x, const float* x_scale, const void* a, const void* b,
@@ -135,7 +136,7 @@ mssm_status mssm_lora(const mssm_lora_problem* p, const void* x, const float* x_
     if (p->dtype == MSSM_F8 ? !x_scale : x_scale != nullptr) return MSSM_ERR_NULL;
     st = check_align({x, x_scale, a, b, scale, index, y, workspace});
     if (st != MSSM_OK) return st;
-    const mssm::LoraPlan plan = mssm::plan_lora(p->rows, p->in_dim, p->rank);
+    const mssm::LoraPlan plan = mssm::plan_lora(p->rows, p->in_dim, p->rank, p->dtype == MSSM_F32);
     if (!workspace || workspace_bytes < plan.ws_bytes) return MSSM_ERR_WORKSPACE;
     const mssm::LoraArgs k{p->rows, p->in_dim, p->out_dim, p->rank, p->adapters, p->dtype, p->out_dtype, x, x_scale, a, b,
                            scale, index, y, static_cast<float*>(workspace)};

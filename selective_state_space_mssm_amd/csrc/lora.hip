@@ -29,6 +29,12 @@ struct LoraKernelArgs {
 // ---- eight neighbouring elements of a row, wherever it starts ----------------------
 
 template <typename V> struct __attribute__((packed, aligned(1))) Loose { V v; };
+// Stores past the caches, at any address.
+template <typename V>
+__device__ __forceinline__ void stream(void* p, V v) {
+    typedef V Anywhere __attribute__((aligned(1)));
+    __builtin_nontemporal_store(v, static_cast<Anywhere*>(p));
+}
 
 template <int N>
 __device__ __forceinline__ Planes<N> widen(const float (&x)[8]) {
@@ -68,21 +74,81 @@ __device__ __forceinline__ void load_part(const T* row, int64_t k, int64_t end, 
         for (int i = 0; i < 8; ++i) v[i] = k + i < end ? load_one(row + k + i) : 0.0f;
     }
 }
+__device__ __forceinline__ void store_eight(float* p, const float (&v)[8]) {
+    stream(p, f32x4{v[0], v[1], v[2], v[3]});
+    stream(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+}
+__device__ __forceinline__ void store_eight(uint16_t* p, const float (&v)[8]) {
+    bf16x8 b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = static_cast<__bf16>(v[i]);
+    stream(p, b);
+}
+template <typename T>
+__device__ __forceinline__ void store_part(T* row, int64_t n, int64_t end, const float (&v)[8]) {
+    if (n + 8 <= end) {
+        store_eight(row + n, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n + i < end) store_act(row, n + i, v[i]);
+    }
+}
 // Planes of the type: bfloat16 and e4m3 (widened, which is exact) are one.
 template <typename T> constexpr int kInner = sizeof(T) == 4 ? 3 : 1;
-template <typename T>
-__device__ __forceinline__ Planes<kInner<T>> load_operand(const T* row, int64_t k, int64_t end) {
-    if constexpr (sizeof(T) == 2) {
-        if (k + 8 <= end) {
-            Planes<1> out;
-            out.p[0] = reinterpret_cast<const Loose<u32x4>*>(row + k)->v;
-            return out;
+
+// Eight elements as loaded, to be made operands when they are needed.
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    f32x4 lo, hi;
+    __device__ __forceinline__ void load(const float* p) {
+        lo = reinterpret_cast<const Loose<f32x4>*>(p)->v;
+        hi = reinterpret_cast<const Loose<f32x4>*>(p + 4)->v;
+    }
+    __device__ __forceinline__ void load_part(const float* row, int64_t k, int64_t end) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i] = k + i < end ? row[k + i] : 0.0f, hi[i] = k + 4 + i < end ? row[k + 4 + i] : 0.0f;
+    }
+    __device__ __forceinline__ Planes<3> planes() const { return split<3>(lo, hi); }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
+    }
+};
+template <> struct Eight<uint16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = reinterpret_cast<const Loose<u32x4>*>(p)->v; }
+    __device__ __forceinline__ void load_part(const uint16_t* row, int64_t k, int64_t end) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = k + 2 * i < end ? row[k + 2 * i] : 0u, hi = k + 2 * i + 1 < end ? row[k + 2 * i + 1] : 0u;
+            v[i] = hi << 16 | lo;
         }
     }
-    float v[8];
-    load_part(row, k, end, v);
-    return split<kInner<T>>(v);
-}
+    __device__ __forceinline__ Planes<1> planes() const { return Planes<1>{{v}}; }
+    __device__ __forceinline__ void floats(float (&x)[8]) const { to_floats(v, x); }
+};
+template <> struct Eight<uint8_t> {
+    u32x2 v;
+    __device__ __forceinline__ void load(const uint8_t* p) { v = reinterpret_cast<const Loose<u32x2>*>(p)->v; }
+    __device__ __forceinline__ void load_part(const uint8_t* row, int64_t k, int64_t end) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i] |= k + 4 * i + j < end ? static_cast<uint32_t>(row[k + 4 * i + j]) << (8 * j) : 0u;
+        }
+    }
+    __device__ __forceinline__ Planes<1> planes() const {  // widened, which is exact
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[i]), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[i]), true);
+            x[4 * i] = lo[0]; x[4 * i + 1] = lo[1]; x[4 * i + 2] = hi[0]; x[4 * i + 3] = hi[1];
+        }
+        return split<1>(x);
+    }
+};
 
 // ---- few rows ---------------------------------------------------------------------
 
@@ -151,7 +217,7 @@ __device__ __forceinline__ void each_adapter(const LoraKernelArgs& a, int64_t m0
 
 // 16 MT rows and the whole rank; the four waves take every fourth 32 of K (of this split's part).
 template <typename X, typename W, int RT, int MT>
-__global__ __launch_bounds__(256) void lora_down_kernel(LoraKernelArgs a) {
+__global__ __launch_bounds__(256, 2) void lora_down_kernel(LoraKernelArgs a) {
     __shared__ f32x4 part[4][RT * MT][64];
     const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16 * MT, k0 = blockIdx.y * a.step, k1 = imin64(a.K, k0 + a.step);
@@ -159,20 +225,58 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraKernelArgs a) {
         f32x4 acc[RT][MT] = {};
         const X* x = static_cast<const X*>(a.x);
         const W* wa = static_cast<const W*>(a.a) + i * a.R * a.K;
-        for (int64_t k = k0 + w * 32 + g * 8; k - g * 8 < k1; k += 128) {
+        const X* xr[MT];
+        const W* wr[RT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xr[t] = x + imin64(m0 + 16 * t + c, a.M - 1) * a.K;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) wr[r] = wa + imin64(16 * r + c, a.R - 1) * a.K;
+        auto step = [&](const Eight<X>(&xe)[MT], const Eight<W>(&we)[RT]) {
             Planes<kInner<X>> xf[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int64_t m = m0 + 16 * t + c;
-                xf[t] = load_operand(x + (m < a.M ? m : a.M - 1) * a.K, k, k1);
-            }
+            for (int t = 0; t < MT; ++t) xf[t] = xe[t].planes();
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int64_t row = 16 * r + c;
-                const auto wf = load_operand(wa + (row < a.R ? row : a.R - 1) * a.K, k, k1);
+                const Planes<kInner<W>> wf = we[r].planes();
 #pragma unroll
                 for (int t = 0; t < MT; ++t) acc[r][t] = mma(wf, xf[t], acc[r][t]);
             }
+        };
+        auto fetch = [&](int64_t k, Eight<X>(&xe)[MT], Eight<W>(&we)[RT]) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) xe[t].load(xr[t] + k + 8 * g);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) we[r].load(wr[r] + k + 8 * g);
+        };
+        // whole steps, the next one's loads under way if there are registers for them; then what is left of K
+        constexpr bool AHEAD = RT * (sizeof(W) / 2) + MT <= 8;
+        Eight<X> xe[AHEAD ? 2 : 1][MT];
+        Eight<W> we[AHEAD ? 2 : 1][RT];
+        int64_t k = k0 + w * 32;
+        if constexpr (!AHEAD) {
+            for (; k + 32 <= k1; k += 128) {
+                fetch(k, xe[0], we[0]);
+                step(xe[0], we[0]);
+            }
+        } else {
+        if (k + 32 <= k1) fetch(k, xe[0], we[0]);
+        for (; k + 32 <= k1; k += 256) {
+            if (k + 160 <= k1) fetch(k + 128, xe[1], we[1]);
+            step(xe[0], we[0]);
+            if (k + 160 > k1) {
+                k += 128;
+                break;
+            }
+            if (k + 288 <= k1) fetch(k + 256, xe[0], we[0]);
+            step(xe[1], we[1]);
+        }
+        }
+        if (k < k1) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) xe[0][t].load_part(xr[t], k + 8 * g, k1);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) we[0][r].load_part(wr[r], k + 8 * g, k1);
+            step(xe[0], we[0]);
         }
         __syncthreads();  // the sums of the adapter before are read
 #pragma unroll
@@ -191,56 +295,88 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraKernelArgs a) {
     });
 }
 
-// A wave: 16 MT rows and 64 columns; row 4 g + r of tile j is column 16 g + 4 j + r,
-// so that a lane has 16 neighbours of a row of y.
+// A wave: 16 MT rows and 64 columns; row 4 g + r of tile j is column 32 (j / 2) + 8 g
+// + 4 (j % 2) + r, so that a lane has eight neighbours of a row of y twice, and the
+// four lanes of a row 64 bytes at a time.
+// The rows' inner values are cut into planes once for the workgroup's 256 columns.
 template <typename W, typename Y, int RS, int MT>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraKernelArgs a) {
+__global__ __launch_bounds__(256, 2) void lora_up_kernel(LoraKernelArgs a) {
     constexpr int PT = sizeof(Y) == 2 && sizeof(W) == 2 ? 2 : 3;  // planes of the inner values
+    constexpr int ROW = RS * 64 + 16, PLANE = 16 * MT * ROW;      // 16 bytes apart: the 16 rows of a read on different banks
+    __shared__ __align__(16) uint8_t lds[PT * PLANE];
     const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16 * MT, n0 = (static_cast<int64_t>(blockIdx.y) * 4 + w) * 64;
-    if (n0 >= a.N) return;
-    f32x4 acc[MT][4];
-    uint64_t used = 0;
+    const uint32_t blocks = static_cast<uint32_t>((a.N + 255) / 256), rows = blockIdx.x / blocks;  // neighbours share rows
+    const int64_t m0 = static_cast<int64_t>(rows) * 16 * MT, n0 = (static_cast<int64_t>(blockIdx.x - rows * blocks) * 4 + w) * 64;
+    const bool whole = n0 + 64 <= a.N;  // the same for all lanes: no branch around a load
     Y* y = static_cast<Y*>(a.y);
-    const int64_t n = n0 + 16 * g;
+    const int64_t n = n0 + 8 * g;
+    Eight<Y> old[MT][2];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t m = m0 + 16 * t + c;
+        const Y* row = y + imin64(m0 + 16 * t + c, a.M - 1) * a.N;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][j][r] = m < a.M && n + 4 * j + r < a.N ? load_act(y, m * a.N + n + 4 * j + r) : 0.0f;
+        for (int half = 0; half < 2; ++half) {
+            if (whole) old[t][half].load(row + n + 32 * half);
+            else old[t][half].load_part(row, n + 32 * half, a.N);
+        }
     }
+    const int32_t mine = lane < 16 * MT && m0 + lane < a.M ? a.index[m0 + lane] : -1;
+    const uint64_t used = __ballot(mine >= 0 && mine < a.S);
+    if (!used) return;
+    for (int item = threadIdx.x; item < 16 * MT * RS * 4; item += 256) {
+        const int row = item / (RS * 4), k = item % (RS * 4) * 8;
+        f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+        if (used >> row & 1 && k < a.RP) {  // others' were never written
+            const float* p = a.inner + (m0 + row) * a.RP + k;
+            for (int q = 0; q < a.splits; ++q, p += a.M * a.RP) {
+                lo += *reinterpret_cast<const f32x4*>(p);
+                hi += *reinterpret_cast<const f32x4*>(p + 4);
+            }
+        }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + e < a.R ? (e < 4 ? lo[e] : hi[e - 4]) : 0.0f;
+        const Planes<PT> t = split<PT>(v);
+#pragma unroll
+        for (int i = 0; i < PT; ++i) *reinterpret_cast<u32x4*>(lds + i * PLANE + row * ROW + k * 2) = t.p[i];
+    }
+    __syncthreads();
+    if (n0 >= a.N) return;
+    f32x4 acc[MT][4] = {};
     each_adapter<16 * MT>(a, m0, lane, [&](int64_t i, uint64_t same) {
-        used |= same;
         const W* wb = static_cast<const W*>(a.b) + i * a.N * a.R;
+        const W* row[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row[j] = wb + imin64(n0 + 32 * (j >> 1) + 8 * (c >> 2) + 4 * (j & 1) + (c & 3), a.N - 1) * a.R;
 #pragma unroll
         for (int s = 0; s < RS; ++s) {
-            Planes<kInner<W>> bf[4];
+            const int64_t k = 32 * s + 8 * g;
+            Eight<W> be[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t row = n0 + 16 * (c >> 2) + 4 * j + (c & 3);
-                bf[j] = load_operand(wb + (row < a.N ? row : a.N - 1) * a.R, 32 * s + 8 * g, a.R);
+                if (32 * s + 32 <= a.R) be[j].load(row[j] + k);
+                else be[j].load_part(row[j], k, a.R);
             }
+            Planes<kInner<W>> bf[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bf[j] = be[j].planes();
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                const int row = 16 * t + c;
-                float v[8] = {};
-                if (same >> row & 1) {
-                    for (int p = 0; p < a.splits; ++p) {
-                        float q[8];
-                        load_part(a.inner + (p * a.M + m0 + row) * a.RP, 32 * s + 8 * g, a.R, q);
+                Planes<PT> tf;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] += q[e];
-                    }
-                }
-                const Planes<PT> tf = split<PT>(v);
+                for (int q = 0; q < PT; ++q) tf.p[q] = *reinterpret_cast<const u32x4*>(lds + q * PLANE + (16 * t + c) * ROW + k * 2);
+                const bool this_one = same >> (16 * t + c) & 1;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const f32x4 sum = mma(bf[j], tf, acc[t][j]);
-                    acc[t][j] = same >> row & 1 ? sum : acc[t][j];  // also where this adapter's weights are no numbers
+                    acc[t][j] = this_one ? sum : acc[t][j];  // also where this adapter's weights are no numbers
                 }
             }
+            // The compiler leaves one wait state too few between the last of these and
+            // what overwrites or reads their results behind the branch that follows.
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_nop 7" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
         }
     });
 #pragma unroll
@@ -248,29 +384,36 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraKernelArgs a) {
         const int row = 16 * t + c;
         if (!(used >> row & 1)) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int half = 0; half < 2; ++half) {
+            float v[8];
+            old[t][half].floats(v);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (n + 4 * j + r < a.N) store_act(y, (m0 + row) * a.N + n + 4 * j + r, acc[t][j][r]);
+            for (int i = 0; i < 8; ++i) v[i] += acc[t][2 * half + (i >> 2)][i & 3];
+            store_part(y + (m0 + row) * a.N, n + 32 * half, a.N, v);
+        }
     }
 }
 
 // ---- schedule -----------------------------------------------------------------------
 
-template <typename X, typename W, typename Y, int MT>
+template <typename X, typename W, typename Y, int ROWS>
 void launch_tiles(const LoraKernelArgs& k, hipStream_t s) {
-    const dim3 down(static_cast<uint32_t>((k.M + 16 * MT - 1) / (16 * MT)), static_cast<uint32_t>(k.splits));
-    const dim3 up(down.x, static_cast<uint32_t>((k.N + 255) / 256));
+    const dim3 down(static_cast<uint32_t>((k.M + ROWS - 1) / ROWS), static_cast<uint32_t>(k.splits));
+    constexpr int MT = ROWS / 16;
     switch ((k.R + 15) / 16) {
         case 1: lora_down_kernel<X, W, 1, MT><<<down, 256, 0, s>>>(k); break;
         case 2: lora_down_kernel<X, W, 2, MT><<<down, 256, 0, s>>>(k); break;
         case 3: case 4: lora_down_kernel<X, W, 4, MT><<<down, 256, 0, s>>>(k); break;
-        default: lora_down_kernel<X, W, 8, MT><<<down, 256, 0, s>>>(k); break;
+        default:
+            if constexpr (MT < (sizeof(W) == 2 ? 4 : 2)) lora_down_kernel<X, W, 8, MT><<<down, 256, 0, s>>>(k);
+            break;
     }
+    constexpr int UT = MT < 2 ? 1 : sizeof(Y) == 4 ? 2 : 4;  // rows / 16; y and the sums in registers
+    const dim3 up(static_cast<uint32_t>((k.M + 16 * UT - 1) / (16 * UT) * ((k.N + 255) / 256)));
     switch ((k.R + 31) / 32) {
-        case 1: lora_up_kernel<W, Y, 1, MT><<<up, 256, 0, s>>>(k); break;
-        case 2: lora_up_kernel<W, Y, 2, MT><<<up, 256, 0, s>>>(k); break;
-        default: lora_up_kernel<W, Y, 4, MT><<<up, 256, 0, s>>>(k); break;
+        case 1: lora_up_kernel<W, Y, 1, UT><<<up, 256, 0, s>>>(k); break;
+        case 2: lora_up_kernel<W, Y, 2, UT><<<up, 256, 0, s>>>(k); break;
+        default: lora_up_kernel<W, Y, 4, UT><<<up, 256, 0, s>>>(k); break;
     }
 }
 
@@ -284,19 +427,23 @@ void launch_t(const LoraArgs& a, const LoraPlan& p, hipStream_t s) {
             lora_row_up_kernel<W, Y><<<dim3(m, static_cast<uint32_t>((a.N + 255) / 256)), 256, 0, s>>>(k);
             break;
         }
-        case 16: launch_tiles<X, W, Y, 1>(k, s); break;
-        default: launch_tiles<X, W, Y, 4>(k, s); break;
+        case 16: launch_tiles<X, W, Y, 16>(k, s); break;
+        case 32: launch_tiles<X, W, Y, 32>(k, s); break;
+        default:
+            if constexpr (sizeof(W) == 2) launch_tiles<X, W, Y, 64>(k, s);
+            break;
     }
 }
 
 }  // namespace
 
-LoraPlan plan_lora(int64_t M, int64_t K, int64_t R) {
+LoraPlan plan_lora(int64_t M, int64_t K, int64_t R, bool f32) {
     LoraPlan p;
     p.rank = (R + 15) / 16 * 16;
     if (p.rank == 48) p.rank = 64;
     if (p.rank > 64) p.rank = 128;
-    p.rows = M <= 64 ? 1 : M <= 2048 ? 16 : 64;
+    // the rank's and the rows' accumulators of a tile have to fit the registers, and float32 has three planes of each operand
+    p.rows = M <= 64 ? 1 : M <= 2048 || (f32 && R > 64) ? 16 : f32 || R > 64 ? 32 : 64;
     const int64_t tiles = (M + p.rows - 1) / p.rows;
     int64_t splits = 1;
     if (p.rows > 1)
