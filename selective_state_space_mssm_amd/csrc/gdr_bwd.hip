@@ -50,7 +50,9 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
-    const int64_t part = blockIdx.x % a.parts, head = blockIdx.x / a.parts, h = head % a.H, n = head / a.H;
+    const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
+    if (at.head >= a.N * a.H) return;
+    const int64_t part = at.part, n = at.head / static_cast<uint32_t>(a.H), h = at.head - n * a.H;
     const int64_t hg = h / (a.H / a.G);
     const int64_t vw = part * VC, v0 = vw + w * 16;
     const bool in_v = v0 < a.V;
@@ -85,8 +87,8 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
             bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_f, w, lane);
         } else {
             bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_f, w, lane);
-            fk.load(kp + chunk * kC * qk_stride, qk_stride, len, K, tid);
-            fq.load(qp + chunk * kC * qk_stride, qk_stride, len, K, tid);
+            fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
         }
     };
     if (chunks) fetch(chunks - 1, (chunks - 1) & 1);
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * rt + 4 * g + r;
-                        dy[rt][r] = t < len ? dyp[(chunk * kC + t) * v_stride + v0 + c] : 0.0f;
+                        dy[rt][r] = View<T>(dyp + chunk * kC * v_stride).one(t * static_cast<uint32_t>(v_stride) + static_cast<uint32_t>(v0) + c, t < len);
                     }
                 }
             }
@@ -226,11 +228,6 @@ struct StateTile {
     }
 };
 
-__device__ __forceinline__ f32x4 load_four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-__device__ __forceinline__ f32x4 load_four(const uint16_t* p) {
-    const u32x2 a = *reinterpret_cast<const u32x2*>(p);
-    return f32x4{bf16_lo(a[0]), bf16_hi(a[0]), bf16_lo(a[1]), bf16_hi(a[1])};
-}
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b, float s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = __builtin_fmaf(a[i], b[i], s);
@@ -264,17 +261,17 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
     const T* kp = static_cast<const T*>(a.k) + ch.start * qk_stride + hg * a.K;
     const T* qp = static_cast<const T*>(a.q) + ch.start * qk_stride + hg * a.K;
+    const View<T> k_rows(kp), q_rows(qp);
     const int row = 16 * w + c;  // this lane's token
     const bool in_t = row < ch.len;
+    const uint32_t row_at = row * static_cast<uint32_t>(qk_stride);
     float rk = 1.0f, rq = 1.0f;
     if (a.norm) {
         float k2 = 0.0f, q2 = 0.0f;
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
-            const bool in = in_t && 16 * m < K;
-            const f32x4 zero = {0, 0, 0, 0};
-            const f32x4 k4 = in ? load_four(kp + row * qk_stride + 16 * m + 4 * g) : zero;
-            const f32x4 q4 = in ? load_four(qp + row * qk_stride + 16 * m + 4 * g) : zero;
+            const f32x4 k4 = k_rows.four(row_at + 16 * m + 4 * g, in_t && 16 * m < K);
+            const f32x4 q4 = q_rows.four(row_at + 16 * m + 4 * g, in_t && 16 * m < K);
             k2 = dot4(k4, k4, k2);
             q2 = dot4(q4, q4, q2);
         }
@@ -289,9 +286,9 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
         tile_barrier();
     } else {
         FloatRows<KP, 256> rows;
-        rows.load(kp, qk_stride, ch.len, K, tid);
+        rows.load(kp, static_cast<uint32_t>(qk_stride), ch.len, K, tid);
         rows.store(lds_k, tid);
-        rows.load(qp, qk_stride, ch.len, K, tid);
+        rows.load(qp, static_cast<uint32_t>(qk_stride), ch.len, K, tid);
         rows.store(lds_q, tid);
     }
     f32x4 dq_sum[KM] = {}, dk_sum[KM] = {};
@@ -306,9 +303,9 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             s_lo[lane] = static_cast<float>(b - hi);
             s_beta[lane] = lane < ch.len ? a.beta[(ch.start + lane) * a.H + h] : 0.0f;
         }
-        const float *S = a.states + cell * a.V * a.K, *L = a.adjoints + cell * a.V * a.K;
-        const float *e = a.misses + cell * kC * a.V, *z = a.pulls + cell * kC * a.V;
-        const T* dy = static_cast<const T*>(a.dy) + ch.start * v_stride + h * a.V;
+        const View<float> S(a.states + cell * a.V * a.K), L(a.adjoints + cell * a.V * a.K);
+        const View<float> e(a.misses + cell * kC * a.V), z(a.pulls + cell * kC * a.V);
+        const View<T> dy(static_cast<const T*>(a.dy) + ch.start * v_stride + h * a.V);
 
         // sums over the value elements
         f32x4 yS[KM] = {}, zS[KM] = {}, uL[KM] = {}, dP[4] = {}, dA[4] = {};
@@ -322,9 +319,7 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const bool in = vb + 8 * o < V && kc < K;
-                        const f32x2 zero = {0, 0};
-                        const f32x2 s2 = in ? *reinterpret_cast<const f32x2*>(S + static_cast<int64_t>(vb + 8 * o + j) * K + kc) : zero;
-                        const f32x2 l2 = in ? *reinterpret_cast<const f32x2*>(L + static_cast<int64_t>(vb + 8 * o + j) * K + kc) : zero;
+                        const f32x2 s2 = S.two((vb + 8 * o + j) * K + kc, in), l2 = L.two((vb + 8 * o + j) * K + kc, in);
                         s0[j] = s2[0]; s1[j] = s2[1]; l0[j] = l2[0]; l1[j] = l2[1];
                         both = __builtin_fmaf(s2[0], l2[0], __builtin_fmaf(s2[1], l2[1], both));
                     }
@@ -341,9 +336,8 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             __syncthreads();
             const int v = vb + 8 * g;
             const bool in = v < V;
-            auto eight = [&](const float* p, int t, float (&x)[8]) {
-                const f32x4 zero = {0, 0, 0, 0};
-                const f32x4 lo = in ? load_four(p + t * a.V + v) : zero, hi = in ? load_four(p + t * a.V + v + 4) : zero;
+            auto eight = [&](const View<float>& p, int t, float (&x)[8]) {
+                const f32x4 lo = p.four(t * V + v, in), hi = p.four(t * V + v + 4, in);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
             };
@@ -353,7 +347,7 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
             const float beta = s_beta[row];
 #pragma unroll
             for (int i = 0; i < 8; ++i) dbeta = __builtin_fmaf(x[i], zz[i], dbeta), x[i] *= beta;
-            const Planes<PL> dyf = load_planes(dy + row * v_stride + v, in && in_t);
+            const Planes<PL> dyf = dy.planes(row * static_cast<uint32_t>(v_stride) + v, in && in_t);
             const Planes<3> zf = split<3>(zz), uf = split<3>(x);
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
@@ -408,9 +402,8 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
             const bool in = in_t && state_column(m, 4 * g) < K;
-            const f32x4 zero = {0, 0, 0, 0};
-            k4[m] = in ? rk * load_four(kp + row * qk_stride + state_column(m, 4 * g)) : zero;
-            q4[m] = in ? rq * load_four(qp + row * qk_stride + state_column(m, 4 * g)) : zero;
+            k4[m] = rk * k_rows.four(row_at + state_column(m, 4 * g), in);
+            q4[m] = rq * q_rows.four(row_at + state_column(m, 4 * g), in);
             dq[m] = fy * yS[m];
             dkr[m] = fz * zS[m];
             dkc[m] = to_end * uL[m];
@@ -472,10 +465,9 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     f32x4 k4[KM], q4[KM];
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
-        const bool in = in_t && state_column(m, 4 * g) < K;
-        const f32x4 zero = {0, 0, 0, 0};
-        k4[m] = in && a.norm ? rk * load_four(kp + row * qk_stride + state_column(m, 4 * g)) : zero;
-        q4[m] = in && a.norm ? rq * load_four(qp + row * qk_stride + state_column(m, 4 * g)) : zero;
+        const bool in = in_t && a.norm && state_column(m, 4 * g) < K;
+        k4[m] = rk * k_rows.four(row_at + state_column(m, 4 * g), in);
+        q4[m] = rq * q_rows.four(row_at + state_column(m, 4 * g), in);
         qd = dot4(q4[m], dq_sum[m], qd);
         kd = dot4(k4[m], dk_sum[m], kd);
     }
@@ -499,7 +491,7 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
     const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const AdjointArgs k{a.q, a.k, a.dy, a.offsets, a.mats, a.dh_final, a.dv, a.dh0, a.adjoints, a.pulls,
                         a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.factors, l.nt, l.pt};
-    gdr_adjoint_kernel<T, KP, NW><<<static_cast<uint32_t>(a.N * a.H * parts), NW * 64, 0, s>>>(k);
+    gdr_adjoint_kernel<T, KP, NW><<<xcd_grid(a.N * a.H, parts), NW * 64, 0, s>>>(k);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const GradArgs d{a.q, a.k, a.dy, a.g, a.beta, a.offsets, a.states, a.misses, a.adjoints, a.pulls, a.dq, a.dk, a.dg, a.dbeta,

@@ -69,18 +69,63 @@ __device__ __forceinline__ Chunk chunk_of(const int32_t* offsets, int64_t slot, 
     return {lo, s.start + t, static_cast<int>(imin64(kC, s.len - t))};
 }
 
+// The parts of a head's value elements read the same rows and matrices: on the same
+// XCD, which has its own L2.  Workgroups go to the 8 XCDs in turn, so of every 8 P
+// of them the x-th of each eight is a part of the x-th head; grids are whole eights
+// of heads.  (Heads next to each other stay on different XCDs: they are as long as
+// their sequence.)
+constexpr uint32_t kXcds = 8;
+__host__ __device__ __forceinline__ uint32_t xcd_grid(int64_t heads, int64_t parts) {
+    return static_cast<uint32_t>((heads + kXcds - 1) / kXcds * kXcds * parts);
+}
+struct HeadPart {
+    uint32_t head, part;
+};
+__device__ __forceinline__ HeadPart head_part(uint32_t parts) {
+    const uint32_t eight = blockIdx.x / kXcds, group = eight / parts;
+    return {group * kXcds + blockIdx.x % kXcds, eight - group * parts};
+}
+
 // ---- elements of rows ---------------------------------------------------------
 
-// Eight neighbouring elements as planes, or zeros.
-__device__ __forceinline__ Planes<1> load_planes(const uint16_t* p, bool in) {
-    Planes<1> out;
-    out.p[0] = in ? *reinterpret_cast<const u32x4*>(p) : u32x4{0, 0, 0, 0};
-    return out;
-}
-__device__ __forceinline__ Planes<3> load_planes(const float* p, bool in) {
-    const f32x4 zero = {0, 0, 0, 0};
-    return split<3>(in ? *reinterpret_cast<const f32x4*>(p) : zero, in ? *reinterpret_cast<const f32x4*>(p + 4) : zero);
-}
+// Memory from `base` on (the same for all lanes), read by element number; what is
+// not `in` reads as zeros.  By an offset outside of the buffer's range, not by a
+// branch: behind a branch around a load the compiler waits for it.
+template <typename T>
+struct View {
+    static constexpr uint32_t kOut = 0x7fffffffu, kBytes = 0x7ffffff0u;
+    __amdgpu_buffer_rsrc_t rsrc;
+    __device__ __forceinline__ explicit View(const T* base) : rsrc(make_rsrc(uniform_ptr(base), kBytes)) {}
+    __device__ __forceinline__ static uint32_t offset(uint32_t at, bool in) { return in ? at * static_cast<uint32_t>(sizeof(T)) : kOut - 15; }
+    __device__ __forceinline__ u32x4 words4(uint32_t at, bool in) const {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(at, in), 0, 0));
+    }
+    __device__ __forceinline__ u32x2 words2(uint32_t at, bool in) const {
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, offset(at, in), 0, 0));
+    }
+    __device__ __forceinline__ float one(uint32_t at, bool in) const {
+        if constexpr (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rsrc, offset(at, in), 0, 0))) << 16);
+        else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, offset(at, in), 0, 0));
+    }
+    __device__ __forceinline__ f32x2 two(uint32_t at, bool in) const {
+        static_assert(sizeof(T) == 4, "float32");
+        return __builtin_bit_cast(f32x2, words2(at, in));
+    }
+    __device__ __forceinline__ f32x4 four(uint32_t at, bool in) const {
+        if constexpr (sizeof(T) == 2) {
+            const u32x2 a = words2(at, in);
+            return f32x4{bf16_lo(a[0]), bf16_hi(a[0]), bf16_lo(a[1]), bf16_hi(a[1])};
+        } else {
+            return __builtin_bit_cast(f32x4, words4(at, in));
+        }
+    }
+    // eight neighbours as an operand
+    __device__ __forceinline__ Planes<kPlanes<T>> planes(uint32_t at, bool in) const {
+        if constexpr (sizeof(T) == 2) return Planes<1>{{words4(at, in)}};
+        else return split<3>(four(at, in), four(at + 4, in));
+    }
+};
+
 template <int N>
 __device__ __forceinline__ float sum_squares(const Planes<N>& x) {
     float s = 0.0f;
@@ -93,25 +138,6 @@ __device__ __forceinline__ float sum_squares(const Planes<N>& x) {
     }
     return s;
 }
-
-// Neighbouring values of a row in float32: two (one column of each of two tiles) or one.
-__device__ __forceinline__ void load_values(const float* p, float (&v)[2]) {
-    const f32x2 a = *reinterpret_cast<const f32x2*>(p);
-    v[0] = a[0]; v[1] = a[1];
-}
-__device__ __forceinline__ void load_values(const uint16_t* p, float (&v)[2]) {
-    const uint32_t a = *reinterpret_cast<const uint32_t*>(p);
-    v[0] = bf16_lo(a); v[1] = bf16_hi(a);
-}
-__device__ __forceinline__ void load_values(const float* p, float (&v)[1]) { v[0] = *p; }
-__device__ __forceinline__ void load_values(const uint16_t* p, float (&v)[1]) { v[0] = load_act(p, 0); }
-__device__ __forceinline__ void store_values(float* p, const float (&v)[2]) { *reinterpret_cast<f32x2*>(p) = f32x2{v[0], v[1]}; }
-__device__ __forceinline__ void store_values(uint16_t* p, const float (&v)[2]) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    *reinterpret_cast<bf16x2*>(p) = bf16x2{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1])};
-}
-__device__ __forceinline__ void store_values(float* p, const float (&v)[1]) { *p = v[0]; }
-__device__ __forceinline__ void store_values(uint16_t* p, const float (&v)[1]) { store_act(p, 0, v[0]); }
 
 // N (a multiple of 4) neighbouring values to a row.
 template <int N>
@@ -240,15 +266,14 @@ template <int W, int THREADS>
 struct FloatRows {
     static constexpr int kItems = kC * (W / 8) / THREADS;
     f32x4 lo[kItems], hi[kItems];
-    __device__ __forceinline__ void load(const float* rows, int64_t stride, int len, int width, int tid) {
+    __device__ __forceinline__ void load(const float* rows, uint32_t stride, int len, int width, int tid) {
+        const View<float> view(rows);
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int item = i * THREADS + tid, row = item / (W / 8), piece = item % (W / 8);
             const bool in = row < len && piece * 8 < width;
-            const float* p = rows + row * stride + piece * 8;
-            const f32x4 zero = {0, 0, 0, 0};
-            lo[i] = in ? *reinterpret_cast<const f32x4*>(p) : zero;
-            hi[i] = in ? *reinterpret_cast<const f32x4*>(p + 4) : zero;
+            lo[i] = view.four(row * stride + piece * 8, in);
+            hi[i] = view.four(row * stride + piece * 8 + 4, in);
         }
     }
     __device__ __forceinline__ void store(uint8_t* lds, int tid) {

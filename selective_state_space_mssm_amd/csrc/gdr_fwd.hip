@@ -8,6 +8,7 @@
 // of the one before.  The other operands, q, k and the chunk's matrices, are
 // shared by the waves of a workgroup.
 #include "gdr_common.h"
+#include <stdlib.h>
 
 namespace mssm {
 namespace {
@@ -44,7 +45,9 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
-    const int64_t part = blockIdx.x % a.parts, head = blockIdx.x / a.parts, h = head % a.H, n = head / a.H;
+    const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
+    if (at.head >= a.N * a.H) return;
+    const int64_t part = at.part, n = at.head / static_cast<uint32_t>(a.H), h = at.head - n * a.H;
     const int64_t hg = h / (a.H / a.G);
     const int64_t vw = part * VC, v0 = vw + w * 16;  // the workgroup's first value element, and the wave's
     const bool in_v = v0 < a.V;                      // V is a multiple of 16
@@ -79,8 +82,8 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_p, w, lane);
         } else {
             bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_n, w, lane);
-            fk.load(kp + chunk * kC * qk_stride, qk_stride, len, K, tid);
-            fq.load(qp + chunk * kC * qk_stride, qk_stride, len, K, tid);
+            fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
         }
     };
     f32x4 O[4];
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int t = 16 * rt + 4 * g + r;
-                    val[rt][r] = t < len ? vp[(chunk * kC + t) * v_stride + v0 + c] : 0.0f;
+                    val[rt][r] = View<T>(vp + chunk * kC * v_stride).one(t * static_cast<uint32_t>(v_stride) + static_cast<uint32_t>(v0) + c, t < len);
                 }
             }
         }
@@ -208,21 +211,273 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     }
 }
 
+// The rows of tile rt as half of an operand summed over the tokens, in planes.
+template <int N>
+__device__ __forceinline__ void put_half(uint8_t* area, int rt, f32x4 x, int lane) {
+    uint8_t* to = area + (rt >> 1) * N * 1024 + lane * 16 + (rt & 1) * 8;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        *reinterpret_cast<u32x2*>(to + n * 1024) = u32x2{upper_halves(x[0], x[1]), upper_halves(x[2], x[3])};
+        if (n + 1 < N) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] -= upper_part(x[r]);
+        }
+    }
+}
+
+// ---- few columns: the waves of a workgroup share a tile of 16 ------------------------
+
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// One tile of 16 columns a workgroup, bfloat16.  What the next chunk waits for is
+// cut over KS waves: each has 32 key elements of the state, multiplies its part of
+// S k, and after an exchange through LDS has a part of the rows of e and u.  Four
+// other waves fetch the chunks and compute y, one step behind.
+template <int KP, bool TRAIN>
+__global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdArgs a) {
+    constexpr int KS = KP / 32, RPW = 4 / KS, PP = 2;  // RPW: row tiles of a chain wave
+    typedef Tile<KP> Keys;
+    constexpr int kPm = PP * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
+    constexpr int kMats = kPm + kN + kF, kPart = 2 * Keys::kBytes + kMats;
+    constexpr int kX = KS * 4 * 1024, kS = KS * PP * 1024, kM = 2 * 3 * 1024;
+    static_assert(2 * (3 + PP) * 1024 <= (kX > 10240 ? kX : 10240), "u lies where the sums were");
+    constexpr int kXU = kX > 10240 ? kX : 10240;
+    __shared__ __align__(16) uint8_t lds[2 * kPart + kXU + kS + kM];
+    static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
+    uint8_t *s_x = lds + 2 * kPart, *s_ud = s_x, *s_u = s_ud + 2 * 3 * 1024, *s_s = s_x + kXU, *s_m = s_s + kS;
+    const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
+    const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
+    if (at.head >= a.N * a.H) return;
+    const int64_t part = at.part, n = at.head / static_cast<uint32_t>(a.H), h = at.head - n * a.H;
+    const int64_t hg = h / (a.H / a.G), v0 = part * 16;
+    const Span sp = span_of(a.offsets, n, a.T, a.each);
+    const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
+    const int K = static_cast<int>(a.K);
+    const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
+    auto length = [&](int64_t chunk) { return static_cast<int>(imin64(kC, sp.len - chunk * kC)); };
+    auto piece = [&](uint8_t* area, int i) { return reinterpret_cast<u32x4*>(area + i * 1024 + lane * 16); };
+
+    if (w < KS) {
+        f32x4 S[2];
+        const int64_t state = ((n * a.H + h) * a.V + v0 + c) * a.K;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int col = state_column(2 * w + m, 4 * g);
+            S[m] = f32x4{0, 0, 0, 0};
+            if (a.h0 && col < K) S[m] = *reinterpret_cast<const f32x4*>(a.h0 + state + col);
+        }
+        const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sp.start * v_stride + h * a.V + v0;
+        f32x4 val[RPW];
+        auto values = [&](int64_t chunk) {
+            const int len = length(chunk);
+            const View<uint16_t> view(vp + chunk * kC * v_stride);
+#pragma unroll
+            for (int i = 0; i < RPW; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * (w * RPW + i) + 4 * g + r;
+                    val[i][r] = view.one(t * static_cast<uint32_t>(v_stride) + c, t < len);
+                }
+        };
+        if (chunks) values(0);
+        for (int64_t chunk = 0; chunk < chunks; ++chunk) {
+            const uint8_t* in = lds + (chunk & 1) * kPart;
+            const uint8_t* lds_n = in + 2 * Keys::kBytes + kPm;
+            const float* f = reinterpret_cast<const float*>(lds_n + kN);
+            const Planes<3> st = split<3>(S[0], S[1]);
+            if constexpr (TRAIN) {
+                float* to = a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int col = state_column(2 * w + m, 4 * g);
+                    if (col < K) *reinterpret_cast<f32x4*>(to + col) = S[m];
+                }
+            }
+            lds_barrier();  // the chunk is there, and what LDS holds of the one before is read
+#pragma unroll
+            for (int i = 0; i < PP; ++i) *piece(s_s, w * PP + i) = st.p[i];
+            f32x4 X[4] = {};
+            {
+                Planes<1> kf[4];
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) kf[rt] = Keys::template rows<1>(in, rt, w, c, g);
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) X[rt] = mma(kf[rt], st, X[rt]);
+            }
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) *reinterpret_cast<f32x4*>(piece(s_x, w * 4 + rt)) = X[rt];
+            f32x4 ek[RPW], beta[RPW], ed[RPW];
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const float* p = f + 16 * (w * RPW + i) + 4 * g;
+                ek[i] = *reinterpret_cast<const f32x4*>(p);
+                beta[i] = *reinterpret_cast<const f32x4*>(p + kC);
+                ed[i] = *reinterpret_cast<const f32x4*>(p + 2 * kC);
+            }
+            const float last = f[4 * kC];
+            Planes<3> nb[RPW][2];
+#pragma unroll
+            for (int i = 0; i < RPW; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int rt = w * RPW + i;
+                    nb[i][s] = load_block<3>(lds_n, rt < 2 ? rt : 2 * rt - 2 + s, lane);  // s = 1: for the lower rows only
+                }
+            lds_barrier();
+            f32x4 e[RPW];
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const int rt = w * RPW + i;
+                f32x4 x = *reinterpret_cast<const f32x4*>(piece(s_x, rt));
+#pragma unroll
+                for (int q = 1; q < KS; ++q) x += *reinterpret_cast<const f32x4*>(piece(s_x, q * 4 + rt));
+                e[i] = val[i] - ek[i] * x;
+                const f32x4 b = beta[i] * e[i];
+                put_half<3>(s_m, rt, b, lane);
+            }
+            if (chunk + 1 < chunks) values(chunk + 1);
+            lds_barrier();
+            {
+                Planes<3> m[2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) m[s].p[i] = *piece(s_m, s * 3 + i);
+#pragma unroll
+                for (int i = 0; i < RPW; ++i) {
+                    const int rt = w * RPW + i;
+                    f32x4 more = {0, 0, 0, 0};
+                    e[i] = mma(nb[i][0], m[0], e[i]);
+                    if (rt >= 2) more = mma(nb[i][1], m[1], more);
+                    e[i] += more;
+                }
+            }
+            Planes<1> kt[2][2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) kt[s][m] = Keys::template columns<1>(in, 2 * w + m, s, c, g);
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const f32x4 u = beta[i] * e[i];
+                put_half<3>(s_ud, w * RPW + i, ed[i] * u, lane);
+                put_half<PP>(s_u, w * RPW + i, u, lane);
+            }
+            if constexpr (TRAIN) {
+                float* to = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
+#pragma unroll
+                for (int i = 0; i < RPW; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) to[(16 * (w * RPW + i) + 4 * g + r) * a.V] = e[i][r];
+            }
+            lds_barrier();
+            Planes<3> ud[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) ud[s].p[i] = *piece(s_ud, s * 3 + i);
+            f32x4 more[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                more[m] = mma(kt[1][m], ud[1], f32x4{0, 0, 0, 0});
+                S[m] = mma(kt[0][m], ud[0], last * S[m]);
+            }
+            S[0] += more[0];
+            S[1] += more[1];
+        }
+        if (a.h_final) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int col = state_column(2 * w + m, 4 * g);
+                if (col < K) *reinterpret_cast<f32x4*>(a.h_final + state + col) = S[m];
+            }
+        }
+    } else {
+        const int rt = w - KS;
+        const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sp.start * qk_stride + hg * a.K;
+        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sp.start * qk_stride + hg * a.K;
+        uint16_t* yp = static_cast<uint16_t*>(a.y) + sp.start * v_stride + h * a.V + v0 + 4 * g;
+        auto fetch = [&](int64_t chunk) {
+            const int len = length(chunk);
+            const uint32_t to = lds_offset(lds + (chunk & 1) * kPart);
+            rows_to_lds<KP, 4>(to, kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, rt, lane);
+            rows_to_lds<KP, 4>(to + Keys::kBytes, qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, rt, lane);
+            bytes_to_lds<4, kMats>(to + 2 * Keys::kBytes, a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes + a.at_p, rt, lane);
+        };
+        f32x4 O;
+        auto put_y = [&](int64_t chunk) {
+            const int t = 16 * rt + c;
+            const float out[4] = {O[0], O[1], O[2], O[3]};
+            if (a.y && t < length(chunk)) store_row(yp + (chunk * kC + t) * v_stride, out);
+        };
+        if (chunks) fetch(0);
+        for (int64_t chunk = 0; chunk < chunks; ++chunk) {
+            const uint8_t* in = lds + (chunk & 1) * kPart;
+            const uint8_t *lds_q = in + Keys::kBytes, *lds_p = lds_q + Keys::kBytes;
+            const float* f = reinterpret_cast<const float*>(lds_p + kPm + kN);
+            tile_barrier();
+            if (chunk) put_y(chunk - 1);
+            if (chunk + 1 < chunks) fetch(chunk + 1);
+            Planes<1> qf[KS];
+            Planes<PP> pb[2];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qf[s] = Keys::template rows<1>(lds_q, rt, s, c, g);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) pb[s] = load_block<PP>(lds_p, rt < 2 ? rt : 2 * rt - 2 + s, lane);
+            const float eq = f[3 * kC + 16 * rt + c];
+            lds_barrier();
+            O = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Planes<PP> st;
+#pragma unroll
+                for (int i = 0; i < PP; ++i) st.p[i] = *piece(s_s, s * PP + i);
+                O = mma(st, qf[s], O);
+            }
+            O *= eq;
+            lds_barrier();
+            lds_barrier();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s && rt < 2) break;
+                Planes<PP> u;
+#pragma unroll
+                for (int i = 0; i < PP; ++i) u.p[i] = *piece(s_u, s * PP + i);
+                O = mma(u, pb[s], O);
+            }
+        }
+        if (chunks) put_y(chunks - 1);
+    }
+}
+
 template <typename T, int KP, int NW, bool TRAIN>
 hipError_t launch_v(const GdrArgs& a, hipStream_t s) {
     const GdrLayout l(a.dtype, a.train);
     const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const FwdArgs k{a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
                     a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors};
-    gdr_fwd_kernel<T, KP, NW, TRAIN><<<static_cast<uint32_t>(a.N * a.H * parts), NW * 64, 0, s>>>(k);
+    gdr_fwd_kernel<T, KP, NW, TRAIN><<<xcd_grid(a.N * a.H, parts), NW * 64, 0, s>>>(k);
     return hipGetLastError();
 }
 template <typename T, int KP, int NW>
 hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
     return a.train ? launch_v<T, KP, NW, true>(a, s) : launch_v<T, KP, NW, false>(a, s);
 }
+template <int KP>
+hipError_t launch_narrow(const GdrArgs& a, hipStream_t s) {
+    const GdrLayout l(a.dtype, a.train);
+    const FwdArgs k{a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
+                    a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, a.V / 16, l.bytes, l.n, l.pm, l.factors};
+    const uint32_t blocks = xcd_grid(a.N * a.H, a.V / 16);
+    if (a.train) gdr_fwd_narrow_kernel<KP, true><<<blocks, 64 * (KP / 32 + 4), 0, s>>>(k);
+    else gdr_fwd_narrow_kernel<KP, false><<<blocks, 64 * (KP / 32 + 4), 0, s>>>(k);
+    return hipGetLastError();
+}
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (getenv("GDR_NARROW") ? atoi(getenv("GDR_NARROW")) : a.N * a.H < 64) return launch_narrow<KP>(a, s);
+    }
     if constexpr (sizeof(T) == 2 || KP == 64) {  // eight waves have 256 registers each, too few for float32 planes of 128
         if (a.V > 64 && a.N * a.H >= 128) return launch_c<T, KP, 8>(a, s);
     }

@@ -119,7 +119,7 @@ __device__ __forceinline__ void solve(f32x4 (&x)[4], float beta) {
 constexpr int kWaves = 4;
 
 template <typename T, int KS, bool TRAIN>
-__global__ __launch_bounds__(64 * kWaves, 2) void gdr_prep_kernel(PrepArgs a) {
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && TRAIN ? 1 : 2) void gdr_prep_kernel(PrepArgs a) {
     constexpr int PL = kPlanes<T>, PP = sizeof(T) == 2 ? 2 : 3;
     __shared__ __align__(16) float shared[kWaves][8][kC];
     const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
@@ -140,8 +140,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void gdr_prep_kernel(PrepArgs a) {
     float k2[4] = {}, q2[4] = {};
     {
         const uint32_t stride = a.G * a.K;
-        const T* k0 = static_cast<const T*>(a.k) + ch.start * stride + hg * a.K;
-        const T* q0 = static_cast<const T*>(a.q) + ch.start * stride + hg * a.K;
+        const View<T> k0(static_cast<const T*>(a.k) + ch.start * stride + hg * a.K);
+        const View<T> q0(static_cast<const T*>(a.q) + ch.start * stride + hg * a.K);
 #pragma unroll 1
         for (int s = 0; s < KS; ++s) {
             if (s * 32u >= a.K) break;
@@ -150,8 +150,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void gdr_prep_kernel(PrepArgs a) {
             for (int t = 0; t < 4; ++t) {
                 const uint32_t row = 16 * t + c, col = s * 32 + 8 * g;
                 const bool in = static_cast<int>(row) < ch.len && col < a.K;
-                kf[t] = load_planes(k0 + row * stride + col, in);
-                qf[t] = load_planes(q0 + row * stride + col, in);
+                kf[t] = k0.planes(row * stride + col, in);
+                qf[t] = q0.planes(row * stride + col, in);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
