@@ -75,15 +75,16 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     T* dvp = static_cast<T*>(a.dv) + sp.start * v_stride + h * a.V + v0 + c;
     auto length = [&](int64_t chunk) { return static_cast<int>(imin64(kC, sp.len - chunk * kC)); };
     auto mats_of = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes; };
+    const RowsToLds<KP, NW> key_loads(static_cast<uint32_t>(qk_stride), K, w, lane);
+    const RowsToLds<VC, NW> value_loads(static_cast<uint32_t>(v_stride), static_cast<int>(a.V - vw), w, lane);
     FloatRows<KP, NW * 64> fk, fq;
     auto fetch = [&](int64_t chunk, int half) {
         const int len = length(chunk);
         uint8_t* to = lds + half * kPart;
         if constexpr (B16) {
-            rows_to_lds<KP, NW>(lds_offset(to), kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
-            rows_to_lds<KP, NW>(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
-            rows_to_lds<VC, NW>(lds_offset(to) + kKeys, dyp + vw + chunk * kC * v_stride, static_cast<uint32_t>(v_stride), len,
-                                static_cast<int>(a.V - vw), w, lane);
+            key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
+            key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
+            value_loads.load(lds_offset(to) + kKeys, dyp + vw + chunk * kC * v_stride, len, w);
             bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_f, w, lane);
         } else {
             bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_f, w, lane);
@@ -281,8 +282,9 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     if (g == 0) s_rk[row] = rk, s_rq[row] = rq;
 
     if constexpr (sizeof(T) == 2) {
-        rows_to_lds<KP, 4>(lds_offset(lds_k), kp, static_cast<uint32_t>(qk_stride), ch.len, K, w, lane);
-        rows_to_lds<KP, 4>(lds_offset(lds_q), qp, static_cast<uint32_t>(qk_stride), ch.len, K, w, lane);
+        const RowsToLds<KP, 4> loads(static_cast<uint32_t>(qk_stride), K, w, lane);
+        loads.load(lds_offset(lds_k), kp, ch.len, w);
+        loads.load(lds_offset(lds_q), qp, ch.len, w);
         tile_barrier();
     } else {
         FloatRows<KP, 256> rows;

@@ -236,30 +236,43 @@ __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
         (__attribute__((address_space(3))) const uint8_t*)(p))));
 }
 
-// bfloat16 rows from memory straight to a tile, by NW waves; rows from `len` and
-// columns from `width` on become zeros.
+// bfloat16 rows from memory straight to a tile, by NW waves; rows from a chunk's
+// length on and columns from `width` on become zeros.  What does not change from
+// chunk to chunk is computed once: a chunk's loads cost a few instructions each.
 template <int W, int NW>
-__device__ __forceinline__ void rows_to_lds(uint32_t lds, const uint16_t* rows, uint32_t stride, int len, int width, int w, int lane) {
-    constexpr int kPieces = Tile<W>::kPieces, kRows = 64 / kPieces;  // rows of one instruction
-    const i32x4 rsrc = buffer_words(rows, 0x7ffffff0u);
+struct RowsToLds {
+    static constexpr int kPieces = Tile<W>::kPieces, kRows = 64 / kPieces, kLoads = kC / kRows / NW;  // rows of a load
+    uint32_t at[kLoads];  // byte offsets of the lane's pieces
+    int row[kLoads];
+    __device__ __forceinline__ RowsToLds(uint32_t stride, int width, int w, int lane) {
 #pragma unroll
-    for (int i = 0; i < kC / kRows / NW; ++i) {
-        const int first = (i * NW + w) * kRows, row = first + lane / kPieces, piece = lane % kPieces ^ Tile<W>::turn(row);
-        const uint32_t at = row < len && piece * 8 < width ? row * stride + piece * 8 : 0x3fffffffu;
-        load_to_lds(lds + first * Tile<W>::kRow, rsrc, at * 2, 0);
+        for (int i = 0; i < kLoads; ++i) {
+            row[i] = (i * NW + w) * kRows + lane / kPieces;
+            const int piece = lane % kPieces ^ Tile<W>::turn(row[i]);
+            at[i] = piece * 8 < width ? (row[i] * stride + piece * 8) * 2 : 0x7ffffffeu;
+        }
     }
-}
+    __device__ __forceinline__ void load(uint32_t lds, const uint16_t* rows, int len, int w) const {
+        const i32x4 rsrc = buffer_words(rows, 0x7ffffff0u);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            load_to_lds(lds + (i * NW + w) * kRows * Tile<W>::kRow, rsrc, row[i] < len ? at[i] : 0x7ffffffeu, 0);
+    }
+};
 // `bytes` (a multiple of 16) from memory straight to LDS, by NW waves.
 template <int NW, int bytes>
 __device__ __forceinline__ void bytes_to_lds(uint32_t lds, const uint8_t* from, int w, int lane) {
-    const i32x4 rsrc = buffer_words(from, bytes);
+    const i32x4 rsrc = buffer_words(from, bytes);  // each load ends within
 #pragma unroll
     for (int i = 0; i < (bytes + 1024 * NW - 1) / (1024 * NW); ++i) {
         const int at = (i * NW + w) * 1024;
-        if (at + 1024 <= bytes) load_to_lds(lds + at, rsrc, at + lane * 16, 0);
-        else if (at + lane * 16 < bytes) load_to_lds(lds + at, rsrc, at + lane * 16, 0);  // the lanes of the last piece
+        if (at + 1024 <= bytes) load_to_lds(lds + at, rsrc, lane * 16, at);
+        else if (at + lane * 16 < bytes) load_to_lds(lds + at, rsrc, lane * 16, at);  // the lanes of the last piece
     }
 }
+// Waits until at most N of the wave's loads and stores, the last ones, are under way.
+template <int N>
+__device__ __forceinline__ void wait_memory() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 // float32 rows on their way to a tile's planes: a thread's pieces, held from the loads' issue to the stores.
 template <int W, int THREADS>

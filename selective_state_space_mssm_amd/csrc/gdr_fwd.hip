@@ -70,15 +70,16 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     T* yp = static_cast<T*>(a.y) + sp.start * v_stride + h * a.V + v0 + 4 * g;
     auto length = [&](int64_t chunk) { return static_cast<int>(imin64(kC, sp.len - chunk * kC)); };
     auto mats_of = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes; };
+    const RowsToLds<KP, NW> key_loads(static_cast<uint32_t>(qk_stride), K, w, lane);
+    const RowsToLds<VC, NW> value_loads(static_cast<uint32_t>(v_stride), static_cast<int>(a.V - vw), w, lane);
     FloatRows<KP, NW * 64> fk, fq;
     auto fetch = [&](int64_t chunk, int half) {
         const int len = length(chunk);
         uint8_t* to = lds + half * kPart;
         if constexpr (B16) {
-            rows_to_lds<KP, NW>(lds_offset(to), kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
-            rows_to_lds<KP, NW>(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, w, lane);
-            rows_to_lds<VC, NW>(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, static_cast<uint32_t>(v_stride), len,
-                                static_cast<int>(a.V - vw), w, lane);
+            key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
+            key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
+            value_loads.load(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, len, w);
             bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_p, w, lane);
         } else {
             bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_n, w, lane);
@@ -232,16 +233,18 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // One tile of 16 columns a workgroup, bfloat16.  What the next chunk waits for is
 // cut over KS waves: each has 32 key elements of the state, multiplies its part of
 // S k, and after an exchange through LDS has a part of the rows of e and u.  Four
-// other waves fetch the chunks and compute y, one step behind.
+// other waves fetch the chunks and compute y.  A compute unit takes 1 KB into LDS
+// in about 30 cycles, 65 KB a chunk in 2,000, which would hold up every other
+// access to memory and each barrier behind it: a fourth of a chunk's loads is
+// issued between each two barriers, in the order in which they are needed.
 template <int KP, bool TRAIN>
 __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdArgs a) {
     constexpr int KS = KP / 32, RPW = 4 / KS, PP = 2;  // RPW: row tiles of a chain wave
     typedef Tile<KP> Keys;
     constexpr int kPm = PP * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
-    constexpr int kMats = kPm + kN + kF, kPart = 2 * Keys::kBytes + kMats;
-    constexpr int kX = KS * 4 * 1024, kS = KS * PP * 1024, kM = 2 * 3 * 1024;
-    static_assert(2 * (3 + PP) * 1024 <= (kX > 10240 ? kX : 10240), "u lies where the sums were");
-    constexpr int kXU = kX > 10240 ? kX : 10240;
+    constexpr int kV = kC * 32, kPart = 2 * Keys::kBytes + kPm + kN + kF + kV;
+    constexpr int kX = KS * (4 - RPW) * 1024, kS = KS * PP * 1024, kM = 2 * 3 * 1024;
+    constexpr int kU = 2 * (3 + PP) * 1024, kXU = kX > kU ? kX : kU;  // u lies where the sums were
     __shared__ __align__(16) uint8_t lds[2 * kPart + kXU + kS + kM];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     uint8_t *s_x = lds + 2 * kPart, *s_ud = s_x, *s_u = s_ud + 2 * 3 * 1024, *s_s = s_x + kXU, *s_m = s_s + kS;
@@ -258,6 +261,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
     auto piece = [&](uint8_t* area, int i) { return reinterpret_cast<u32x4*>(area + i * 1024 + lane * 16); };
 
     if (w < KS) {
+        __builtin_amdgcn_s_setprio(2);
         f32x4 S[2];
         const int64_t state = ((n * a.H + h) * a.V + v0 + c) * a.K;
 #pragma unroll
@@ -266,24 +270,11 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
             S[m] = f32x4{0, 0, 0, 0};
             if (a.h0 && col < K) S[m] = *reinterpret_cast<const f32x4*>(a.h0 + state + col);
         }
-        const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sp.start * v_stride + h * a.V + v0;
-        f32x4 val[RPW];
-        auto values = [&](int64_t chunk) {
-            const int len = length(chunk);
-            const View<uint16_t> view(vp + chunk * kC * v_stride);
-#pragma unroll
-            for (int i = 0; i < RPW; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * (w * RPW + i) + 4 * g + r;
-                    val[i][r] = view.one(t * static_cast<uint32_t>(v_stride) + c, t < len);
-                }
-        };
-        if (chunks) values(0);
         for (int64_t chunk = 0; chunk < chunks; ++chunk) {
             const uint8_t* in = lds + (chunk & 1) * kPart;
             const uint8_t* lds_n = in + 2 * Keys::kBytes + kPm;
             const float* f = reinterpret_cast<const float*>(lds_n + kN);
+            const uint8_t* lds_v = lds_n + kN + kF;
             const Planes<3> st = split<3>(S[0], S[1]);
             if constexpr (TRAIN) {
                 float* to = a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K;
@@ -294,26 +285,45 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
                 }
             }
             lds_barrier();  // the chunk is there, and what LDS holds of the one before is read
-#pragma unroll
-            for (int i = 0; i < PP; ++i) *piece(s_s, w * PP + i) = st.p[i];
             f32x4 X[4] = {};
             {
                 Planes<1> kf[4];
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) kf[rt] = Keys::template rows<1>(in, rt, w, c, g);
 #pragma unroll
+                for (int i = 0; i < PP; ++i) *piece(s_s, w * PP + i) = st.p[i];
+#pragma unroll
                 for (int rt = 0; rt < 4; ++rt) X[rt] = mma(kf[rt], st, X[rt]);
             }
+            // the other waves' rows; a wave's own stay with it
+            auto from = [&](int q, int rt) { return piece(s_x, q * (4 - RPW) + (rt < q * RPW ? rt : rt - RPW)); };
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) *reinterpret_cast<f32x4*>(piece(s_x, w * 4 + rt)) = X[rt];
-            f32x4 ek[RPW], beta[RPW], ed[RPW];
+            for (int rt = 0; rt < 4; ++rt)
+                if (rt / RPW != w) *reinterpret_cast<f32x4*>(from(w, rt)) = X[rt];
+            lds_barrier();
+            f32x4 own[RPW], part_x[RPW][KS];
 #pragma unroll
             for (int i = 0; i < RPW; ++i) {
-                const float* p = f + 16 * (w * RPW + i) + 4 * g;
+                own[i] = w == 0 ? X[i] : w == 1 ? X[RPW + i] : w == 2 ? X[2 * RPW + i & 3] : X[3 * RPW + i & 3];
+#pragma unroll
+                for (int q = 0; q < KS; ++q) part_x[i][q] = *reinterpret_cast<const f32x4*>(from(q == w ? (q + 1) % KS : q, w * RPW + i));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 ek[RPW], beta[RPW], ed[RPW];
+            u32x2 val[RPW];
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const int rt = w * RPW + i;
+                const float* p = f + 16 * rt + 4 * g;
                 ek[i] = *reinterpret_cast<const f32x4*>(p);
                 beta[i] = *reinterpret_cast<const f32x4*>(p + kC);
                 ed[i] = *reinterpret_cast<const f32x4*>(p + 2 * kC);
+                // values: four of the wave's rows, 32 bytes each
+                typedef short s16x4 __attribute__((ext_vector_type(4)));
+                val[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+                    lds_v + (16 * rt + 4 * g + (c >> 2)) * 32 + (c & 3) * 8)));
             }
+            // what the steps behind the exchanges need, on its way during them
             const float last = f[4 * kC];
             Planes<3> nb[RPW][2];
 #pragma unroll
@@ -323,19 +333,23 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
                     const int rt = w * RPW + i;
                     nb[i][s] = load_block<3>(lds_n, rt < 2 ? rt : 2 * rt - 2 + s, lane);  // s = 1: for the lower rows only
                 }
-            lds_barrier();
+            Planes<1> kt[2][2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) kt[s][m] = Keys::template columns<1>(in, 2 * w + m, s, c, g);
+            __builtin_amdgcn_sched_barrier(0);
             f32x4 e[RPW];
 #pragma unroll
             for (int i = 0; i < RPW; ++i) {
                 const int rt = w * RPW + i;
-                f32x4 x = *reinterpret_cast<const f32x4*>(piece(s_x, rt));
+                f32x4 x = own[i];
 #pragma unroll
-                for (int q = 1; q < KS; ++q) x += *reinterpret_cast<const f32x4*>(piece(s_x, q * 4 + rt));
-                e[i] = val[i] - ek[i] * x;
+                for (int q = 0; q < KS; ++q) x += q == w ? f32x4{0, 0, 0, 0} : part_x[i][q];
+                e[i] = f32x4{bf16_lo(val[i][0]), bf16_hi(val[i][0]), bf16_lo(val[i][1]), bf16_hi(val[i][1])} - ek[i] * x;
                 const f32x4 b = beta[i] * e[i];
                 put_half<3>(s_m, rt, b, lane);
             }
-            if (chunk + 1 < chunks) values(chunk + 1);
             lds_barrier();
             {
                 Planes<3> m[2];
@@ -352,11 +366,6 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
                     e[i] += more;
                 }
             }
-            Planes<1> kt[2][2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) kt[s][m] = Keys::template columns<1>(in, 2 * w + m, s, c, g);
 #pragma unroll
             for (int i = 0; i < RPW; ++i) {
                 const f32x4 u = beta[i] * e[i];
@@ -397,27 +406,53 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
         const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sp.start * qk_stride + hg * a.K;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sp.start * qk_stride + hg * a.K;
         uint16_t* yp = static_cast<uint16_t*>(a.y) + sp.start * v_stride + h * a.V + v0 + 4 * g;
-        auto fetch = [&](int64_t chunk) {
-            const int len = length(chunk);
-            const uint32_t to = lds_offset(lds + (chunk & 1) * kPart);
-            rows_to_lds<KP, 4>(to, kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, rt, lane);
-            rows_to_lds<KP, 4>(to + Keys::kBytes, qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, rt, lane);
-            bytes_to_lds<4, kMats>(to + 2 * Keys::kBytes, a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes + a.at_p, rt, lane);
+        const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sp.start * v_stride + h * a.V + v0;
+        const RowsToLds<KP, 4> loads(static_cast<uint32_t>(qk_stride), K, rt, lane);
+        // Of a chunk the keys come first; the wave's kOthers loads behind them nobody
+        // needs before the second barrier.
+        constexpr int kKeyLoads = RowsToLds<KP, 4>::kLoads, kOthers = kKeyLoads + (kN + kF + 4095) / 4096 + kPm / 4096;
+        auto to_half = [&](int64_t chunk) { return lds_offset(lds + (chunk & 1) * kPart); };
+        auto mats = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes + a.at_p; };
+        auto fetch_k = [&](int64_t chunk) { loads.load(to_half(chunk), kp + chunk * kC * qk_stride, length(chunk), rt); };
+        auto fetch_n = [&](int64_t chunk) {
+            const uint32_t to = to_half(chunk) + 2 * Keys::kBytes + kPm;
+            if (rt < 2) {  // two lanes a row
+                const int row = 32 * rt + lane / 2;
+                load_to_lds(to + kN + kF + rt * 1024, buffer_words(vp + chunk * kC * v_stride, 0x7ffffff0u),
+                            row < length(chunk) ? (row * static_cast<uint32_t>(v_stride) + lane % 2 * 8) * 2 : 0x7ffffffeu, 0);
+            }
+            bytes_to_lds<4, kN + kF>(to, mats(chunk) + kPm, rt, lane);
         };
+        auto fetch_q = [&](int64_t chunk) { loads.load(to_half(chunk) + Keys::kBytes, qp + chunk * kC * qk_stride, length(chunk), rt); };
+        auto fetch_p = [&](int64_t chunk) { bytes_to_lds<4, kPm>(to_half(chunk) + 2 * Keys::kBytes, mats(chunk), rt, lane); };
         f32x4 O;
         auto put_y = [&](int64_t chunk) {
             const int t = 16 * rt + c;
             const float out[4] = {O[0], O[1], O[2], O[3]};
             if (a.y && t < length(chunk)) store_row(yp + (chunk * kC + t) * v_stride, out);
         };
-        if (chunks) fetch(0);
+        if (chunks) {
+            fetch_k(0);
+            fetch_q(0);
+            fetch_n(0);
+            fetch_p(0);
+        }
         for (int64_t chunk = 0; chunk < chunks; ++chunk) {
             const uint8_t* in = lds + (chunk & 1) * kPart;
             const uint8_t *lds_q = in + Keys::kBytes, *lds_p = lds_q + Keys::kBytes;
             const float* f = reinterpret_cast<const float*>(lds_p + kPm + kN);
-            tile_barrier();
-            if (chunk) put_y(chunk - 1);
-            if (chunk + 1 < chunks) fetch(chunk + 1);
+            const bool more = chunk + 1 < chunks;
+            wait_memory<kOthers>();
+            lds_barrier();
+            if (more) {
+                fetch_k(chunk + 1);
+                wait_memory<kKeyLoads>();
+            } else {
+                wait_memory<0>();
+            }
+            lds_barrier();
+            if (chunk) put_y(chunk - 1);  // not earlier: the waits above would be for it too
+            if (more) fetch_q(chunk + 1);
             Planes<1> qf[KS];
             Planes<PP> pb[2];
 #pragma unroll
@@ -425,7 +460,6 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
 #pragma unroll
             for (int s = 0; s < 2; ++s) pb[s] = load_block<PP>(lds_p, rt < 2 ? rt : 2 * rt - 2 + s, lane);
             const float eq = f[3 * kC + 16 * rt + c];
-            lds_barrier();
             O = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -436,7 +470,9 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
             }
             O *= eq;
             lds_barrier();
+            if (more) fetch_n(chunk + 1);
             lds_barrier();
+            if (more) fetch_p(chunk + 1);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (s && rt < 2) break;
