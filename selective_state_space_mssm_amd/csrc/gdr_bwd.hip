@@ -37,7 +37,9 @@ struct AdjointArgs {
     int64_t mat_bytes, at_f, at_nt, at_pt;
 };
 
-// The chain: as gdr_fwd_kernel, which see for its waves, LDS and lanes; Pᵀ comes from memory.
+// The chain: as gdr_fwd_kernel, which see for its waves, LDS and lanes.  Pᵀ is in LDS
+// once (bfloat16), from the barrier behind its use on the next chunk's, or comes from
+// memory.
 template <typename T, int KP, int NW>
 __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     constexpr bool B16 = sizeof(T) == 2;
@@ -47,7 +49,7 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     constexpr int kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4, kMats = kF + kN;
     constexpr int kKeys = 2 * PL * Keys::kBytes;
     constexpr int kPart = B16 ? kKeys + Values::kBytes + kMats : kMats;
-    __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
+    __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? kN : kKeys)];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
@@ -72,27 +74,35 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
     const T* kp = static_cast<const T*>(a.k) + sp.start * qk_stride + hg * a.K;
     const T* qp = static_cast<const T*>(a.q) + sp.start * qk_stride + hg * a.K;
     const T* dyp = static_cast<const T*>(a.dy) + sp.start * v_stride + h * a.V;
-    T* dvp = static_cast<T*>(a.dv) + sp.start * v_stride + h * a.V + v0 + c;
+    T* dvp = static_cast<T*>(a.dv) + sp.start * v_stride + h * a.V + v0 + (c & ~3);
     auto length = [&](int64_t chunk) { return static_cast<int>(imin64(kC, sp.len - chunk * kC)); };
     auto mats_of = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes; };
     const RowsToLds<KP, NW> key_loads(static_cast<uint32_t>(qk_stride), K, w, lane);
     const RowsToLds<VC, NW> value_loads(static_cast<uint32_t>(v_stride), static_cast<int>(a.V - vw), w, lane);
     FloatRows<KP, NW * 64> fk, fq;
-    auto fetch = [&](int64_t chunk, int half) {
+    constexpr int kParts = 4;  // as in gdr_fwd_kernel
+    auto fetch = [&](int64_t chunk, int half, int part) {
         const int len = length(chunk);
         uint8_t* to = lds + half * kPart;
         if constexpr (B16) {
-            key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
-            key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
-            value_loads.load(lds_offset(to) + kKeys, dyp + vw + chunk * kC * v_stride, len, w);
-            bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_f, w, lane);
+            if (part == 0) key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
+            if (part == 1) key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
+            if (part == 2) value_loads.load(lds_offset(to) + kKeys, dyp + vw + chunk * kC * v_stride, len, w);
+            if (part == 3) bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_f, w, lane);
         } else {
-            bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_f, w, lane);
-            fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
-            fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_f, w, lane);
+            if (part == 1) fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            if (part == 2) fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
         }
     };
-    if (chunks) fetch(chunks - 1, (chunks - 1) & 1);
+    auto fetch_pt = [&](int64_t chunk) {
+        if constexpr (B16) bytes_to_lds<NW, kN>(lds_offset(lds) + 2 * kPart, mats_of(chunk) + a.at_pt, w, lane);
+    };
+    if (chunks) {
+        fetch_pt(chunks - 1);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) fetch(chunks - 1, (chunks - 1) & 1, q);
+    }
     for (int64_t chunk = chunks - 1; chunk >= 0; --chunk) {
         const int half = static_cast<int>(chunk & 1), len = length(chunk);
         const uint8_t* in = lds + half * kPart;
@@ -106,7 +116,6 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
             fq.store(lds + 2 * kPart + PL * Keys::kBytes, tid);
             __syncthreads();
         }
-        const uint8_t* pt = mats_of(chunk) + a.at_pt;
         f32x4 dy[4];  // item r of tile rt: token 16 rt + 4 g + r of this lane's column
         f32x4 X[4] = {};
         if (in_v) {
@@ -129,11 +138,23 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
                 const Planes<PL> d = split<PL>(dy[2 * s], dy[2 * s + 1]);
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt)
-                    if (block_of<false>(rt, s) >= 0) X[rt] = mma(load_block<3>(pt, block_of<false>(rt, s), lane), d, X[rt]);
+                    if (block_of<false>(rt, s) >= 0) {
+                        if constexpr (B16) X[rt] = mma(load_block<3>(lds + 2 * kPart, block_of<false>(rt, s), lane), d, X[rt]);
+                        else X[rt] = mma(load_block<3>(mats_of(chunk) + a.at_pt, block_of<false>(rt, s), lane), d, X[rt]);
+                    }
             }
         }
-        if (chunk > 0) fetch(chunk - 1, half ^ 1);
-        if (!in_v) continue;
+        if constexpr (B16) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // Pᵀ is read
+        }
+        const bool more = chunk > 0;
+        if (more) fetch_pt(chunk - 1);
+        if (!in_v) {
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+                if (more) fetch(chunk - 1, half ^ 1, q);
+            continue;
+        }
 
         {
             float* to = a.adjoints + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K;
@@ -148,6 +169,10 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
             const Planes<3> lt = split<3>(L[2 * s], L[2 * s + 1]);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) Y[rt] = mma(Keys::template rows<PL>(lds_k, rt, s, c, g), lt, Y[rt]);
+            if (more) {
+#pragma unroll
+                for (int q = s * kParts / KS; q < (s + 1) * kParts / KS; ++q) fetch(chunk - 1, half ^ 1, q);
+            }
         }
         f32x4 beta[4];
 #pragma unroll
@@ -162,14 +187,17 @@ __global__ __launch_bounds__(NW * 64) void gdr_adjoint_kernel(AdjointArgs a) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 if (block_of<false>(rt, s) >= 0) X[rt] = mma(load_block<3>(lds_n, block_of<false>(rt, s), lane), mx[s], X[rt]);
-        float* z = a.pulls + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
+        {   // four value elements of a token a lane
+            float* z = a.pulls + ((slot0 + chunk) * a.H + h) * kC * a.V + (4 * g + (c & 3)) * a.V + v0 + (c & ~3);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = (i >> 2) * 16 + 4 * g + (i & 3);
-            const float x = X[i >> 2][i & 3], dr = x * beta[i >> 2][i & 3];
-            X[i >> 2][i & 3] = dr;
-            z[t * a.V] = x;
-            if (t < len) store_act(dvp, (chunk * kC + t) * v_stride, dr);
+            for (int rt = 0; rt < 4; ++rt) {
+                *reinterpret_cast<f32x4*>(z + 16 * rt * a.V) = quad_transpose(X[rt], c);
+                X[rt] *= beta[rt];  // dr
+                const f32x4 dr = quad_transpose(X[rt], c);
+                const float out[4] = {dr[0], dr[1], dr[2], dr[3]};
+                const int t = 16 * rt + 4 * g + (c & 3);
+                if (t < len) store_row(dvp + (chunk * kC + t) * v_stride, out);
+            }
         }
         // the adjoint of the state before the chunk
         const float last = f[4 * kC];

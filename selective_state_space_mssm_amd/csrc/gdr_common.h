@@ -139,6 +139,26 @@ __device__ __forceinline__ float sum_squares(const Planes<N>& x) {
     return s;
 }
 
+// Sixteen tokens of sixteen value elements: from four tokens (4 g + r) of element c a
+// lane, as the accumulators have them, to four elements (4 (c / 4) + r) of token
+// 4 g + c % 4, as they lie in memory: one 16-byte store instead of four of 4 bytes.
+__device__ __forceinline__ f32x4 quad_transpose(f32x4 x, int c) {
+    const bool odd = c & 1, upper = c & 2;
+    auto swap = [](auto move, bool second, float& a, float& b) {
+        const float other = move(second ? a : b);
+        a = second ? other : a;
+        b = second ? b : other;
+    };
+    auto by1 = [](float v) { return dpp_move<0xB1>(v); };
+    auto by2 = [](float v) { return dpp_move<0x4E>(v); };
+    float v[4] = {x[0], x[1], x[2], x[3]};
+    swap(by1, odd, v[0], v[1]);
+    swap(by1, odd, v[2], v[3]);
+    swap(by2, upper, v[0], v[2]);
+    swap(by2, upper, v[1], v[3]);
+    return f32x4{v[0], v[1], v[2], v[3]};
+}
+
 // N (a multiple of 4) neighbouring values to a row.
 template <int N>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[N]) {
@@ -205,7 +225,7 @@ struct Tile {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         const uint8_t* p = lds + at(16 * rt + 4 * g + (c >> 2), piece) + byte;
         return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(p)));
+            reinterpret_cast<__attribute__((address_space(3))) s16x4*>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)))));
     }
     // ... of column 16 m + c
     __device__ static __forceinline__ u32x2 four(const uint8_t* lds, int rt, int m, int c, int g) {
@@ -231,9 +251,9 @@ struct Tile {
 // 16 bytes of a row of q or k lie.
 __device__ __forceinline__ constexpr int state_column(int m, int i) { return 32 * (m >> 1) + 8 * (i >> 2) + 4 * (m & 1) + (i & 3); }
 
+// The lower half of a pointer to LDS is its offset there.
 __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
-    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-        (__attribute__((address_space(3))) const uint8_t*)(p))));
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)));
 }
 
 // bfloat16 rows from memory straight to a tile, by NW waves; rows from a chunk's

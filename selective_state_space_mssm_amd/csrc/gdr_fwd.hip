@@ -73,18 +73,21 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     const RowsToLds<KP, NW> key_loads(static_cast<uint32_t>(qk_stride), K, w, lane);
     const RowsToLds<VC, NW> value_loads(static_cast<uint32_t>(v_stride), static_cast<int>(a.V - vw), w, lane);
     FloatRows<KP, NW * 64> fk, fq;
-    auto fetch = [&](int64_t chunk, int half) {
+    // In four parts: a compute unit takes 1 KB into LDS in about 30 cycles, the 80 KB
+    // of a bfloat16 chunk in 2,500, for which its waves would otherwise wait at once.
+    constexpr int kParts = 4;
+    auto fetch = [&](int64_t chunk, int half, int part) {
         const int len = length(chunk);
         uint8_t* to = lds + half * kPart;
         if constexpr (B16) {
-            key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
-            key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
-            value_loads.load(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, len, w);
-            bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_p, w, lane);
+            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_p, w, lane);
+            if (part == 1) key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
+            if (part == 2) key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
+            if (part == 3) value_loads.load(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, len, w);
         } else {
-            bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_n, w, lane);
-            fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
-            fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_n, w, lane);
+            if (part == 1) fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            if (part == 2) fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
         }
     };
     f32x4 O[4];
@@ -97,7 +100,10 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             if (16 * rt + c < len) store_row(yp + (chunk * kC + 16 * rt + c) * v_stride, out);
         }
     };
-    if (chunks) fetch(0, 0);
+    if (chunks) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) fetch(0, 0, q);
+    }
     for (int64_t chunk = 0; chunk < chunks; ++chunk) {
         const int half = static_cast<int>(chunk & 1), len = length(chunk);
         const uint8_t* in = lds + half * kPart;
@@ -112,8 +118,13 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             __syncthreads();
         }
         if (chunk) put_y(chunk - 1);  // here, not when it was ready: the barrier waits for stores too
-        if (chunk + 1 < chunks) fetch(chunk + 1, half ^ 1);
-        if (!in_v) continue;
+        const bool more = chunk + 1 < chunks;
+        if (!in_v) {
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+                if (more) fetch(chunk + 1, half ^ 1, q);
+            continue;
+        }
 
         f32x4 val[4];  // item r of tile rt: token 16 rt + 4 g + r of this lane's column
 #pragma unroll
@@ -155,6 +166,10 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             for (int rt = 0; rt < 4; ++rt) X[rt] = mma(kf[rt], st, X[rt]);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) O[rt] = mma(so, qf[rt], O[rt]);
+            if (more) {
+#pragma unroll
+                for (int q = s * kParts / KS; q < (s + 1) * kParts / KS; ++q) fetch(chunk + 1, half ^ 1, q);
+            }
         }
         // e = r + N (beta r) with r = v - exp(b) S k
         f32x4 beta[4];
@@ -171,9 +186,9 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             for (int rt = 0; rt < 4; ++rt)
                 if (block_of<true>(rt, s) >= 0) X[rt] = mma(load_block<3>(lds_n, block_of<true>(rt, s), lane), mx[s], X[rt]);
         if constexpr (TRAIN) {
-            float* e = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
+            float* e = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + (4 * g + (c & 3)) * a.V + v0 + (c & ~3);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[((i >> 2) * 16 + 4 * g + (i & 3)) * a.V] = X[i >> 2][i & 3];
+            for (int rt = 0; rt < 4; ++rt) *reinterpret_cast<f32x4*>(e + 16 * rt * a.V) = quad_transpose(X[rt], c);
         }
         // u; y = scale exp(b) S q + P u, and the state's update
         const float last = f[4 * kC];
@@ -320,8 +335,9 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
                 ed[i] = *reinterpret_cast<const f32x4*>(p + 2 * kC);
                 // values: four of the wave's rows, 32 bytes each
                 typedef short s16x4 __attribute__((ext_vector_type(4)));
-                val[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
-                    lds_v + (16 * rt + 4 * g + (c >> 2)) * 32 + (c & 3) * 8)));
+                val[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    reinterpret_cast<__attribute__((address_space(3))) s16x4*>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+                        lds_v + (16 * rt + 4 * g + (c >> 2)) * 32 + (c & 3) * 8)))));
             }
             // what the steps behind the exchanges need, on its way during them
             const float last = f[4 * kC];
@@ -373,11 +389,9 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
                 put_half<PP>(s_u, w * RPW + i, u, lane);
             }
             if constexpr (TRAIN) {
-                float* to = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + v0 + c;
+                float* to = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + (4 * g + (c & 3)) * a.V + v0 + (c & ~3);
 #pragma unroll
-                for (int i = 0; i < RPW; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) to[(16 * (w * RPW + i) + 4 * g + r) * a.V] = e[i][r];
+                for (int i = 0; i < RPW; ++i) *reinterpret_cast<f32x4*>(to + 16 * (w * RPW + i) * a.V) = quad_transpose(e[i], c);
             }
             lds_barrier();
             Planes<3> ud[2];
