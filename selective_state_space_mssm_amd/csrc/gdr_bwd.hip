@@ -241,18 +241,34 @@ struct GradArgs {
     int norm;
 };
 
-constexpr int kPitch = kC + 4;  // floats of a row of a 64 x 64 matrix in LDS
-
-// 32 value elements of a state as planes in LDS, an operand row (64 bytes) for
-// each of KP columns; slot (g, j) is element 8 g + j.
-template <int KP>
-struct StateTile {
-    static constexpr int kBytes = KP * 64;
-    __device__ static __forceinline__ int at(int column, int piece) { return column * 64 + ((piece ^ ((column >> 1) & 3)) * 16); }
-    __device__ static __forceinline__ Planes<3> read(const uint8_t* lds, int column, int piece) {
-        Planes<3> out;
+// Half of an operand's slots, in planes.
+template <int N>
+__device__ __forceinline__ void put_four(uint8_t* to, int plane_bytes, f32x4 x) {
 #pragma unroll
-        for (int n = 0; n < 3; ++n) out.p[n] = *reinterpret_cast<const u32x4*>(lds + n * kBytes + at(column, piece));
+    for (int n = 0; n < N; ++n) {
+        *reinterpret_cast<u32x2*>(to + n * plane_bytes) = u32x2{upper_halves(x[0], x[1]), upper_halves(x[2], x[3])};
+        if (n + 1 < N) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] -= upper_part(x[r]);
+        }
+    }
+}
+
+// 32 value elements of 64 tokens as planes in LDS, an operand row (64 bytes) for each
+// token, in folded order.
+struct TokenTile {
+    static constexpr int kBytes = kC * 64;
+    __device__ static __forceinline__ int at(int token, int piece) { return token * 64 + ((piece ^ ((token >> 1) & 3)) * 16); }
+    // elements 4 q ..
+    template <int N>
+    __device__ static __forceinline__ void put(uint8_t* lds, int token, int q, f32x4 x) {
+        put_four<N>(lds + at(token, q & 3) + (q >> 2) * 8, kBytes, x);
+    }
+    template <int N>
+    __device__ static __forceinline__ Planes<N> read(const uint8_t* lds, int token, int piece) {
+        Planes<N> out;
+#pragma unroll
+        for (int n = 0; n < N; ++n) out.p[n] = *reinterpret_cast<const u32x4*>(lds + n * kBytes + at(token, piece));
         return out;
     }
 };
@@ -267,23 +283,31 @@ __device__ __forceinline__ float group4_sum(float v) {  // over the lanes l, l ^
     return v + __shfl_xor(v, 32);
 }
 
-// A workgroup: one chunk and one head of q and k, with all value heads that
-// share it, whose dq and dk are summed in registers.  Wave w has the tokens 16 w
-// .. 16 w + 15 in the columns of its accumulators and the key elements in their
-// rows, so that a lane's factors are one token's and it stores four neighbours.
-template <typename T, int KP>
-__global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
-    constexpr int PL = kPlanes<T>, KM = KP / 16;
+// A workgroup: one chunk and one head of q and k, with all value heads that share
+// it, whose dq and dk are summed in registers.  Wave w of half kh has the tokens 16 w
+// .. 16 w + 15 in the columns of its accumulators and half of the key elements in
+// their rows, so that a lane's factors are one token's and it stores four neighbours.
+// 32 value elements at a time are cut into planes in LDS, with the next ones' loads
+// under way; a state's columns are read by transposing reads.  Of the 64 x 64
+// matrices a wave has the blocks of its rows, transposed, and of its columns, which
+// as they lie in the accumulators are the operands that it needs next.
+template <typename T, int KP, int HALVES>
+__global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
+    constexpr int PL = kPlanes<T>, KH = KP / 16 / HALVES;  // row tiles of key elements of a wave
+    constexpr int THREADS = 256 * HALVES, WAVES = 4 * HALVES;
     typedef Tile<KP> Keys;
-    typedef StateTile<KP> State;
-    constexpr int kMatrix = kC * kPitch * 4, kKeys = 2 * PL * Keys::kBytes, kStates = 6 * State::kBytes;
-    __shared__ __align__(16) uint8_t lds[kKeys + (2 * kMatrix > kStates ? 2 * kMatrix : kStates)];
-    __shared__ float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[kC], s_end[8];
-    uint8_t *lds_k = lds, *lds_q = lds + PL * Keys::kBytes;
-    uint8_t *lds_s = lds + kKeys, *lds_l = lds_s + 3 * State::kBytes;             // while summing over value elements
-    float *sX = reinterpret_cast<float*>(lds + kKeys), *sM = sX + kC * kPitch;  // then
-    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
-    const int64_t hg = blockIdx.x % a.G, slot = a.slot0 + blockIdx.x / a.G;
+    typedef Tile<KP, 32> State;
+    typedef TokenTile Tokens;
+    constexpr int kKeys = 2 * PL * Keys::kBytes, kStaged = 6 * State::kBytes + (6 + PL) * Tokens::kBytes;
+    constexpr bool kShare = kKeys + kStaged > (HALVES == 1 ? 76 : 150) * 1024;  // q and k come after the sums, in the same place
+    __shared__ __align__(16) uint8_t lds[kShare ? (kStaged > kKeys ? kStaged : kKeys) : kKeys + kStaged];
+    __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_dots[4][kC], s_end[16];
+    static_assert(sizeof(lds) + 3500 <= 160 * 1024 / (3 - HALVES), "LDS of a compute unit");
+    uint8_t *lds_k = lds, *lds_q = lds_k + PL * Keys::kBytes;
+    uint8_t *lds_s = lds + (kShare ? 0 : kKeys), *lds_l = lds_s + 3 * State::kBytes, *lds_z = lds_l + 3 * State::kBytes,
+            *lds_u = lds_z + 3 * Tokens::kBytes, *lds_dy = lds_u + 3 * Tokens::kBytes;
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), w = wave & 3, kh = wave >> 2, c = lane & 15, g = lane >> 4;
+    const int64_t hg = blockIdx.x % static_cast<uint32_t>(a.G), slot = blockIdx.x / static_cast<uint32_t>(a.G);
     const Chunk ch = chunk_of(a.offsets, slot, a.T, a.N, a.each);
     if (ch.len == 0) return;
     const int K = static_cast<int>(a.K), V = static_cast<int>(a.V);
@@ -293,195 +317,255 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     const View<T> k_rows(kp), q_rows(qp);
     const int row = 16 * w + c;  // this lane's token
     const bool in_t = row < ch.len;
-    const uint32_t row_at = row * static_cast<uint32_t>(qk_stride);
-    float rk = 1.0f, rq = 1.0f;
-    if (a.norm) {
-        float k2 = 0.0f, q2 = 0.0f;
-#pragma unroll
-        for (int m = 0; m < KM; ++m) {
-            const f32x4 k4 = k_rows.four(row_at + 16 * m + 4 * g, in_t && 16 * m < K);
-            const f32x4 q4 = q_rows.four(row_at + 16 * m + 4 * g, in_t && 16 * m < K);
-            k2 = dot4(k4, k4, k2);
-            q2 = dot4(q4, q4, q2);
+    // Everything that a chunk needs at first is asked for at once, and waited for behind the last of it.
+    FloatRows<KP, THREADS> k_float, q_float;
+    auto ask_keys = [&] {
+        if constexpr (sizeof(T) == 2) {
+            const RowsToLds<KP, WAVES> loads(static_cast<uint32_t>(qk_stride), K, wave, lane);
+            loads.load(lds_offset(lds_k), kp, ch.len, wave);
+            loads.load(lds_offset(lds_q), qp, ch.len, wave);
+        } else {
+            k_float.load(kp, static_cast<uint32_t>(qk_stride), ch.len, K, tid);
+            q_float.load(qp, static_cast<uint32_t>(qk_stride), ch.len, K, tid);
         }
-        rk = 1.0f / __builtin_sqrtf(group4_sum(k2) + kGdrNormEps);
-        rq = 1.0f / __builtin_sqrtf(group4_sum(q2) + kGdrNormEps);
-    }
-    if (g == 0) s_rk[row] = rk, s_rq[row] = rq;
+    };
+    auto keep_keys = [&] {
+        if constexpr (sizeof(T) == 4) {
+            k_float.store(lds_k, tid);
+            q_float.store(lds_q, tid);
+        }
+        wait_memory<0>();
+    };
+    if constexpr (!kShare) ask_keys();
+    auto column = [&](int m) { return state_column(kh * KH + m, 4 * g); };  // of the wave's tile m, of this lane's rows
 
-    if constexpr (sizeof(T) == 2) {
-        const RowsToLds<KP, 4> loads(static_cast<uint32_t>(qk_stride), K, w, lane);
-        loads.load(lds_offset(lds_k), kp, ch.len, w);
-        loads.load(lds_offset(lds_q), qp, ch.len, w);
-        tile_barrier();
-    } else {
-        FloatRows<KP, 256> rows;
-        rows.load(kp, static_cast<uint32_t>(qk_stride), ch.len, K, tid);
-        rows.store(lds_k, tid);
-        rows.load(qp, static_cast<uint32_t>(qk_stride), ch.len, K, tid);
-        rows.store(lds_q, tid);
-    }
-    f32x4 dq_sum[KM] = {}, dk_sum[KM] = {};
-    const int per = static_cast<int>(a.H / a.G);
-    for (int hh = 0; hh < per; ++hh) {
-        const int64_t h = hg * per + hh, cell = slot * a.H + h;
-        __syncthreads();  // the head before is done with LDS
-        if (w == 0) {
-            const double b = decays_since_start(a.g + ch.start * a.H + h, a.H, ch.len, lane);
-            const float hi = static_cast<float>(b);
-            s_hi[lane] = hi;
-            s_lo[lane] = static_cast<float>(b - hi);
-            s_beta[lane] = lane < ch.len ? a.beta[(ch.start + lane) * a.H + h] : 0.0f;
+    // four key elements of a token out of a tile
+    auto from_tile = [&](const uint8_t* tile, int token, int col) {
+        f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int n = PL - 1; n >= 0; --n) {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(tile + n * Keys::kBytes + Keys::at(token, col >> 3) + (col & 4) * 2);
+            v += f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
         }
+        return v;
+    };
+    f32x4 dq_sum[KH] = {}, dk_sum[KH] = {};
+    const int per = static_cast<int>(a.H / a.G);
+    constexpr int kItems = KP * 8 / THREADS, kTokens = 512 / THREADS;  // four columns of an element each; four elements of a token
+    const int to_t = tid >> 3, to_q = tid & 7;                         // and of tokens 32 further
+    float to_beta[kTokens], dbeta[kTokens];
+    f32x4 st_s[kItems], st_l[kItems], to_z[kTokens], to_e[kTokens], to_dy[kTokens];
+    auto fetch = [&](int64_t h, int vb) {
+        const int64_t cell = slot * a.H + h;
         const View<float> S(a.states + cell * a.V * a.K), L(a.adjoints + cell * a.V * a.K);
         const View<float> e(a.misses + cell * kC * a.V), z(a.pulls + cell * kC * a.V);
         const View<T> dy(static_cast<const T*>(a.dy) + ch.start * v_stride + h * a.V);
-
-        // sums over the value elements
-        f32x4 yS[KM] = {}, zS[KM] = {}, uL[KM] = {}, dP[4] = {}, dA[4] = {};
-        float dbeta = 0.0f, both = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int item = tid + THREADS * i, v = vb + item / (KP / 4), k = item % (KP / 4) * 4;
+            st_s[i] = S.four(v * K + k, v < V && k < K);
+            st_l[i] = L.four(v * K + k, v < V && k < K);
+        }
+        const int v = vb + 4 * to_q;
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            const int t = to_t + 32 * i;
+            to_z[i] = z.four(t * V + v, v < V);
+            to_e[i] = e.four(t * V + v, v < V);
+            to_dy[i] = dy.four(t * static_cast<uint32_t>(v_stride) + v, v < V && t < ch.len);
+            if (vb == 0) to_beta[i] = View<float>(a.beta + ch.start * a.H + h).one(t * static_cast<uint32_t>(a.H), t < ch.len);
+        }
+    };
+    fetch(hg * per, 0);
+    float g_log = View<float>(a.g + ch.start * a.H + hg * per).one(lane * static_cast<uint32_t>(a.H), lane < ch.len);
+    {   // the lengths of q and k: eight lanes a token
+        const int t = tid >> 3;
+#pragma unroll
+        for (int i = 0; i < 512 / THREADS; ++i) {
+            float k2 = 0.0f, q2 = 0.0f;
+#pragma unroll
+            for (int p = 0; p < KP / 64; ++p) {
+                const uint32_t col = 64 * p + 8 * (tid & 7), at = (t + 32 * i) * static_cast<uint32_t>(qk_stride) + col;
+                const bool in = t + 32 * i < ch.len && col < a.K;
+                k2 += sum_squares(k_rows.planes(at, in));
+                q2 += sum_squares(q_rows.planes(at, in));
+            }
+            k2 = group_sum<8>(k2);
+            q2 = group_sum<8>(q2);
+            if ((tid & 7) == 0) {
+                s_rk[t + 32 * i] = a.norm ? 1.0f / __builtin_sqrtf(k2 + kGdrNormEps) : 1.0f;
+                s_rq[t + 32 * i] = a.norm ? 1.0f / __builtin_sqrtf(q2 + kGdrNormEps) : 1.0f;
+            }
+        }
+    }
+    if constexpr (!kShare) keep_keys();
+    float rk = 1.0f, rq = 1.0f;
+    for (int hh = 0; hh < per; ++hh) {
+        const int64_t h = hg * per + hh;
+        __syncthreads();  // the head before is done with LDS
+        if (wave == 0) {
+            const double b = decays_since_start(g_log, lane);
+            const float hi = static_cast<float>(b);
+            s_hi[lane] = hi;
+            s_lo[lane] = static_cast<float>(b - hi);
+        }
+        // sums over the value elements; X: dy . u and M: Z . u, of block b the rows (tokens i) of
+        // column block w for b > w, transposed (rows: tokens j) for b <= w, and of the diagonal both
+        f32x4 yS[KH] = {}, zS[KH] = {}, uL[KH] = {}, X[4] = {}, M[4] = {}, Xd = {0, 0, 0, 0}, Md = {0, 0, 0, 0};
+        float both = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            dbeta[i] = 0.0f;
+            if (to_q == 0) s_beta[to_t + 32 * i] = to_beta[i];
+        }
+#pragma unroll 1
         for (int vb = 0; vb < V; vb += 32) {
-            __syncthreads();
-            {   // 8 value elements of 2 columns a thread
-                const int o = tid / (KP / 2), kc = tid % (KP / 2) * 2;
-                if (o < 4) {
-                    float s0[8], s1[8], l0[8], l1[8];
+            __syncthreads();  // what is staged has been read
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool in = vb + 8 * o < V && kc < K;
-                        const f32x2 s2 = S.two((vb + 8 * o + j) * K + kc, in), l2 = L.two((vb + 8 * o + j) * K + kc, in);
-                        s0[j] = s2[0]; s1[j] = s2[1]; l0[j] = l2[0]; l1[j] = l2[1];
-                        both = __builtin_fmaf(s2[0], l2[0], __builtin_fmaf(s2[1], l2[1], both));
-                    }
-                    auto put = [&](uint8_t* to, int column, const Planes<3>& p) {
+            for (int i = 0; i < kItems; ++i) {
+                const int item = tid + THREADS * i, v = item / (KP / 4), k = item % (KP / 4) * 4;
+                const int at = State::at(v, k >> 3) + (k & 4) * 2;
+                both = dot4(st_s[i], st_l[i], both);
+                put_four<3>(lds_s + at, State::kBytes, st_s[i]);
+                put_four<3>(lds_l + at, State::kBytes, st_l[i]);
+            }
 #pragma unroll
-                        for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x4*>(to + n * State::kBytes + State::at(column, o)) = p.p[n];
-                    };
-                    put(lds_s, kc, split<3>(s0));
-                    put(lds_s, kc + 1, split<3>(s1));
-                    put(lds_l, kc, split<3>(l0));
-                    put(lds_l, kc + 1, split<3>(l1));
-                }
+            for (int i = 0; i < kTokens; ++i) {
+                dbeta[i] = dot4(to_z[i], to_e[i], dbeta[i]);
+                Tokens::put<3>(lds_z, to_t + 32 * i, to_q, to_z[i]);
+                Tokens::put<3>(lds_u, to_t + 32 * i, to_q, to_beta[i] * to_e[i]);
+                Tokens::put<PL>(lds_dy, to_t + 32 * i, to_q, to_dy[i]);
             }
             __syncthreads();
-            const int v = vb + 8 * g;
-            const bool in = v < V;
-            auto eight = [&](const View<float>& p, int t, float (&x)[8]) {
-                const f32x4 lo = p.four(t * V + v, in), hi = p.four(t * V + v + 4, in);
+            if (vb + 32 < V) fetch(h, vb + 32);
+            int c = lane & 15, g = lane >> 4;
+            asm volatile("" : "+v"(c), "+v"(g));  // addresses are computed here, not kept (and spilled) from before the loops
+            const int row = 16 * w + c;
+            const Planes<3> zf = Tokens::read<3>(lds_z, row, g), uf = Tokens::read<3>(lds_u, row, g);
+            const Planes<PL> dyf = Tokens::read<PL>(lds_dy, row, g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
-            };
-            float x[8], zz[8];
-            eight(z, row, zz);
-            eight(e, row, x);
-            const float beta = s_beta[row];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dbeta = __builtin_fmaf(x[i], zz[i], dbeta), x[i] *= beta;
-            const Planes<PL> dyf = dy.planes(row * static_cast<uint32_t>(v_stride) + v, in && in_t);
-            const Planes<3> zf = split<3>(zz), uf = split<3>(x);
-#pragma unroll
-            for (int m = 0; m < KM; ++m) {
-                const Planes<3> sf = State::read(lds_s, state_column(m, c), g), lf = State::read(lds_l, state_column(m, c), g);
+            for (int m = 0; m < KH; ++m) {
+                const Planes<3> sf = State::template columns<3>(lds_s, kh * KH + m, 0, c, g);
                 yS[m] = mma(sf, dyf, yS[m]);
                 zS[m] = mma(sf, zf, zS[m]);
-                uL[m] = mma(lf, uf, uL[m]);
+                uL[m] = mma(State::template columns<3>(lds_l, kh * KH + m, 0, c, g), uf, uL[m]);
+                if (m % 2) __builtin_amdgcn_sched_barrier(0);  // all operands at once would not fit the registers
             }
 #pragma unroll
-            for (int jb = 0; jb < 4; ++jb) {  // rows (of the accumulator): token i of this wave; columns: token j
-                if (jb > w) continue;
-                float xj[8];
-                eight(e, 16 * jb + c, xj);
-                const float bj = s_beta[16 * jb + c];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) xj[i] *= bj;
-                const Planes<3> uj = split<3>(xj);
-                dP[jb] = mma(dyf, uj, dP[jb]);
-                dA[jb] = mma(zf, uj, dA[jb]);
+            for (int b = 0; b < 4; ++b) {
+                if (b <= w) {
+                    const Planes<3> uj = Tokens::read<3>(lds_u, 16 * b + c, g);
+                    X[b] = mma(uj, dyf, X[b]);
+                    M[b] = mma(uj, zf, M[b]);
+                } else {
+                    X[b] = mma(Tokens::read<PL>(lds_dy, 16 * b + c, g), uf, X[b]);
+                    M[b] = mma(Tokens::read<3>(lds_z, 16 * b + c, g), uf, M[b]);
+                }
+                if (b % 2) __builtin_amdgcn_sched_barrier(0);
             }
+            Xd = mma(dyf, uf, Xd);
+            Md = mma(zf, uf, Md);
         }
-        __syncthreads();
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            const int j = 16 * jb + c;
+        if constexpr (kShare) {
+            ask_keys();
+            __syncthreads();
+            keep_keys();
+            __syncthreads();
+        }
+        rk = s_rk[row];
+        rq = s_rq[row];
+        if (hh + 1 < per) {  // the next head's, on their way meanwhile
+            fetch(h + 1, 0);
+            g_log = View<float>(a.g + ch.start * a.H + h + 1).one(lane * static_cast<uint32_t>(a.H), lane < ch.len);
+        }
+        const float row_hi = s_hi[row], row_lo = s_lo[row], row_beta = s_beta[row];
+        // X and M with their decays: X_ij = scale G_ij dP_ij (j <= i), M_ij = -G_ij beta_i Z_i . u_j (j < i)
+        const f32x4 zero = {0, 0, 0, 0};
+        auto four = [&](const float* p, int b) { return *reinterpret_cast<const f32x4*>(p + 16 * b + 4 * g); };
+        auto finish = [&](int b, bool columns, f32x4& x, f32x4& m) {  // columns: rows are tokens i, the lane's is j
+            const f32x4 hi = four(s_hi, b), lo = four(s_lo, b), beta = four(s_beta, b);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * w + 4 * g + r;
-                float x = 0.0f, mm = 0.0f;
-                if (j <= i) {
-                    const float d = decay_between(s_hi[i], s_lo[i], s_hi[j], s_lo[j]);
-                    x = a.scale * d * dP[jb][r];
-                    mm = j < i ? -d * s_beta[i] * dA[jb][r] : 0.0f;
-                }
-                sX[i * kPitch + j] = x;
-                sM[i * kPitch + j] = mm;
+                const int other = 16 * b + 4 * g + r, ahead = columns ? other - row : row - other;  // i - j
+                const float sum = (hi[r] - row_hi) + (lo[r] - row_lo);
+                const float d = ahead >= 0 ? fast_exp2((columns ? sum : -sum) * kLog2e) : 0.0f;
+                x[r] *= a.scale * d;
+                m[r] *= ahead > 0 ? -d * (columns ? beta[r] : row_beta) : 0.0f;
             }
-        }
-        dbeta = group4_sum(dbeta);
-        if (g == 0 && in_t) a.dbeta[(ch.start + row) * a.H + h] = dbeta;
-        both = group_sum<16>(both);
-        both = group4_sum(both);
-        if (lane == 0) s_end[w] = both;
-        __syncthreads();
-
-        const float in_chunk = whole_exp(static_cast<double>(s_hi[row]) + s_lo[row]);
-        const double end = static_cast<double>(s_hi[kC - 1]) + s_lo[kC - 1];
-        const float to_end = whole_exp(end - (static_cast<double>(s_hi[row]) + s_lo[row]));
-        const float fy = a.scale * in_chunk, fz = -in_chunk * s_beta[row];
-        f32x4 dq[KM], dkr[KM], dkc[KM], k4[KM], q4[KM];
-        float wrote = 0.0f;
+        };
 #pragma unroll
-        for (int m = 0; m < KM; ++m) {
-            const bool in = in_t && state_column(m, 4 * g) < K;
-            k4[m] = rk * k_rows.four(row_at + state_column(m, 4 * g), in);
-            q4[m] = rq * q_rows.four(row_at + state_column(m, 4 * g), in);
-            dq[m] = fy * yS[m];
-            dkr[m] = fz * zS[m];
-            dkc[m] = to_end * uL[m];
-            wrote = dot4(k4[m], dkc[m], wrote);
+        for (int b = 0; b < 4; ++b) finish(b, b > w, X[b], M[b]);
+        finish(w, true, Xd, Md);
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            const float sum = group_sum<8>(dbeta[i]);
+            const int t = to_t + 32 * i;
+            if (to_q == 0 && t < ch.len) a.dbeta[(ch.start + t) * a.H + h] = sum;
         }
+        both = group4_sum(group_sum<16>(both));
+        if (lane == 0) s_end[wave] = both;
+
+        int c = lane & 15, g = lane >> 4;
+        asm volatile("" : "+v"(c), "+v"(g));  // as above
+        const float in_chunk = whole_exp(static_cast<double>(row_hi) + row_lo);
+        const double end = static_cast<double>(s_hi[kC - 1]) + s_lo[kC - 1];
+        const float to_end = whole_exp(end - (static_cast<double>(row_hi) + row_lo));
+        const float fy = a.scale * in_chunk, fz = -in_chunk * row_beta;
+        // summed over the tokens of blocks 2 s and 2 s + 1: the lane's row of X and M, and its column
+        Planes<3> xr[2], mr[2], xc[2], mc[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            // the tokens summed over: 32 s + slot; this lane's row of X and M, and its column
-            float xr[8], mr[8], xc[8], mc[8];
+            auto operand = [&](const f32x4(&x)[4], const f32x4& diagonal, bool columns, const float* factor) {
+                f32x4 part[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = 32 * s + 4 * g + (i & 3) + (i >> 2) * 16;
-                const float rkt = s_rk[t];
-                xr[i] = sX[row * kPitch + t] * rkt;
-                mr[i] = sM[row * kPitch + t] * rkt;
-                xc[i] = sX[t * kPitch + row] * s_rq[t];
-                mc[i] = sM[t * kPitch + row] * rkt;
-            }
-            const Planes<3> xrf = split<3>(xr), mrf = split<3>(mr), xcf = split<3>(xc), mcf = split<3>(mc);
-#pragma unroll
-            for (int m = 0; m < KM; ++m) {
-                const Planes<PL> kt = Keys::template columns<PL>(lds_k, m, s, c, g);
-                const Planes<PL> qt = Keys::template columns<PL>(lds_q, m, s, c, g);
-                dq[m] = mma(kt, xrf, dq[m]);
-                dkr[m] = mma(kt, mrf, dkr[m]);
-                dkc[m] = mma(kt, mcf, dkc[m]);
-                dkc[m] = mma(qt, xcf, dkc[m]);
-            }
+                for (int i = 0; i < 2; ++i) {
+                    const int b = 2 * s + i;
+                    const f32x4 v = columns ? (b > w ? x[b] : b == w ? diagonal : zero) : (b <= w ? x[b] : zero);
+                    part[i] = v * four(factor, b);
+                }
+                return split<3>(part[0], part[1]);
+            };
+            xr[s] = operand(X, Xd, false, s_rk);
+            mr[s] = operand(M, Md, false, s_rk);
+            xc[s] = operand(X, Xd, true, s_rq);
+            mc[s] = operand(M, Md, true, s_rk);
         }
-        float db = 0.0f;
+        float wrote = 0.0f, db = 0.0f;
 #pragma unroll
-        for (int m = 0; m < KM; ++m) {
-            db = dot4(q4[m], dq[m], db);
-            db = dot4(k4[m], dkr[m] - dkc[m], db);
-            dq_sum[m] += dq[m];
-            dk_sum[m] += dkr[m] + dkc[m];
+        for (int m = 0; m < KH; ++m) {
+            __builtin_amdgcn_sched_barrier(0);  // one after the other: all at once would not fit the registers
+            const int col = state_column(kh * KH + m, 4 * g), token = 16 * w + c;
+            const f32x4 k4 = rk * from_tile(lds_k, token, col), q4 = rq * from_tile(lds_q, token, col);
+            f32x4 dq = fy * yS[m], dkr = fz * zS[m], dkc = to_end * uL[m];
+            wrote = dot4(k4, dkc, wrote);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Planes<PL> kt = Keys::template columns<PL>(lds_k, kh * KH + m, s, c, g);
+                const Planes<PL> qt = Keys::template columns<PL>(lds_q, kh * KH + m, s, c, g);
+                dq = mma(kt, xr[s], dq);
+                dkr = mma(kt, mr[s], dkr);
+                dkc = mma(kt, mc[s], dkc);
+                dkc = mma(qt, xc[s], dkc);
+            }
+            db = dot4(q4, dq, db);
+            db = dot4(k4, dkr - dkc, db);
+            dq_sum[m] += dq;
+            dk_sum[m] += dkr + dkc;
         }
+        __builtin_amdgcn_sched_barrier(0);
         db = group4_sum(db);
-        if (g == 0) s_db[row] = db;
-        wrote = group4_sum(wrote);
-        wrote = group_sum<16>(wrote);
-        if (lane == 0) s_end[4 + w] = wrote;
+        if (g == 0) s_db[kh][row] = db;
+        wrote = group4_sum(group_sum<16>(wrote));
+        if (lane == 0) s_end[8 + wave] = wrote;
         __syncthreads();
-        if (w == 0) {
-            double v = s_db[lane];
-            if (lane == kC - 1)
-                v += static_cast<double>(whole_exp(end)) * ((static_cast<double>(s_end[0]) + s_end[1]) + (static_cast<double>(s_end[2]) + s_end[3])) +
-                     ((static_cast<double>(s_end[4]) + s_end[5]) + (static_cast<double>(s_end[6]) + s_end[7]));
+        if (wave == 0) {
+            double v = static_cast<double>(s_db[0][lane]) + (HALVES == 2 ? s_db[HALVES - 1][lane] : 0.0f);
+            if (lane == kC - 1) {
+                double states = 0.0, writes = 0.0;
+#pragma unroll
+                for (int i = 0; i < WAVES; ++i) states += s_end[i], writes += s_end[8 + i];
+                v += static_cast<double>(whole_exp(end)) * states + writes;
+            }
 #pragma unroll
             for (int d = 1; d < kC; d *= 2) {  // from the last token on
                 const double o = __shfl_down(v, d);
@@ -492,26 +576,31 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GradArgs a) {
     }
     // through the division by their lengths
     float qd = 0.0f, kd = 0.0f;
-    f32x4 k4[KM], q4[KM];
+    f32x4 k4[KH], q4[KH];
 #pragma unroll
-    for (int m = 0; m < KM; ++m) {
-        const bool in = in_t && a.norm && state_column(m, 4 * g) < K;
-        k4[m] = rk * k_rows.four(row_at + state_column(m, 4 * g), in);
-        q4[m] = rq * q_rows.four(row_at + state_column(m, 4 * g), in);
+    for (int m = 0; m < KH; ++m) {
+        k4[m] = (a.norm ? rk : 0.0f) * from_tile(lds_k, row, column(m));
+        q4[m] = (a.norm ? rq : 0.0f) * from_tile(lds_q, row, column(m));
         qd = dot4(q4[m], dq_sum[m], qd);
         kd = dot4(k4[m], dk_sum[m], kd);
     }
     qd = group4_sum(qd);
     kd = group4_sum(kd);
+    if (g == 0) s_dots[kh][row] = qd, s_dots[2 + kh][row] = kd;
+    __syncthreads();
+    if constexpr (HALVES == 2) {
+        qd = s_dots[0][row] + s_dots[1][row];
+        kd = s_dots[2][row] + s_dots[3][row];
+    }
     T* dqp = static_cast<T*>(a.dq) + (ch.start + row) * qk_stride + hg * a.K;
     T* dkp = static_cast<T*>(a.dk) + (ch.start + row) * qk_stride + hg * a.K;
 #pragma unroll
-    for (int m = 0; m < KM; ++m) {
-        if (!in_t || state_column(m, 4 * g) >= K) continue;
+    for (int m = 0; m < KH; ++m) {
+        if (!in_t || column(m) >= K) continue;
         const f32x4 x = rq * (dq_sum[m] - qd * q4[m]), y = rk * (dk_sum[m] - kd * k4[m]);
         const float xs[4] = {x[0], x[1], x[2], x[3]}, ys[4] = {y[0], y[1], y[2], y[3]};
-        store_row(dqp + state_column(m, 4 * g), xs);
-        store_row(dkp + state_column(m, 4 * g), ys);
+        store_row(dqp + column(m), xs);
+        store_row(dkp + column(m), ys);
     }
 }
 
@@ -526,7 +615,8 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const GradArgs d{a.q, a.k, a.dy, a.g, a.beta, a.offsets, a.states, a.misses, a.adjoints, a.pulls, a.dq, a.dk, a.dg, a.dbeta,
                      a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, 0, a.scale, a.norm};
-    gdr_grad_kernel<T, KP><<<static_cast<uint32_t>(gdr_slots(a.T, a.N) * a.G), 256, 0, s>>>(d);
+    constexpr int HALVES = 2;
+    gdr_grad_kernel<T, KP, HALVES><<<static_cast<uint32_t>(gdr_slots(a.T, a.N) * a.G), 256 * HALVES, 0, s>>>(d);
     return hipGetLastError();
 }
 template <typename T, int KP>

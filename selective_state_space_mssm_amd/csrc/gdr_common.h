@@ -55,13 +55,18 @@ struct Chunk {
     int64_t seq, start;  // its first token
     int len;             // tokens, up to 64
 };
+// By a whole wave, 64 sequences at a time: few loads behind one another.
 __device__ __forceinline__ Chunk chunk_of(const int32_t* offsets, int64_t slot, int64_t T, int64_t N, int64_t each) {
-    int64_t lo = 0, hi = N;  // the last sequence whose first slot is not behind this one
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        const int64_t s = offsets ? imin64(T, offsets[mid] < 0 ? 0 : offsets[mid]) : mid * each;
-        if ((s >> 6) + mid <= slot) lo = mid;
-        else hi = mid;
+    const int64_t lane = threadIdx.x & 63;
+    int64_t lo = 0, count = N;  // the last of `count` sequences whose first slot is not behind this one
+    while (count > 1) {
+        const int64_t step = (count + 63) >> 6, n = lo + lane * step;
+        int64_t s = 0;
+        if (lane * step < count) s = offsets ? imin64(T, offsets[n] < 0 ? 0 : offsets[n]) : n * each;
+        const int before = __builtin_popcountll(__ballot(lane * step < count && (s >> 6) + n <= slot));
+        const int64_t at = (before > 1 ? before - 1 : 0) * step;
+        lo += at;
+        count = imin64(step, count - at);
     }
     const Span s = span_of(offsets, lo, T, each);
     const int64_t t = (slot - first_slot(s, lo)) * kC;
@@ -182,8 +187,7 @@ __device__ __forceinline__ float whole_exp(double x) {
     return __builtin_fmaf(e, static_cast<float>(x - f), e);
 }
 // One wave, a token a lane: the sum of the chunk's log decays up to the lane's token.
-__device__ __forceinline__ double decays_since_start(const float* g, int64_t stride, int len, int lane) {
-    const float gl = lane < len ? g[lane * stride] : 0.0f;
+__device__ __forceinline__ double decays_since_start(float gl, int lane) {
     double b = gl < kGdrLeast ? kGdrLeast : gl;
 #pragma unroll
     for (int d = 1; d < kC; d *= 2) {
@@ -199,15 +203,15 @@ __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_
 
 // ---- a chunk's rows in LDS --------------------------------------------------------
 
-// 64 rows (tokens) of W columns, as bfloat16 planes.  A row's 16-byte pieces are
+// R rows (tokens, or value elements) of W columns, as bfloat16 planes.  A row's 16-byte pieces are
 // exchanged among themselves by the row's number, so that the 16 rows that a read
 // takes at once spread over the banks.  Read as operands by rows (summed over the
 // columns) in one 16-byte read, or by columns (summed over the tokens) in two
 // transposing reads: sixteen lanes read four rows of 16 values, 8 bytes a lane,
 // and each gets a column's four.
-template <int W>
+template <int W, int R = kC>
 struct Tile {
-    static constexpr int kRow = W * 2, kBytes = kC * kRow, kPieces = W / 8;
+    static constexpr int kRow = W * 2, kBytes = R * kRow, kPieces = W / 8;
     static_assert(kPieces == 8 || kPieces == 16, "rows of 128 or 256 bytes");
     __device__ static __forceinline__ int turn(int row) { return kPieces == 16 ? row & 15 : (row >> 1) & 7; }
     __device__ static __forceinline__ int at(int row, int piece) { return row * kRow + ((piece ^ turn(row)) * 16); }

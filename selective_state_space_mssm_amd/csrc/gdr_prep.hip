@@ -132,8 +132,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && TRAIN ? 1 : 2) void 
     float* f = reinterpret_cast<float*>(out + a.at_f);
 
     // the tokens' decays, a token a lane, under way with the first rows
-    const double b = decays_since_start(a.g + ch.start * a.H + h, a.H, ch.len, lane);
-    const float beta = lane < ch.len ? a.beta[(ch.start + lane) * a.H + h] : 0.0f;
+    const float g_log = View<float>(a.g + ch.start * a.H + h).one(lane * a.H, lane < ch.len);
+    const float beta = View<float>(a.beta + ch.start * a.H + h).one(lane * a.H, lane < ch.len);
 
     // K Kᵀ, block rows above columns (kk[i][j], i >= j) and transposed (kt[j][i]); K Qᵀ (kq[j][i]), Q Kᵀ (qk[i][j])
     f32x4 kk[4][4] = {}, kt[4][4] = {}, kq[4][4] = {}, qk[4][4] = {};
@@ -182,6 +182,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && TRAIN ? 1 : 2) void 
         rk = 1.0f / __builtin_sqrtf(kl + kGdrNormEps);
         rq = 1.0f / __builtin_sqrtf(ql + kGdrNormEps);
     }
+    const double b = decays_since_start(g_log, lane);
     // Between blocks a decay is the product of three, none above 1: from the row's
     // block's start, over the blocks between, to the column's block's end.
     const double end = __shfl(b, kC - 1), block_end = __shfl(b, lane | 15);
