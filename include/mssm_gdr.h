@@ -67,8 +67,10 @@ typedef struct {
  * cores.  Required: p, q, k, v, g, beta, y, workspace.  Optional (NULL): h0 ->
  * zeros; offsets; h_final -> not written (it may be h0's own buffer).  Without
  * offsets tokens has to be a multiple of seqs (else MSSM_ERR_SHAPE).  heads *
- * (tokens / 64 + seqs) has to be below 2^23, heads * value_dim and qk_heads *
- * key_dim at most 2^22 (MSSM_ERR_SHAPE).
+ * (tokens / 64 + seqs) has to be below 2^23, heads * seqs at most 2^20, heads *
+ * value_dim and qk_heads * key_dim at most 2^22 (MSSM_ERR_SHAPE).  A NaN or an
+ * infinity in a token spoils its chunk of 64 tokens and what follows it in its
+ * sequence, in the heads that read it, and nothing else.
  */
 size_t mssm_gdr_fwd_workspace_bytes(const mssm_gdr_problem* p);
 

@@ -43,8 +43,10 @@ mssm_status check_chunked(const mssm_gdr_problem* p) {
     if (st != MSSM_OK) return st;
     // byte offsets within a chunk stay below 2^31
     if (p->qk_heads * p->key_dim > (int64_t{1} << 22) || p->heads * p->value_dim > (int64_t{1} << 22)) return MSSM_ERR_SHAPE;
-    // every kernel's workgroups, at most heads * slots * 2 value parts, stay below 2^24 (2^32 threads)
-    if (p->heads > (int64_t{1} << 23) || mssm::gdr_slots(p->tokens, p->seqs) >= (int64_t{1} << 23) / p->heads) return MSSM_ERR_SHAPE;
+    // threads of a launch stay below 2^32: the chunks' kernels have up to 512 for each
+    // chunk and head, the chains' 256 for 64 value columns of each sequence and head
+    if (p->heads > (int64_t{1} << 20) || p->seqs > (int64_t{1} << 20) / p->heads) return MSSM_ERR_SHAPE;
+    if (mssm::gdr_slots(p->tokens, p->seqs) >= (int64_t{1} << 23) / p->heads) return MSSM_ERR_SHAPE;
     return MSSM_OK;
 }
 

@@ -8,7 +8,6 @@
 // of the one before.  The other operands, q, k and the chunk's matrices, are
 // shared by the waves of a workgroup.
 #include "gdr_common.h"
-#include <stdlib.h>
 
 namespace mssm {
 namespace {
@@ -525,11 +524,21 @@ hipError_t launch_narrow(const GdrArgs& a, hipStream_t s) {
 }
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
+    // A tile of 16 columns a workgroup while there are at most 512 (of key dim up to 64:
+    // 256) of them.  1,024 tokens, with the chunks' own pass, us of this form / of the
+    // wide one: key and value dim 128, 64 heads (512 tiles) 81 / 86, 96 heads 118 / 97;
+    // 128 and 64, 128 heads (512) 94 / 100, 192 heads 137 / 117; dim 64, 64 heads (256)
+    // 45 / 66, 96 heads 75 / 72; 64 and 128, 32 heads (256) 44 / 64, 64 heads 70 / 67.
     if constexpr (sizeof(T) == 2) {
-        if (getenv("GDR_NARROW") ? atoi(getenv("GDR_NARROW")) : a.N * a.H < 64) return launch_narrow<KP>(a, s);
+        if (a.N * a.H * (a.V / 16) <= (KP == 128 ? 512 : 256)) return launch_narrow<KP>(a, s);
     }
-    if constexpr (sizeof(T) == 2 || KP == 64) {  // eight waves have 256 registers each, too few for float32 planes of 128
-        if (a.V > 64 && a.N * a.H >= 128) return launch_c<T, KP, 8>(a, s);
+    // Workgroups of 128 columns once those of 64 are more than the 256 compute units; as
+    // above, us with 64 / 128 columns: 128 and 128, 128 heads 105 / 118, 160 heads 171 /
+    // 128; 128 and 256, 48 heads 83 / 100, 72 heads 153 / 109; float32, 64 and 128, 128
+    // heads 125 / 157, 160 heads 229 / 180.  Their eight waves have 256 registers each,
+    // too few for the float32 planes of a key dim of 128.
+    if constexpr (sizeof(T) == 2 || KP == 64) {
+        if (a.V > 64 && a.N * a.H * ((a.V + 63) / 64) > 256) return launch_c<T, KP, 8>(a, s);
     }
     return launch_c<T, KP, 4>(a, s);
 }
