@@ -123,6 +123,21 @@ def test_the_workspace_holds_every_chunk_of_packed_sequences():
         assert len(set(used)) == len(used) and (not used or max(used) < total // 64 + n)
 
 
+def test_offsets_that_are_none_name_no_slot_outside():
+    # clamped as on the device: start to 0 .. tokens, end to start .. tokens
+    import random
+    r = random.Random(1)
+    for _ in range(500):
+        n, total = r.randint(1, 9), r.randint(1, 700)
+        wild = lambda: r.choice([r.randint(-100, 800), r.randint(0, total), -2 ** 31, 2 ** 31 - 1])  # noqa: E731
+        offsets = [wild() for _ in range(n + 1)]
+        for i, (a, b) in enumerate(zip(offsets, offsets[1:])):
+            a = min(max(a, 0), total)
+            b = a if b < a else min(b, total)
+            assert a // 64 + i < total // 64 + n
+            assert all(a // 64 + i + c < total // 64 + n for c in range(-(-(b - a) // 64)))
+
+
 def test_binding_refuses_before_the_library():
     torch = pytest.importorskip("torch")
     z = torch.zeros
