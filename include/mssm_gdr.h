@@ -119,7 +119,7 @@ mssm_status mssm_gdr_bwd(const mssm_gdr_problem* p, const void* q, const void* k
  *   seqs, else MSSM_ERR_SHAPE).  A row whose slot is not in 0 .. seqs - 1 is not
  *   in use: its y is 0 and no state changes.  Rows with the same slot are tokens
  *   of one sequence and go through its state in the order of the rows.
- * rows * heads has to be below 2^31 (MSSM_ERR_SHAPE).
+ * rows * heads has to be below 2^31, heads at most 2^20 (MSSM_ERR_SHAPE).
  */
 mssm_status mssm_gdr_step(const mssm_gdr_problem* p, const void* q, const void* k, const void* v, const float* g,
                           const float* beta, const int32_t* slots, float* state, void* y, void* hip_stream);

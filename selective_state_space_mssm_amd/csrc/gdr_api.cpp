@@ -206,7 +206,8 @@ mssm_status mssm_gdr_step(const mssm_gdr_problem* p, const void* q, const void* 
                           const float* beta, const int32_t* slots, float* state, void* y, void* hip_stream) {
     mssm_status st = check_problem(p);
     if (st != MSSM_OK) return st;
-    if (p->tokens >= (int64_t{1} << 31) / p->heads || (!slots && p->tokens > p->seqs)) return MSSM_ERR_SHAPE;
+    // a launch holds every value part of at least one row: up to 8 workgroups of 256 threads a head
+    if (p->heads > (int64_t{1} << 20) || p->tokens >= (int64_t{1} << 31) / p->heads || (!slots && p->tokens > p->seqs)) return MSSM_ERR_SHAPE;
     if (any_null({q, k, v, g, beta, state, y})) return MSSM_ERR_NULL;
     st = check_align({q, k, v, g, beta, slots, state, y});
     if (st != MSSM_OK) return st;

@@ -1,10 +1,10 @@
 // gdr_common.h -- device helpers shared by the gated delta rule's kernels: where a
 // sequence's chunks lie, their decays, and a chunk's rows in LDS.
 //
-// Products as in planes.h.  The order of the slots used throughout is slot (g, j) <-> 4 g + j for j < 4 and 16 + 4 g +
-// (j - 4) otherwise ("folded"): two accumulators of 16 rows each, one above the
-// other, are then an operand that is summed over these rows without any lane
-// having to exchange a value.
+// Products as in planes.h.  The order of the slots used throughout is slot (g, j)
+// <-> 4 g + j for j < 4 and 16 + 4 g + (j - 4) otherwise ("folded"): two
+// accumulators of 16 rows each, one above the other, are then an operand that is
+// summed over these rows without any lane having to exchange a value.
 #pragma once
 
 #include <hip/hip_runtime.h>

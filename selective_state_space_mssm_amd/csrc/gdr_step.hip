@@ -133,7 +133,7 @@ void launch_r(const GdrStepArgs& a, hipStream_t s) {
     StepArgs k{a.q, a.k, a.v, a.g, a.beta, a.slots, a.state, a.y, 0, a.rows, a.pool, a.G, a.H, a.K, a.V,
                (a.V + 16 * RI - 1) / (16 * RI), a.scale, a.norm};
     // a launch has fewer than 2^32 threads: as many rows at a time as fit
-    const int64_t most = (int64_t{1} << 23) / (a.H * k.parts) > 0 ? (int64_t{1} << 23) / (a.H * k.parts) : 1;
+    const int64_t most = (int64_t{1} << 23) / (a.H * k.parts);  // heads are at most 2^20, parts 8
     for (k.row0 = 0; k.row0 < a.rows; k.row0 += most)
         gdr_step_kernel<T, QN, RI><<<static_cast<uint32_t>(imin64(most, a.rows - k.row0) * a.H * k.parts), 256, 0, s>>>(k);
 }

@@ -259,17 +259,17 @@ __global__ __launch_bounds__(256, 2) void lora_down_kernel(LoraKernelArgs a) {
                 step(xe[0], we[0]);
             }
         } else {
-        if (k + 32 <= k1) fetch(k, xe[0], we[0]);
-        for (; k + 32 <= k1; k += 256) {
-            if (k + 160 <= k1) fetch(k + 128, xe[1], we[1]);
-            step(xe[0], we[0]);
-            if (k + 160 > k1) {
-                k += 128;
-                break;
+            if (k + 32 <= k1) fetch(k, xe[0], we[0]);
+            for (; k + 32 <= k1; k += 256) {
+                if (k + 160 <= k1) fetch(k + 128, xe[1], we[1]);
+                step(xe[0], we[0]);
+                if (k + 160 > k1) {
+                    k += 128;
+                    break;
+                }
+                if (k + 288 <= k1) fetch(k + 256, xe[0], we[0]);
+                step(xe[1], we[1]);
             }
-            if (k + 288 <= k1) fetch(k + 256, xe[0], we[0]);
-            step(xe[1], we[1]);
-        }
         }
         if (k < k1) {
 #pragma unroll

@@ -103,6 +103,7 @@ def test_workspaces_are_refused(name):
 def test_steps_are_refused():
     assert call("step", problem(tokens=3)) == SHAPE                    # three rows of two states, without slots
     assert call("step", problem(tokens=1 << 30, seqs=1 << 30)) == SHAPE
+    assert call("step", problem(tokens=1, groups=1, heads=(1 << 20) + 1)) == SHAPE
 
 
 def test_queries_refuse_invalid_problems():
