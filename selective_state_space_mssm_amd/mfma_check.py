@@ -8,7 +8,9 @@ loop exit have been seen to get none, on the path of the exit alone (an 8-bit
 product wrong in the last two values of its last accumulator).  ``check_asm``
 follows every path from every matrix instruction and reports each instruction
 that reads or writes part of its result too early.  Matrix instructions that take
-it whole as their accumulator are interlocked and are not reported.
+it whole as their accumulator are interlocked and are not reported, nor are those
+that only write to its registers and take as long or longer: matrix instructions of
+one length end in the order in which they begin.
 
 ``__graft_entry__.build`` runs it on the assembly of the library it builds and
 fails the build on any finding.
@@ -45,6 +47,14 @@ def _adds_to(dst, op, args):
         return False
     parts = [_regs(p) for p in re.split(r",\s*(?![^\[]*\])", args)[:4]]
     return parts[3:] == [dst] and not any(dst & p for p in parts[1:3])
+
+
+def _overwrites(dst, first, op, args):
+    """A matrix instruction that reads nothing of the result and takes at least as long: they end in order, so what it
+    writes of the result's registers is its own."""
+    if not op.startswith("v_mfma") or PASSES.get(op, 16) < PASSES.get(first, 16):
+        return False
+    return not any(dst & _regs(p) for p in re.split(r",\s*(?![^\[]*\])", args)[1:4])
 
 
 def _interlocked(dst, op, args):
@@ -96,10 +106,11 @@ def check_function(body):
                     break
                 seen[k, dst] = waited
                 o, a = ins[k]
-                if dst & _regs(a) and not _interlocked(dst, o, a):
+                after = _overwrites(dst, op, o, a)
+                if dst & _regs(a) and not after and not _interlocked(dst, o, a):
                     found.append((f"{op} {args}", f"{o} {a}", waited))
                     break
-                if _adds_to(dst, o, a):
+                if after or _adds_to(dst, o, a):
                     dst -= _regs(a.split(",")[0])  # those are its own result from here on
                     if not dst:
                         break
