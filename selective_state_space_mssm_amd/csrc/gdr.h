@@ -21,6 +21,15 @@ constexpr float kGdrNormEps = 1e-6f;  // added to the squared length of q and k
 // first is at least ceil(length / 64) further), of T / 64 + N in all.
 inline int64_t gdr_slots(int64_t tokens, int64_t seqs) { return tokens / kGdrChunk + seqs; }
 
+// The pieces of the sequences that the forward's chains go through side by side:
+// 2^shift tokens each, numbered as the chunks are, `count` in all; shift = 0: whole
+// sequences.
+struct GdrPieces {
+    int shift = 0;
+    int64_t count;
+    GdrPieces(int64_t T, int64_t N, int64_t H, int64_t K, int64_t V, int dtype);
+};
+
 // What the chunk-parallel pass leaves for each (slot, head), in bytes: the
 // matrices N and P as operands of the matrix instructions (their 6 blocks of 16
 // x 32 that are not zero, as bfloat16 planes of 1 KB that add up to the float32
@@ -54,6 +63,8 @@ struct GdrArgs {
     float* h_final;          // nullable
     // chunk matrices (slots, H, GdrLayout::bytes)
     uint8_t* mats;
+    float* starts;           // (pieces, H, V, K) the state before a piece
+    float* moves;            // (pieces, H, K, K) what a piece makes of a state's rows, transposed
     bool train;              // with the transposes, the states and the misses:
     float* states;           // (slots, H, V, K) before every chunk; null: not kept
     float* misses;           // (slots, H, 64, V) e; null: not kept

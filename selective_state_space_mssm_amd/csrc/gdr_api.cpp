@@ -68,6 +68,12 @@ size_t cells(const mssm_gdr_problem* p) { return static_cast<size_t>(mssm::gdr_s
 void place_forward(const mssm_gdr_problem* p, bool train, Cut& c, GdrArgs& a) {
     a.mats = static_cast<uint8_t*>(c.take(cells(p) * static_cast<size_t>(GdrLayout(p->dtype, train).bytes)));
     a.train = train;
+    const mssm::GdrPieces pieces(p->tokens, p->seqs, p->heads, p->key_dim, p->value_dim, p->dtype);
+    if (pieces.shift) {
+        const size_t states = static_cast<size_t>(pieces.count * p->heads * p->key_dim) * 4;
+        a.starts = static_cast<float*>(c.take(states * p->value_dim));
+        a.moves = static_cast<float*>(c.take(states * p->key_dim));
+    }
     if (!train) return;
     a.states = static_cast<float*>(c.take(cells(p) * p->value_dim * p->key_dim * 4));
     a.misses = static_cast<float*>(c.take(cells(p) * mssm::kGdrChunk * p->value_dim * 4));

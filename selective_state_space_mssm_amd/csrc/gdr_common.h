@@ -50,28 +50,50 @@ __device__ __forceinline__ Span span_of(const int32_t* offsets, int64_t n, int64
 __device__ __forceinline__ int64_t first_slot(const Span& s, int64_t n) { return (s.start >> 6) + n; }
 static_assert(kC == 64, "first_slot divides by 64");
 
-// The sequence and chunk of a slot; len = 0: the slot is no chunk.
-struct Chunk {
-    int64_t seq, start;  // its first token
-    int len;             // tokens, up to 64
-};
-// By a whole wave, 64 sequences at a time: few loads behind one another.
-__device__ __forceinline__ Chunk chunk_of(const int32_t* offsets, int64_t slot, int64_t T, int64_t N, int64_t each) {
+// Of pieces of 2^shift tokens, numbered as the chunks are, the sequence of number
+// `slot` (if it is one of its pieces).  By a whole wave, 64 sequences at a time: few
+// loads behind one another.
+__device__ __forceinline__ int64_t sequence_of(const int32_t* offsets, int64_t slot, int64_t T, int64_t N, int64_t each, int shift) {
     const int64_t lane = threadIdx.x & 63;
     int64_t lo = 0, count = N;  // the last of `count` sequences whose first slot is not behind this one
     while (count > 1) {
         const int64_t step = (count + 63) >> 6, n = lo + lane * step;
         int64_t s = 0;
         if (lane * step < count) s = offsets ? imin64(T, offsets[n] < 0 ? 0 : offsets[n]) : n * each;
-        const int before = __builtin_popcountll(__ballot(lane * step < count && (s >> 6) + n <= slot));
+        const int before = __builtin_popcountll(__ballot(lane * step < count && (s >> shift) + n <= slot));
         const int64_t at = (before > 1 ? before - 1 : 0) * step;
         lo += at;
         count = imin64(step, count - at);
     }
-    const Span s = span_of(offsets, lo, T, each);
-    const int64_t t = (slot - first_slot(s, lo)) * kC;
-    if (t < 0 || t >= s.len) return {lo, 0, 0};
-    return {lo, s.start + t, static_cast<int>(imin64(kC, s.len - t))};
+    return lo;
+}
+
+// The sequence and chunk of a slot; len = 0: the slot is no chunk.
+struct Chunk {
+    int64_t seq, start;  // its first token
+    int len;             // tokens, up to 64
+};
+__device__ __forceinline__ Chunk chunk_of(const int32_t* offsets, int64_t slot, int64_t T, int64_t N, int64_t each) {
+    const int64_t n = sequence_of(offsets, slot, T, N, each, 6);
+    const Span s = span_of(offsets, n, T, each);
+    const int64_t t = (slot - first_slot(s, n)) * kC;
+    if (t < 0 || t >= s.len) return {n, 0, 0};
+    return {n, s.start + t, static_cast<int>(imin64(kC, s.len - t))};
+}
+
+// What a chain goes through: a whole sequence, or one of its pieces of 2^shift tokens.
+struct Piece {
+    int64_t seq, start, len, slot0;  // slot0: of its first chunk
+    bool first, last, none;          // none: not a piece (a sequence of no tokens has an empty one)
+};
+__device__ __forceinline__ Piece piece_of(const int32_t* offsets, int64_t i, int64_t T, int64_t N, int64_t each, int shift) {
+    const int64_t n = shift ? sequence_of(offsets, i, T, N, each, shift) : i;
+    const Span s = span_of(offsets, n, T, each);
+    if (!shift) return {n, s.start, s.len, first_slot(s, n), true, true, false};
+    const int64_t t = (i - ((s.start >> shift) + n)) << shift;
+    if (t < 0 || (t > 0 && t >= s.len)) return {n, 0, 0, 0, false, false, true};
+    const int64_t len = imin64(int64_t{1} << shift, s.len - t);
+    return {n, s.start + t, len, first_slot(s, n) + (t >> 6), t == 0, t + len == s.len, false};
 }
 
 // The parts of a head's value elements read the same rows and matrices: on the same

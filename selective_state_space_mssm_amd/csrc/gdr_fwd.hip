@@ -25,41 +25,59 @@ struct FwdArgs {
     float* misses;
     int64_t T, N, each, G, H, K, V, parts;
     int64_t mat_bytes, at_n, at_p, at_f;
+    int64_t pieces;
+    int shift;
+    float* starts;
+    float* moves;
 };
+
+enum Form { kForward, kTrain, kEnds };
 
 // NW waves with a tile of 16 columns each.  While a chunk is worked on, the next
 // one's rows and matrices come in: bfloat16 straight into the other half of LDS,
 // one barrier a chunk; float32 through registers, where it is cut into planes,
 // with P from memory (the L2, mostly) as the planes leave no room for it.
-template <typename T, int KP, int NW, bool TRAIN>
+// kEnds: only the state behind a piece, and what the piece makes of any row of a state:
+// a second tile of each wave starts with unit rows (one for each key element) and sees
+// values of zero.
+template <typename T, int KP, int NW, int FORM>
 __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
-    constexpr bool B16 = sizeof(T) == 2;
-    constexpr int PL = kPlanes<T>, PP = B16 ? 2 : 3, KS = KP / 32, KM = KP / 16, VC = NW * 16;
+    constexpr bool B16 = sizeof(T) == 2, TRAIN = FORM == kTrain, ENDS = FORM == kEnds;
+    constexpr int PL = kPlanes<T>, PP = B16 ? 2 : 3, KS = KP / 32, KM = KP / 16, VC = NW * 16, CT = ENDS ? 2 : 1;
     typedef Tile<KP> Keys;
     typedef Tile<VC> Values;
     constexpr int kPm = PP * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
-    constexpr int kMats = (B16 ? kPm : 0) + kN + kF;
-    constexpr int kKeys = 2 * PL * Keys::kBytes;
+    constexpr bool kPhere = B16 && !ENDS;
+    constexpr int kMats = (kPhere ? kPm : 0) + kN + kF;
+    constexpr int kKeys = (ENDS ? 1 : 2) * PL * Keys::kBytes;
     constexpr int kPart = B16 ? kKeys + Values::kBytes + kMats : kMats;  // of what LDS holds twice
     __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
-    if (at.head >= a.N * a.H) return;
-    const int64_t part = at.part, n = at.head / static_cast<uint32_t>(a.H), h = at.head - n * a.H;
+    if (at.head >= a.pieces * a.H) return;
+    const int64_t part = at.part, piece = at.head / static_cast<uint32_t>(a.H), h = at.head - piece * a.H;
     const int64_t hg = h / (a.H / a.G);
     const int64_t vw = part * VC, v0 = vw + w * 16;  // the workgroup's first value element, and the wave's
-    const bool in_v = v0 < a.V;                      // V is a multiple of 16
-    const Span sp = span_of(a.offsets, n, a.T, a.each);
-    const int64_t slot0 = first_slot(sp, n), chunks = (sp.len + kC - 1) / kC;
+    const Piece sp = piece_of(a.offsets, piece, a.T, a.N, a.each, a.shift);
+    if (sp.none || (ENDS && sp.last)) return;
+    const int64_t n = sp.seq, slot0 = sp.slot0, chunks = (sp.len + kC - 1) / kC;
     const int K = static_cast<int>(a.K);
+    const bool of_v = v0 < a.V, in_v = of_v || (ENDS && v0 < K);  // V and K are multiples of 16
 
-    f32x4 S[KM];
+    f32x4 S[CT][KM];
+    const float* start = sp.first ? a.h0 : a.starts;
+    if (ENDS && !sp.first) start = nullptr;
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
-        S[m] = f32x4{0, 0, 0, 0};
-        if (a.h0 && in_v && state_column(m, 4 * g) < K)
-            S[m] = *reinterpret_cast<const f32x4*>(a.h0 + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g));
+        const int col = state_column(m, 4 * g);
+        S[0][m] = f32x4{0, 0, 0, 0};
+        if (start && of_v && col < K)
+            S[0][m] = *reinterpret_cast<const f32x4*>(start + (((sp.first ? n : piece) * a.H + h) * a.V + v0 + c) * a.K + col);
+        if constexpr (ENDS) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[1][m][r] = col + r == v0 + c ? 1.0f : 0.0f;
+        }
     }
 
     const int64_t qk_stride = a.G * a.K, v_stride = a.H * a.V;
@@ -79,19 +97,19 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         const int len = length(chunk);
         uint8_t* to = lds + half * kPart;
         if constexpr (B16) {
-            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_p, w, lane);
+            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + (ENDS ? a.at_n : a.at_p), w, lane);
             if (part == 1) key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
-            if (part == 2) key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
+            if (part == 2 && !ENDS) key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
             if (part == 3) value_loads.load(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, len, w);
         } else {
             if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to), mats_of(chunk) + a.at_n, w, lane);
             if (part == 1) fk.load(kp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
-            if (part == 2) fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
+            if (part == 2 && !ENDS) fq.load(qp + chunk * kC * qk_stride, static_cast<uint32_t>(qk_stride), len, K, tid);
         }
     };
     f32x4 O[4];
     auto put_y = [&](int64_t chunk) {  // row 4 g + r: value elements; column c of tile rt: token 16 rt + c
-        if (!a.y || !in_v) return;
+        if (ENDS || !a.y || !in_v) return;
         const int len = length(chunk);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -107,13 +125,13 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         const int half = static_cast<int>(chunk & 1), len = length(chunk);
         const uint8_t* in = lds + half * kPart;
         const uint8_t *lds_k = B16 ? in : lds + 2 * kPart, *lds_q = lds_k + PL * Keys::kBytes, *lds_v = in + kKeys;
-        const uint8_t* lds_p = in + kKeys + (B16 ? Values::kBytes : 0);
-        const uint8_t* lds_n = B16 ? lds_p + kPm : in;
+        const uint8_t* lds_p = B16 ? in + kKeys + Values::kBytes : in;
+        const uint8_t* lds_n = kPhere ? lds_p + kPm : lds_p;
         const float* f = reinterpret_cast<const float*>(lds_n + kN);
         tile_barrier();  // this half is whole, nobody reads the other one
         if constexpr (!B16) {
             fk.store(lds + 2 * kPart, tid);
-            fq.store(lds + 2 * kPart + PL * Keys::kBytes, tid);
+            if constexpr (!ENDS) fq.store(lds + 2 * kPart + PL * Keys::kBytes, tid);
             __syncthreads();
         }
         if (chunk) put_y(chunk - 1);  // here, not when it was ready: the barrier waits for stores too
@@ -125,6 +143,8 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             continue;
         }
 
+        int c = lane & 15, g = lane >> 4;
+        if constexpr (ENDS) asm volatile("" : "+v"(c), "+v"(g));  // addresses are computed here, not kept (and spilled)
         f32x4 val[4];  // item r of tile rt: token 16 rt + 4 g + r of this lane's column
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -135,7 +155,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int t = 16 * rt + 4 * g + r;
-                    val[rt][r] = View<T>(vp + chunk * kC * v_stride).one(t * static_cast<uint32_t>(v_stride) + static_cast<uint32_t>(v0) + c, t < len);
+                    val[rt][r] = View<T>(vp + chunk * kC * v_stride).one(t * static_cast<uint32_t>(v_stride) + static_cast<uint32_t>(v0) + c, t < len && of_v);
                 }
             }
         }
@@ -143,28 +163,32 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             float* to = a.states + (((slot0 + chunk) * a.H + h) * a.V + v0 + c) * a.K;
 #pragma unroll
             for (int m = 0; m < KM; ++m)
-                if (state_column(m, 4 * g) < K) *reinterpret_cast<f32x4*>(to + state_column(m, 4 * g)) = S[m];
+                if (state_column(m, 4 * g) < K) *reinterpret_cast<f32x4*>(to + state_column(m, 4 * g)) = S[0][m];
         }
         // S k (tokens in the rows) and S q (tokens in the columns)
-        f32x4 X[4] = {};
+        f32x4 X[CT][4] = {};
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) O[rt] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const Planes<3> st = split<3>(S[2 * s], S[2 * s + 1]);
+            Planes<3> st[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) st[j] = split<3>(S[j][2 * s], S[j][2 * s + 1]);
             Planes<PP> so;
 #pragma unroll
-            for (int i = 0; i < PP; ++i) so.p[i] = st.p[i];
+            for (int i = 0; i < PP; ++i) so.p[i] = st[0].p[i];
             Planes<PL> kf[4], qf[4];
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 kf[rt] = Keys::template rows<PL>(lds_k, rt, s, c, g);
-                qf[rt] = Keys::template rows<PL>(lds_q, rt, s, c, g);
+                if constexpr (!ENDS) qf[rt] = Keys::template rows<PL>(lds_q, rt, s, c, g);
             }
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) X[rt] = mma(kf[rt], st, X[rt]);
+            for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) O[rt] = mma(so, qf[rt], O[rt]);
+                for (int j = 0; j < CT; ++j) X[j][rt] = mma(kf[rt], st[j], X[j][rt]);
+#pragma unroll
+            for (int rt = 0; rt < 4 && !ENDS; ++rt) O[rt] = mma(so, qf[rt], O[rt]);
             if (more) {
 #pragma unroll
                 for (int q = s * kParts / KS; q < (s + 1) * kParts / KS; ++q) fetch(chunk + 1, half ^ 1, q);
@@ -176,53 +200,173 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         for (int rt = 0; rt < 4; ++rt) {
             const f32x4 ek = *reinterpret_cast<const f32x4*>(f + 16 * rt + 4 * g);
             beta[rt] = *reinterpret_cast<const f32x4*>(f + kC + 16 * rt + 4 * g);
-            X[rt] = val[rt] - ek * X[rt];
+            X[0][rt] = val[rt] - ek * X[0][rt];
+            if constexpr (ENDS) X[1][rt] = -ek * X[1][rt];
         }
-        const Planes<3> mx[2] = {split<3>(beta[0] * X[0], beta[1] * X[1]), split<3>(beta[2] * X[2], beta[3] * X[3])};
+        Planes<3> mx[CT][2];
+        auto cut = [&](int s) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int j = 0; j < CT; ++j) mx[j][s] = split<3>(beta[2 * s] * X[j][2 * s], beta[2 * s + 1] * X[j][2 * s + 1]);
+        };
+        if constexpr (!ENDS) cut(0), cut(1);  // two tiles' operands at once would not fit the registers
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int s = ENDS ? 1 - i : i;   // the later rows first: that leaves the earlier ones as they are
+            if constexpr (ENDS) {
+                __builtin_amdgcn_sched_barrier(0);
+                cut(s);
+            }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt)
-                if (block_of<true>(rt, s) >= 0) X[rt] = mma(load_block<3>(lds_n, block_of<true>(rt, s), lane), mx[s], X[rt]);
+                if (block_of<true>(rt, s) >= 0) {
+                    const Planes<3> nb = load_block<3>(lds_n, block_of<true>(rt, s), lane);
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) X[j][rt] = mma(nb, mx[j][s], X[j][rt]);
+                }
+        }
         if constexpr (TRAIN) {
             float* e = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + (4 * g + (c & 3)) * a.V + v0 + (c & ~3);
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) *reinterpret_cast<f32x4*>(e + 16 * rt * a.V) = quad_transpose(X[rt], c);
+            for (int rt = 0; rt < 4; ++rt) *reinterpret_cast<f32x4*>(e + 16 * rt * a.V) = quad_transpose(X[0][rt], c);
         }
         // u; y = scale exp(b) S q + P u, and the state's update
         const float last = f[4 * kC];
-        Planes<3> ud[2];
+        Planes<3> ud[CT][2];
         Planes<PP> u[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        auto cut_u = [&](int s) {
             const f32x4 d0 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 4 * g),
                         d1 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 16 + 4 * g);
-            X[2 * s] *= beta[2 * s];
-            X[2 * s + 1] *= beta[2 * s + 1];
-            ud[s] = split<3>(d0 * X[2 * s], d1 * X[2 * s + 1]);
-            u[s] = split<PP>(X[2 * s], X[2 * s + 1]);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                X[j][2 * s] *= beta[2 * s];
+                X[j][2 * s + 1] *= beta[2 * s + 1];
+                ud[j][s] = split<3>(d0 * X[j][2 * s], d1 * X[j][2 * s + 1]);
+            }
+            u[s] = split<PP>(X[0][2 * s], X[0][2 * s + 1]);
+        };
+        if constexpr (!ENDS) cut_u(0), cut_u(1);
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int i = 0; i < KM; ++i) S[j][i] *= last;
+#pragma unroll
+        for (int rt = 0; rt < 4 && !ENDS; ++rt) O[rt] *= f[3 * kC + 16 * rt + c];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if constexpr (ENDS) {
+                __builtin_amdgcn_sched_barrier(0);
+                cut_u(s);
+            }
+#pragma unroll
+            for (int m = 0; m < KM; ++m) {
+                const Planes<PL> kt = Keys::template columns<PL>(lds_k, m, s, c, g);
+#pragma unroll
+                for (int j = 0; j < CT; ++j) S[j][m] = mma(kt, ud[j][s], S[j][m]);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < KM; ++i) S[i] *= last;
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) O[rt] *= f[3 * kC + 16 * rt + c];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int m = 0; m < KM; ++m) S[m] = mma(Keys::template columns<PL>(lds_k, m, s, c, g), ud[s], S[m]);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2 && !ENDS; ++s)
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt)
                 if (block_of<true>(rt, s) >= 0)
-                    O[rt] = mma(u[s], load_block<PP>(B16 ? lds_p : mats_of(chunk) + a.at_p, block_of<true>(rt, s), lane), O[rt]);
+                    O[rt] = mma(u[s], load_block<PP>(kPhere ? lds_p : mats_of(chunk) + a.at_p, block_of<true>(rt, s), lane), O[rt]);
+    }
+    if constexpr (ENDS) {
+        float* end = a.starts + (((piece + 1) * a.H + h) * a.V + v0 + c) * a.K;
+        float* move = a.moves + (piece * a.H + h) * a.K * a.K + v0 + c;
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+            const int col = state_column(m, 4 * g);
+            if (col < K && of_v) *reinterpret_cast<f32x4*>(end + col) = S[0][m];
+            if (col < K && v0 < K && !sp.first) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) move[(col + r) * a.K] = S[1][m][r];
+            }
+        }
+        return;
     }
     if (chunks) put_y(chunks - 1);
-    if (a.h_final && in_v) {
+    if (a.h_final && in_v && sp.last) {
 #pragma unroll
         for (int m = 0; m < KM; ++m)
             if (state_column(m, 4 * g) < K)
-                *reinterpret_cast<f32x4*>(a.h_final + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g)) = S[m];
+                *reinterpret_cast<f32x4*>(a.h_final + ((n * a.H + h) * a.V + v0 + c) * a.K + state_column(m, 4 * g)) = S[0][m];
+    }
+}
+
+// The states before a sequence's pieces, one behind the other, from the states behind
+// them (each from zeros, in the next one's place) and their moves:
+//     start' = end + start move,   rows of 16 value elements a workgroup.
+// Wave w has a quarter of the key elements, and the rows go round through LDS.
+template <int KP>
+__global__ __launch_bounds__(256) void gdr_join_kernel(FwdArgs a) {
+    constexpr int KS = KP / 32, MT = KP / 64, ROW = KP + 4;
+    __shared__ __align__(16) float rows[16 * ROW];
+    const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4, K = static_cast<int>(a.K);
+    const HeadPart at = head_part(static_cast<uint32_t>(a.parts));  // a head's moves are read by all its workgroups
+    if (at.head >= a.N * a.H) return;
+    const int64_t v0 = at.part * 16, n = at.head / static_cast<uint32_t>(a.H), h = at.head - n * a.H;
+    const Span s = span_of(a.offsets, n, a.T, a.each);
+    const int64_t first = (s.start >> a.shift) + n, count = (s.len + (int64_t{1} << a.shift) - 1) >> a.shift;
+    auto state = [&](int64_t piece, int m) { return a.starts + ((piece * a.H + h) * a.V + v0 + c) * a.K + 16 * m + 4 * g; };
+    f32x4 move[2][MT][KS][2], end[2][MT];
+    auto fetch = [&](int64_t piece, f32x4(&mv)[MT][KS][2], f32x4(&to)[MT]) {  // a piece's move, and the end that it adds to
+        const View<float> from(a.moves + (piece * a.H + h) * a.K * a.K);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = MT * w + i;
+            to[i] = 16 * m < K ? *reinterpret_cast<const f32x4*>(state(piece + 1, m)) : f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < KS; ++q)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int j = 32 * q + 8 * g + 4 * p;
+                    mv[i][q][p] = from.four((16 * m + c) * K + j, 16 * m < K && j < K);
+                }
+        }
+    };
+    auto keep = [&](const f32x4(&x)[MT]) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(rows + c * ROW + 16 * (MT * w + i) + 4 * g) = x[i];
+    };
+    auto step = [&](int64_t piece, const f32x4(&mv)[MT][KS][2], f32x4(&to)[MT]) {
+        Planes<3> in[KS];
+#pragma unroll
+        for (int q = 0; q < KS; ++q) {
+            const float* p = rows + c * ROW + 32 * q + 8 * g;
+            in[q] = split<3>(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+        }
+        __syncthreads();  // the rows are read
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int q = 0; q < KS; ++q) to[i] = mma(split<3>(mv[i][q][0], mv[i][q][1]), in[q], to[i]);
+        // the compiler leaves a wait state too few before the result is stored
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 7" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            if (16 * (MT * w + i) < K) *reinterpret_cast<f32x4*>(state(piece + 1, MT * w + i)) = to[i];
+        keep(to);
+        __syncthreads();
+    };
+    if (count < 3) return;  // the second piece starts with the first one's end
+    f32x4 x[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int m = MT * w + i;
+        x[i] = 16 * m < K ? *reinterpret_cast<const f32x4*>(state(first + 1, m)) : f32x4{0, 0, 0, 0};
+    }
+    fetch(first + 1, move[0], end[0]);
+    keep(x);
+    __syncthreads();
+    for (int64_t p = 1; p + 1 < count; p += 2) {
+        if (p + 2 < count) fetch(first + p + 1, move[1], end[1]);
+        step(first + p, move[0], end[0]);
+        if (p + 2 >= count) break;
+        if (p + 3 < count) fetch(first + p + 2, move[0], end[0]);
+        step(first + p + 1, move[1], end[1]);
     }
 }
 
@@ -499,24 +643,31 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
     }
 }
 
-template <typename T, int KP, int NW, bool TRAIN>
-hipError_t launch_v(const GdrArgs& a, hipStream_t s) {
+FwdArgs arguments(const GdrArgs& a, const GdrPieces& p, int64_t parts) {
     const GdrLayout l(a.dtype, a.train);
-    const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
-    const FwdArgs k{a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
-                    a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors};
-    gdr_fwd_kernel<T, KP, NW, TRAIN><<<xcd_grid(a.N * a.H, parts), NW * 64, 0, s>>>(k);
+    return {a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
+            a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors, p.count, p.shift, a.starts, a.moves};
+}
+template <typename T, int KP, int NW, int FORM>
+hipError_t launch_v(const GdrArgs& a, const GdrPieces& p, hipStream_t s) {
+    const int64_t parts = ((FORM == kEnds && a.K > a.V ? a.K : a.V) + 16 * NW - 1) / (16 * NW);
+    gdr_fwd_kernel<T, KP, NW, FORM><<<xcd_grid(p.count * a.H, parts), NW * 64, 0, s>>>(arguments(a, p, parts));
     return hipGetLastError();
 }
 template <typename T, int KP, int NW>
-hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
-    return a.train ? launch_v<T, KP, NW, true>(a, s) : launch_v<T, KP, NW, false>(a, s);
+hipError_t launch_c(const GdrArgs& a, const GdrPieces& p, hipStream_t s) {
+    if (p.shift) {
+        hipError_t e = launch_v<T, KP, NW, kEnds>(a, p, s);
+        if (e != hipSuccess) return e;
+        gdr_join_kernel<KP><<<xcd_grid(a.N * a.H, a.V / 16), 256, 0, s>>>(arguments(a, p, a.V / 16));
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return a.train ? launch_v<T, KP, NW, kTrain>(a, p, s) : launch_v<T, KP, NW, kForward>(a, p, s);
 }
 template <int KP>
-hipError_t launch_narrow(const GdrArgs& a, hipStream_t s) {
-    const GdrLayout l(a.dtype, a.train);
-    const FwdArgs k{a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
-                    a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, a.V / 16, l.bytes, l.n, l.pm, l.factors};
+hipError_t launch_narrow(const GdrArgs& a, const GdrPieces& p, hipStream_t s) {
+    const FwdArgs k = arguments(a, p, a.V / 16);
     const uint32_t blocks = xcd_grid(a.N * a.H, a.V / 16);
     if (a.train) gdr_fwd_narrow_kernel<KP, true><<<blocks, 64 * (KP / 32 + 4), 0, s>>>(k);
     else gdr_fwd_narrow_kernel<KP, false><<<blocks, 64 * (KP / 32 + 4), 0, s>>>(k);
@@ -529,8 +680,9 @@ hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
     // wide one: key and value dim 128, 64 heads (512 tiles) 81 / 86, 96 heads 118 / 97;
     // 128 and 64, 128 heads (512) 94 / 100, 192 heads 137 / 117; dim 64, 64 heads (256)
     // 45 / 66, 96 heads 75 / 72; 64 and 128, 32 heads (256) 44 / 64, 64 heads 70 / 67.
+    const GdrPieces p(a.T, a.N, a.H, a.K, a.V, a.dtype);
     if constexpr (sizeof(T) == 2) {
-        if (a.N * a.H * (a.V / 16) <= (KP == 128 ? 512 : 256)) return launch_narrow<KP>(a, s);
+        if (!p.shift && a.N * a.H * (a.V / 16) <= (KP == 128 ? 512 : 256)) return launch_narrow<KP>(a, p, s);
     }
     // Workgroups of 128 columns once those of 64 are more than the 256 compute units; as
     // above, us with 64 / 128 columns: 128 and 128, 128 heads 105 / 118, 160 heads 171 /
@@ -538,9 +690,9 @@ hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
     // heads 125 / 157, 160 heads 229 / 180.  Their eight waves have 256 registers each,
     // too few for the float32 planes of a key dim of 128.
     if constexpr (sizeof(T) == 2 || KP == 64) {
-        if (a.V > 64 && a.N * a.H * ((a.V + 63) / 64) > 256) return launch_c<T, KP, 8>(a, s);
+        if (a.V > 64 && p.count * a.H * ((a.V + 63) / 64) > 256) return launch_c<T, KP, 8>(a, p, s);
     }
-    return launch_c<T, KP, 4>(a, s);
+    return launch_c<T, KP, 4>(a, p, s);
 }
 template <typename T>
 hipError_t launch_t(const GdrArgs& a, hipStream_t s) {
@@ -548,6 +700,25 @@ hipError_t launch_t(const GdrArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+// Pieces of 512 tokens or more, so long that their workgroups are at most the 256
+// compute units, if a sequence then has at least 8 of them (float32: 4).  What they
+// cost is the pass over all but the last for their ends and moves, with twice the
+// columns, and the join, 3 us a piece.  us in pieces / through whole sequences (bfloat16
+// by the form for few columns), key and value dim 128: bfloat16, 16 heads, 32,768
+// tokens (16 pieces) 595 / 998, 8,192 (16) 194 / 239, 32 heads, 16,384 (8) 568 / 603,
+// 4 heads, 4,096 (8) 125 / 126, 1 head, 65,536 (128) 470 / 1,552; float32, 16 heads,
+// 2,048 tokens (4) 171 / 255, 8,192 (8) 345 / 959.
+GdrPieces::GdrPieces(int64_t T, int64_t N, int64_t H, int64_t K, int64_t V, int dtype) : count(N) {
+    const int64_t columns = V > 64 && (dtype == MSSM_BF16 || K <= 64) ? 128 : 64, least = dtype == MSSM_BF16 ? 8 : 4;
+    const int64_t units = N * H * (((K > V ? K : V) + columns - 1) / columns), each = (T + N - 1) / N;
+    if (units * least > 256) return;
+    int by = 9;
+    while ((each + (int64_t{1} << by) - 1) >> by > 256 / units) ++by;
+    if ((each + (int64_t{1} << by) - 1) >> by < least) return;
+    shift = by;
+    count = (T >> shift) + N;
+}
 
 hipError_t launch_gdr_fwd(const GdrArgs& a, hipStream_t s) {
     return a.dtype == MSSM_F32 ? launch_t<float>(a, s) : launch_t<uint16_t>(a, s);
