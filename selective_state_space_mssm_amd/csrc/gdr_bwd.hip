@@ -19,6 +19,8 @@
 //             exp(b_C) <L, S> + sum_t D_t k_t . (L u_t) more;   dg_i = sum_{t >= i} db_t
 #include "gdr_common.h"
 
+#include <type_traits>
+
 namespace mssm {
 namespace {
 
@@ -236,7 +238,7 @@ struct GradArgs {
     const float *states, *misses, *adjoints, *pulls;
     void *dq, *dk;
     float *dg, *dbeta;
-    int64_t T, N, each, G, H, K, V, slot0;
+    int64_t T, N, each, G, H, K, V;
     float scale;
     int norm;
 };
@@ -291,18 +293,18 @@ __device__ __forceinline__ float group4_sum(float v) {  // over the lanes l, l ^
 // under way; a state's columns are read by transposing reads.  Of the 64 x 64
 // matrices a wave has the blocks of its rows, transposed, and of its columns, which
 // as they lie in the accumulators are the operands that it needs next.
-template <typename T, int KP, int HALVES>
-__global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
-    constexpr int PL = kPlanes<T>, KH = KP / 16 / HALVES;  // row tiles of key elements of a wave
-    constexpr int THREADS = 256 * HALVES, WAVES = 4 * HALVES;
+template <typename T, int KP>
+__global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
+    constexpr int PL = kPlanes<T>, KH = KP / 32;  // row tiles of key elements of a wave
+    constexpr int THREADS = 512, WAVES = 8;
     typedef Tile<KP> Keys;
     typedef Tile<KP, 32> State;
     typedef TokenTile Tokens;
     constexpr int kKeys = 2 * PL * Keys::kBytes, kStaged = 6 * State::kBytes + (6 + PL) * Tokens::kBytes;
-    constexpr bool kShare = kKeys + kStaged > (HALVES == 1 ? 76 : 150) * 1024;  // q and k come after the sums, in the same place
+    constexpr bool kShare = kKeys + kStaged > 150 * 1024;  // q and k come after the sums, in the same place
     __shared__ __align__(16) uint8_t lds[kShare ? (kStaged > kKeys ? kStaged : kKeys) : kKeys + kStaged];
     __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_dots[4][kC], s_end[16];
-    static_assert(sizeof(lds) + 3500 <= 160 * 1024 / (3 - HALVES), "LDS of a compute unit");
+    static_assert(sizeof(lds) + 3500 <= 160 * 1024 && kStaged >= 2 * 5 * 4 * 1024, "LDS of a compute unit, and of the exchange");
     uint8_t *lds_k = lds, *lds_q = lds_k + PL * Keys::kBytes;
     uint8_t *lds_s = lds + (kShare ? 0 : kKeys), *lds_l = lds_s + 3 * State::kBytes, *lds_z = lds_l + 3 * State::kBytes,
             *lds_u = lds_z + 3 * Tokens::kBytes, *lds_dy = lds_u + 3 * Tokens::kBytes;
@@ -351,7 +353,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
     };
     f32x4 dq_sum[KH] = {}, dk_sum[KH] = {};
     const int per = static_cast<int>(a.H / a.G);
-    constexpr int kItems = KP * 8 / THREADS, kTokens = 512 / THREADS;  // four columns of an element each; four elements of a token
+    constexpr int kItems = KP * 8 / THREADS, kTokens = 1;  // four columns of an element each; four elements of a token
     const int to_t = tid >> 3, to_q = tid & 7;                         // and of tokens 32 further
     float to_beta[kTokens], dbeta[kTokens];
     f32x4 st_s[kItems], st_l[kItems], to_z[kTokens], to_e[kTokens], to_dy[kTokens];
@@ -409,9 +411,9 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
             s_hi[lane] = hi;
             s_lo[lane] = static_cast<float>(b - hi);
         }
-        // sums over the value elements; X: dy . u and M: Z . u, of block b the rows (tokens i) of
-        // column block w for b > w, transposed (rows: tokens j) for b <= w, and of the diagonal both
-        f32x4 yS[KH] = {}, zS[KH] = {}, uL[KH] = {}, X[4] = {}, M[4] = {}, Xd = {0, 0, 0, 0}, Md = {0, 0, 0, 0};
+        // sums over the value elements; X: dy . u, or in the waves of the second half M: Z . u, of block b the rows
+        // (tokens i) of column block w for b > w, transposed (rows: tokens j) for b <= w, and of the diagonal both
+        f32x4 yS[KH] = {}, zS[KH] = {}, uL[KH] = {}, half[5] = {};
         float both = 0.0f;
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
@@ -451,22 +453,55 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
                 uL[m] = mma(State::template columns<3>(lds_l, kh * KH + m, 0, c, g), uf, uL[m]);
                 if (m % 2) __builtin_amdgcn_sched_barrier(0);  // all operands at once would not fit the registers
             }
+            auto blocks = [&](const uint8_t* lds_x, auto& xf) {  // of Z or dy with u
+                typedef std::remove_cv_t<std::remove_reference_t<decltype(xf)>> X;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b <= w) {
-                    const Planes<3> uj = Tokens::read<3>(lds_u, 16 * b + c, g);
-                    X[b] = mma(uj, dyf, X[b]);
-                    M[b] = mma(uj, zf, M[b]);
-                } else {
-                    X[b] = mma(Tokens::read<PL>(lds_dy, 16 * b + c, g), uf, X[b]);
-                    M[b] = mma(Tokens::read<3>(lds_z, 16 * b + c, g), uf, M[b]);
+                for (int b = 0; b < 4; ++b) {
+                    if (b <= w) half[b] = mma(Tokens::read<3>(lds_u, 16 * b + c, g), xf, half[b]);
+                    else half[b] = mma(Tokens::read<sizeof(X) / 16>(lds_x, 16 * b + c, g), uf, half[b]);
+                    if (b % 2) __builtin_amdgcn_sched_barrier(0);
                 }
-                if (b % 2) __builtin_amdgcn_sched_barrier(0);
+                half[4] = mma(xf, uf, half[4]);
+            };
+            if (kh == 0) blocks(lds_dy, dyf);
+            else blocks(lds_z, zf);
+        }
+        __syncthreads();  // what was staged has been read
+        f32x4* exchange = reinterpret_cast<f32x4*>(lds_s) + wave * 5 * 64 + lane;
+        {   // with their decays: X_ij = scale G_ij dP_ij (j <= i), M_ij = -G_ij beta_i Z_i . u_j (j < i)
+            const float row_hi = s_hi[row], row_lo = s_lo[row], row_beta = s_beta[row];
+#pragma unroll
+            for (int n = 0; n < 5; ++n) {
+                const int b = n < 4 ? n : w;
+                const bool columns = n == 4 || b > w;  // rows are tokens i, the lane's is j
+                const f32x4 hi = *reinterpret_cast<const f32x4*>(s_hi + 16 * b + 4 * g), lo = *reinterpret_cast<const f32x4*>(s_lo + 16 * b + 4 * g),
+                            beta = *reinterpret_cast<const f32x4*>(s_beta + 16 * b + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int other = 16 * b + 4 * g + r, ahead = columns ? other - row : row - other;  // i - j
+                    const float sum = (hi[r] - row_hi) + (lo[r] - row_lo);
+                    const float d = ahead >= 0 ? fast_exp2((columns ? sum : -sum) * kLog2e) : 0.0f;
+                    half[n][r] *= kh == 0 ? a.scale * d : ahead > 0 ? -d * (columns ? beta[r] : row_beta) : 0.0f;
+                }
+                exchange[n * 64] = half[n];
             }
-            Xd = mma(dyf, uf, Xd);
-            Md = mma(zf, uf, Md);
+        }
+        __syncthreads();
+        f32x4 X[5], M[5];
+        {
+            const f32x4* other = reinterpret_cast<const f32x4*>(lds_s) + (wave ^ 4) * 5 * 64 + lane;
+#pragma unroll
+            for (int n = 0; n < 5; ++n) {
+                const f32x4 o = other[n * 64];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    X[n][r] = kh == 0 ? half[n][r] : o[r];
+                    M[n][r] = kh == 0 ? o[r] : half[n][r];
+                }
+            }
         }
         if constexpr (kShare) {
+            __syncthreads();  // the exchange has been read
             ask_keys();
             __syncthreads();
             keep_keys();
@@ -479,23 +514,8 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
             g_log = View<float>(a.g + ch.start * a.H + h + 1).one(lane * static_cast<uint32_t>(a.H), lane < ch.len);
         }
         const float row_hi = s_hi[row], row_lo = s_lo[row], row_beta = s_beta[row];
-        // X and M with their decays: X_ij = scale G_ij dP_ij (j <= i), M_ij = -G_ij beta_i Z_i . u_j (j < i)
         const f32x4 zero = {0, 0, 0, 0};
         auto four = [&](const float* p, int b) { return *reinterpret_cast<const f32x4*>(p + 16 * b + 4 * g); };
-        auto finish = [&](int b, bool columns, f32x4& x, f32x4& m) {  // columns: rows are tokens i, the lane's is j
-            const f32x4 hi = four(s_hi, b), lo = four(s_lo, b), beta = four(s_beta, b);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int other = 16 * b + 4 * g + r, ahead = columns ? other - row : row - other;  // i - j
-                const float sum = (hi[r] - row_hi) + (lo[r] - row_lo);
-                const float d = ahead >= 0 ? fast_exp2((columns ? sum : -sum) * kLog2e) : 0.0f;
-                x[r] *= a.scale * d;
-                m[r] *= ahead > 0 ? -d * (columns ? beta[r] : row_beta) : 0.0f;
-            }
-        };
-#pragma unroll
-        for (int b = 0; b < 4; ++b) finish(b, b > w, X[b], M[b]);
-        finish(w, true, Xd, Md);
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
             const float sum = group_sum<8>(dbeta[i]);
@@ -511,46 +531,50 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
         const double end = static_cast<double>(s_hi[kC - 1]) + s_lo[kC - 1];
         const float to_end = whole_exp(end - (static_cast<double>(row_hi) + row_lo));
         const float fy = a.scale * in_chunk, fz = -in_chunk * row_beta;
+        float wrote = 0.0f, db = 0.0f;
+        const int token = 16 * w + c;
+#pragma unroll
+        for (int m = 0; m < KH; ++m) {
+            const f32x4 k4 = rk * from_tile(lds_k, token, state_column(kh * KH + m, 4 * g));
+            yS[m] *= fy;
+            zS[m] *= fz;
+            uL[m] *= to_end;
+            wrote = dot4(k4, uL[m], wrote);
+        }
         // summed over the tokens of blocks 2 s and 2 s + 1: the lane's row of X and M, and its column
-        Planes<3> xr[2], mr[2], xc[2], mc[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            auto operand = [&](const f32x4(&x)[4], const f32x4& diagonal, bool columns, const float* factor) {
+            __builtin_amdgcn_sched_barrier(0);  // one after the other: both at once would not fit the registers
+            auto operand = [&](const f32x4(&x)[5], bool columns, const float* factor) {
                 f32x4 part[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int b = 2 * s + i;
-                    const f32x4 v = columns ? (b > w ? x[b] : b == w ? diagonal : zero) : (b <= w ? x[b] : zero);
+                    const f32x4 v = columns ? (b > w ? x[b] : b == w ? x[4] : zero) : (b <= w ? x[b] : zero);
                     part[i] = v * four(factor, b);
                 }
                 return split<3>(part[0], part[1]);
             };
-            xr[s] = operand(X, Xd, false, s_rk);
-            mr[s] = operand(M, Md, false, s_rk);
-            xc[s] = operand(X, Xd, true, s_rq);
-            mc[s] = operand(M, Md, true, s_rk);
-        }
-        float wrote = 0.0f, db = 0.0f;
+            const Planes<3> xr = operand(X, false, s_rk), mr = operand(M, false, s_rk), xc = operand(X, true, s_rq), mc = operand(M, true, s_rk);
 #pragma unroll
-        for (int m = 0; m < KH; ++m) {
-            __builtin_amdgcn_sched_barrier(0);  // one after the other: all at once would not fit the registers
-            const int col = state_column(kh * KH + m, 4 * g), token = 16 * w + c;
-            const f32x4 k4 = rk * from_tile(lds_k, token, col), q4 = rq * from_tile(lds_q, token, col);
-            f32x4 dq = fy * yS[m], dkr = fz * zS[m], dkc = to_end * uL[m];
-            wrote = dot4(k4, dkc, wrote);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int m = 0; m < KH; ++m) {
                 const Planes<PL> kt = Keys::template columns<PL>(lds_k, kh * KH + m, s, c, g);
                 const Planes<PL> qt = Keys::template columns<PL>(lds_q, kh * KH + m, s, c, g);
-                dq = mma(kt, xr[s], dq);
-                dkr = mma(kt, mr[s], dkr);
-                dkc = mma(kt, mc[s], dkc);
-                dkc = mma(qt, xc[s], dkc);
+                yS[m] = mma(kt, xr, yS[m]);
+                zS[m] = mma(kt, mr, zS[m]);
+                uL[m] = mma(kt, mc, uL[m]);
+                uL[m] = mma(qt, xc, uL[m]);
             }
-            db = dot4(q4, dq, db);
-            db = dot4(k4, dkr - dkc, db);
-            dq_sum[m] += dq;
-            dk_sum[m] += dkr + dkc;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < KH; ++m) {
+            const int col = state_column(kh * KH + m, 4 * g);
+            const f32x4 k4 = rk * from_tile(lds_k, token, col), q4 = rq * from_tile(lds_q, token, col);
+            db = dot4(q4, yS[m], db);
+            db = dot4(k4, zS[m] - uL[m], db);
+            dq_sum[m] += yS[m];
+            dk_sum[m] += zS[m] + uL[m];
         }
         __builtin_amdgcn_sched_barrier(0);
         db = group4_sum(db);
@@ -559,7 +583,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
         if (lane == 0) s_end[8 + wave] = wrote;
         __syncthreads();
         if (wave == 0) {
-            double v = static_cast<double>(s_db[0][lane]) + (HALVES == 2 ? s_db[HALVES - 1][lane] : 0.0f);
+            double v = static_cast<double>(s_db[0][lane]) + s_db[1][lane];
             if (lane == kC - 1) {
                 double states = 0.0, writes = 0.0;
 #pragma unroll
@@ -588,10 +612,8 @@ __global__ __launch_bounds__(256 * HALVES, 2) void gdr_grad_kernel(GradArgs a) {
     kd = group4_sum(kd);
     if (g == 0) s_dots[kh][row] = qd, s_dots[2 + kh][row] = kd;
     __syncthreads();
-    if constexpr (HALVES == 2) {
-        qd = s_dots[0][row] + s_dots[1][row];
-        kd = s_dots[2][row] + s_dots[3][row];
-    }
+    qd = s_dots[0][row] + s_dots[1][row];
+    kd = s_dots[2][row] + s_dots[3][row];
     T* dqp = static_cast<T*>(a.dq) + (ch.start + row) * qk_stride + hg * a.K;
     T* dkp = static_cast<T*>(a.dk) + (ch.start + row) * qk_stride + hg * a.K;
 #pragma unroll
@@ -614,9 +636,8 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const GradArgs d{a.q, a.k, a.dy, a.g, a.beta, a.offsets, a.states, a.misses, a.adjoints, a.pulls, a.dq, a.dk, a.dg, a.dbeta,
-                     a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, 0, a.scale, a.norm};
-    constexpr int HALVES = 2;
-    gdr_grad_kernel<T, KP, HALVES><<<static_cast<uint32_t>(gdr_slots(a.T, a.N) * a.G), 256 * HALVES, 0, s>>>(d);
+                     a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, a.scale, a.norm};
+    gdr_grad_kernel<T, KP><<<static_cast<uint32_t>(gdr_slots(a.T, a.N) * a.G), 512, 0, s>>>(d);
     return hipGetLastError();
 }
 template <typename T, int KP>
