@@ -19,8 +19,6 @@
 //             exp(b_C) <L, S> + sum_t D_t k_t . (L u_t) more;   dg_i = sum_{t >= i} db_t
 #include "gdr_common.h"
 
-#include <type_traits>
-
 namespace mssm {
 namespace {
 
@@ -453,12 +451,25 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
                 uL[m] = mma(State::template columns<3>(lds_l, kh * KH + m, 0, c, g), uf, uL[m]);
                 if (m % 2) __builtin_amdgcn_sched_barrier(0);  // all operands at once would not fit the registers
             }
-            auto blocks = [&](const uint8_t* lds_x, auto& xf) {  // of Z or dy with u
-                typedef std::remove_cv_t<std::remove_reference_t<decltype(xf)>> X;
+            // of Z or dy with u; the operands are chosen, not the instructions: behind a branch each read of LDS waits
+            auto blocks = [&](const uint8_t* lds_x, auto& xf) {
+                constexpr int PX = sizeof(xf) / 16;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    if (b <= w) half[b] = mma(Tokens::read<3>(lds_u, 16 * b + c, g), xf, half[b]);
-                    else half[b] = mma(Tokens::read<sizeof(X) / 16>(lds_x, 16 * b + c, g), uf, half[b]);
+                    const bool below = b <= w;
+                    Planes<3> rows, columns;
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        const uint8_t* from = below ? lds_u + p * Tokens::kBytes : lds_x + p % PX * Tokens::kBytes;
+                        rows.p[p] = Tokens::template read<1>(from, 16 * b + c, g).p[0];
+                        columns.p[p] = below ? xf.p[p % PX] : uf.p[p];
+                    }
+                    if constexpr (PX == 3) {
+                        half[b] = mma(rows, columns, half[b]);
+                    } else {
+#pragma unroll
+                        for (int p = 2; p >= 0; --p) half[b] = mma(Planes<1>{{rows.p[p]}}, Planes<1>{{columns.p[p]}}, half[b]);
+                    }
                     if (b % 2) __builtin_amdgcn_sched_barrier(0);
                 }
                 half[4] = mma(xf, uf, half[4]);
@@ -480,7 +491,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
                 for (int r = 0; r < 4; ++r) {
                     const int other = 16 * b + 4 * g + r, ahead = columns ? other - row : row - other;  // i - j
                     const float sum = (hi[r] - row_hi) + (lo[r] - row_lo);
-                    const float d = ahead >= 0 ? fast_exp2((columns ? sum : -sum) * kLog2e) : 0.0f;
+                    const float d = fast_exp2(ahead >= 0 ? (columns ? sum : -sum) * kLog2e : -1000.0f);  // 0 there
                     half[n][r] *= kh == 0 ? a.scale * d : ahead > 0 ? -d * (columns ? beta[r] : row_beta) : 0.0f;
                 }
                 exchange[n * 64] = half[n];
