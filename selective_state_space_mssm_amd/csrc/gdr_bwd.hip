@@ -653,8 +653,13 @@ hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
 }
 template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
-    if constexpr (sizeof(T) == 2 || KP == 64) {  // eight waves have 256 registers each, too few for float32 planes of 128
-        if (a.V > 64 && a.N * a.H >= 128) return launch_c<T, KP, 8>(a, s);
+    // As the forward: chains of 128 columns once those of 64 are more than the compute
+    // units.  1,024 tokens, the whole backward in us with 64 / 128 columns: key and value
+    // dim 128, 128 heads 411 / 448; 128 and 256, 72 heads 452 / 408; float32, 64 and 128,
+    // 128 heads 363 / 417, 64 and 256, 72 heads 477 / 390.  Eight waves have too few
+    // registers for the float32 planes of a key dim of 128.
+    if constexpr (sizeof(T) == 2 || KP == 64) {
+        if (a.V > 64 && a.N * a.H * ((a.V + 63) / 64) > 256) return launch_c<T, KP, 8>(a, s);
     }
     return launch_c<T, KP, 4>(a, s);
 }
