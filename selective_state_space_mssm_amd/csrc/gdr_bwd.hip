@@ -299,10 +299,11 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
     typedef Tile<KP, 32> State;
     typedef TokenTile Tokens;
     constexpr int kKeys = 2 * PL * Keys::kBytes, kStaged = 6 * State::kBytes + (6 + PL) * Tokens::kBytes;
+    constexpr int kExchange = WAVES * 5 * 1024;
     constexpr bool kShare = kKeys + kStaged > 150 * 1024;  // q and k come after the sums, in the same place
-    __shared__ __align__(16) uint8_t lds[kShare ? (kStaged > kKeys ? kStaged : kKeys) : kKeys + kStaged];
+    __shared__ __align__(16) uint8_t lds[kKeys + (kShare ? kExchange : kStaged)];
     __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_dots[4][kC], s_end[16];
-    static_assert(sizeof(lds) + 3500 <= 160 * 1024 && kStaged >= 2 * 5 * 4 * 1024, "LDS of a compute unit, and of the exchange");
+    static_assert(sizeof(lds) + 3500 <= 160 * 1024 && kStaged >= kExchange && (!kShare || kKeys >= kStaged), "LDS of a compute unit, and its parts");
     uint8_t *lds_k = lds, *lds_q = lds_k + PL * Keys::kBytes;
     uint8_t *lds_s = lds + (kShare ? 0 : kKeys), *lds_l = lds_s + 3 * State::kBytes, *lds_z = lds_l + 3 * State::kBytes,
             *lds_u = lds_z + 3 * Tokens::kBytes, *lds_dy = lds_u + 3 * Tokens::kBytes;
@@ -356,6 +357,9 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
     float to_beta[kTokens], dbeta[kTokens];
     f32x4 st_s[kItems], st_l[kItems], to_z[kTokens], to_e[kTokens], to_dy[kTokens];
     auto fetch = [&](int64_t h, int vb) {
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));  // addresses are computed here, not kept (and spilled) from before the loops
+        const int to_t = tid >> 3, to_q = tid & 7;
         const int64_t cell = slot * a.H + h;
         const View<float> S(a.states + cell * a.V * a.K), L(a.adjoints + cell * a.V * a.K);
         const View<float> e(a.misses + cell * kC * a.V), z(a.pulls + cell * kC * a.V);
@@ -421,6 +425,9 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
 #pragma unroll 1
         for (int vb = 0; vb < V; vb += 32) {
             __syncthreads();  // what is staged has been read
+            int tid = threadIdx.x;
+            asm volatile("" : "+v"(tid));  // as above
+            const int to_t = tid >> 3, to_q = tid & 7;
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
                 const int item = tid + THREADS * i, v = item / (KP / 4), k = item % (KP / 4) * 4;
@@ -439,7 +446,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             __syncthreads();
             if (vb + 32 < V) fetch(h, vb + 32);
             int c = lane & 15, g = lane >> 4;
-            asm volatile("" : "+v"(c), "+v"(g));  // addresses are computed here, not kept (and spilled) from before the loops
+            asm volatile("" : "+v"(c), "+v"(g));  // as above
             const int row = 16 * w + c;
             const Planes<3> zf = Tokens::read<3>(lds_z, row, g), uf = Tokens::read<3>(lds_u, row, g);
             const Planes<PL> dyf = Tokens::read<PL>(lds_dy, row, g);
@@ -478,7 +485,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             else blocks(lds_z, zf);
         }
         __syncthreads();  // what was staged has been read
-        f32x4* exchange = reinterpret_cast<f32x4*>(lds_s) + wave * 5 * 64 + lane;
+        f32x4* exchange = reinterpret_cast<f32x4*>(lds + kKeys) + wave * 5 * 64 + lane;  // read from there: they would not fit the registers
         {   // with their decays: X_ij = scale G_ij dP_ij (j <= i), M_ij = -G_ij beta_i Z_i . u_j (j < i)
             const float row_hi = s_hi[row], row_lo = s_lo[row], row_beta = s_beta[row];
 #pragma unroll
@@ -498,21 +505,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             }
         }
         __syncthreads();
-        f32x4 X[5], M[5];
-        {
-            const f32x4* other = reinterpret_cast<const f32x4*>(lds_s) + (wave ^ 4) * 5 * 64 + lane;
-#pragma unroll
-            for (int n = 0; n < 5; ++n) {
-                const f32x4 o = other[n * 64];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    X[n][r] = kh == 0 ? half[n][r] : o[r];
-                    M[n][r] = kh == 0 ? o[r] : half[n][r];
-                }
-            }
-        }
         if constexpr (kShare) {
-            __syncthreads();  // the exchange has been read
             ask_keys();
             __syncthreads();
             keep_keys();
@@ -556,17 +549,17 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             __builtin_amdgcn_sched_barrier(0);  // one after the other: both at once would not fit the registers
-            auto operand = [&](const f32x4(&x)[5], bool columns, const float* factor) {
+            auto operand = [&](int of, bool columns, const float* factor) {
                 f32x4 part[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int b = 2 * s + i;
-                    const f32x4 v = columns ? (b > w ? x[b] : b == w ? x[4] : zero) : (b <= w ? x[b] : zero);
-                    part[i] = v * four(factor, b);
+                    const f32x4 v = reinterpret_cast<const f32x4*>(lds + kKeys)[((4 * of + w) * 5 + (columns && b == w ? 4 : b)) * 64 + 16 * g + c];
+                    part[i] = (columns ? b >= w : b <= w) ? v * four(factor, b) : zero;
                 }
                 return split<3>(part[0], part[1]);
             };
-            const Planes<3> xr = operand(X, false, s_rk), mr = operand(M, false, s_rk), xc = operand(X, true, s_rq), mc = operand(M, true, s_rk);
+            const Planes<3> xr = operand(0, false, s_rk), mr = operand(1, false, s_rk), xc = operand(0, true, s_rq), mc = operand(1, true, s_rk);
 #pragma unroll
             for (int m = 0; m < KH; ++m) {
                 const Planes<PL> kt = Keys::template columns<PL>(lds_k, kh * KH + m, s, c, g);
