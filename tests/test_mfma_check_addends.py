@@ -1,4 +1,4 @@
-"""CPU tests of the matrix-result checker where a result is the next instruction's addend: that one may write anywhere,
+"""CPU tests of the check of matrix results where a result is the next instruction's addend: that one may write anywhere,
 and what it leaves of the result is still followed."""
 import pytest
 
