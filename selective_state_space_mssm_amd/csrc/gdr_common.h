@@ -86,10 +86,13 @@ struct Piece {
     int64_t seq, start, len, slot0;  // slot0: of its first chunk
     bool first, last, none;          // none: not a piece (a sequence of no tokens has an empty one)
 };
-__device__ __forceinline__ Piece piece_of(const int32_t* offsets, int64_t i, int64_t T, int64_t N, int64_t each, int shift) {
-    const int64_t n = shift ? sequence_of(offsets, i, T, N, each, shift) : i;
+__device__ __forceinline__ Piece whole_of(const int32_t* offsets, int64_t n, int64_t T, int64_t each) {
     const Span s = span_of(offsets, n, T, each);
-    if (!shift) return {n, s.start, s.len, first_slot(s, n), true, true, false};
+    return {n, s.start, s.len, first_slot(s, n), true, true, false};
+}
+__device__ __forceinline__ Piece piece_of(const int32_t* offsets, int64_t i, int64_t T, int64_t N, int64_t each, int shift) {
+    const int64_t n = sequence_of(offsets, i, T, N, each, shift);
+    const Span s = span_of(offsets, n, T, each);
     const int64_t t = (i - ((s.start >> shift) + n)) << shift;
     if (t < 0 || (t > 0 && t >= s.len)) return {n, 0, 0, 0, false, false, true};
     const int64_t len = imin64(int64_t{1} << shift, s.len - t);

@@ -12,7 +12,7 @@
 // 310 us, 4.8 us a chunk (matrix instructions busy for 50 % of the time on the
 // compute units in use, vector instructions for 53 %); 16 columns a workgroup, 1.7 us
 // a chunk.  For the backward the states and e are written too, 96 KB a chunk and
-// head: 8,192 packed tokens of 32 heads 360 us, 1.8 TB/s, the longest sequences alone
+// head: 8,192 packed tokens of 32 heads 332 us, 2.0 TB/s, the longest sequences alone
 // at the end.  float32, 64 and 64: 7 us a chunk, 4 waves a compute unit.
 #include "gdr_common.h"
 
@@ -47,7 +47,9 @@ enum Form { kForward, kTrain, kEnds };
 // kEnds: only the state behind a piece, and what the piece makes of any row of a state:
 // a second tile of each wave starts with unit rows (one for each key element) and sees
 // values of zero.
-template <typename T, int KP, int NW, int FORM>
+// Whole sequences are a form of their own (with both in one, 364 us for 326 of 8,192
+// packed tokens of 32 heads with what the backward needs).
+template <typename T, int KP, int NW, int FORM, bool PIECES>
 __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     constexpr bool B16 = sizeof(T) == 2, TRAIN = FORM == kTrain, ENDS = FORM == kEnds;
     constexpr int PL = kPlanes<T>, PP = B16 ? 2 : 3, KS = KP / 32, KM = KP / 16, VC = NW * 16, CT = ENDS ? 2 : 1;
@@ -66,7 +68,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     const int64_t part = at.part, piece = at.head / static_cast<uint32_t>(a.H), h = at.head - piece * a.H;
     const int64_t hg = h / (a.H / a.G);
     const int64_t vw = part * VC, v0 = vw + w * 16;  // the workgroup's first value element, and the wave's
-    const Piece sp = piece_of(a.offsets, piece, a.T, a.N, a.each, a.shift);
+    const Piece sp = PIECES ? piece_of(a.offsets, piece, a.T, a.N, a.each, a.shift) : whole_of(a.offsets, piece, a.T, a.each);
     if (sp.none || (ENDS && sp.last)) return;
     const int64_t n = sp.seq, slot0 = sp.slot0, chunks = (sp.len + kC - 1) / kC;
     const int K = static_cast<int>(a.K);
@@ -655,22 +657,23 @@ FwdArgs arguments(const GdrArgs& a, const GdrPieces& p, int64_t parts) {
     return {a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
             a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors, p.count, p.shift, a.starts, a.moves};
 }
-template <typename T, int KP, int NW, int FORM>
+template <typename T, int KP, int NW, int FORM, bool PIECES>
 hipError_t launch_v(const GdrArgs& a, const GdrPieces& p, hipStream_t s) {
     const int64_t parts = ((FORM == kEnds && a.K > a.V ? a.K : a.V) + 16 * NW - 1) / (16 * NW);
-    gdr_fwd_kernel<T, KP, NW, FORM><<<xcd_grid(p.count * a.H, parts), NW * 64, 0, s>>>(arguments(a, p, parts));
+    gdr_fwd_kernel<T, KP, NW, FORM, PIECES><<<xcd_grid(p.count * a.H, parts), NW * 64, 0, s>>>(arguments(a, p, parts));
     return hipGetLastError();
 }
 template <typename T, int KP, int NW>
 hipError_t launch_c(const GdrArgs& a, const GdrPieces& p, hipStream_t s) {
     if (p.shift) {
-        hipError_t e = launch_v<T, KP, NW, kEnds>(a, p, s);
+        hipError_t e = launch_v<T, KP, NW, kEnds, true>(a, p, s);
         if (e != hipSuccess) return e;
         gdr_join_kernel<KP><<<xcd_grid(a.N * a.H, a.V / 16), 256, 0, s>>>(arguments(a, p, a.V / 16));
         e = hipGetLastError();
         if (e != hipSuccess) return e;
+        return a.train ? launch_v<T, KP, NW, kTrain, true>(a, p, s) : launch_v<T, KP, NW, kForward, true>(a, p, s);
     }
-    return a.train ? launch_v<T, KP, NW, kTrain>(a, p, s) : launch_v<T, KP, NW, kForward>(a, p, s);
+    return a.train ? launch_v<T, KP, NW, kTrain, false>(a, p, s) : launch_v<T, KP, NW, kForward, false>(a, p, s);
 }
 template <int KP>
 hipError_t launch_narrow(const GdrArgs& a, const GdrPieces& p, hipStream_t s) {
