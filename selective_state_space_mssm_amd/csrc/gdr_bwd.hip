@@ -293,9 +293,10 @@ __device__ __forceinline__ float group4_sum(float v) {  // over the lanes l, l ^
 // .. 16 w + 15 in the columns of its accumulators and half of the key elements in
 // their rows, so that a lane's factors are one token's and it stores four neighbours.
 // 32 value elements at a time are cut into planes in LDS, with the next ones' loads
-// under way; a state's columns are read by transposing reads.  Of the 64 x 64
-// matrices a wave has the blocks of its rows, transposed, and of its columns, which
-// as they lie in the accumulators are the operands that it needs next.
+// under way; a state's columns are read by transposing reads.  Of the two 64 x 64
+// matrices the waves of one half have dy uᵀ, the others Z uᵀ, each the blocks of its
+// rows, transposed, and of its columns: as they lie in the accumulators, and are
+// exchanged through LDS, these are the operands that follow.
 template <typename T, int KP>
 __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
     constexpr int PL = kPlanes<T>, KH = KP / 32;  // row tiles of key elements of a wave

@@ -2,8 +2,8 @@
 // (mssm_gdr_fwd, mssm_gdr_fwd_train; the equations are in gdr_prep.hip).
 //
 // The columns of the state's transpose (K x V), one for each value element, do
-// not depend on one another, so each wave takes 16 or 32 of them through the
-// whole sequence by itself: the state stays in its accumulators, and every
+// not depend on one another, so each wave takes 16 of them through the whole
+// sequence by itself: the state stays in its accumulators, and every
 // product of the chain takes its float32 operand straight from the accumulators
 // of the one before.  The other operands, q, k and the chunk's matrices, are
 // shared by the waves of a workgroup.
