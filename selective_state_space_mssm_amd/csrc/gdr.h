@@ -30,6 +30,14 @@ struct GdrPieces {
     GdrPieces(int64_t T, int64_t N, int64_t H, int64_t K, int64_t V, int dtype);
 };
 
+// Which piece of a sequence (`first`, `last`: of its pieces) reads h0 in which launch:
+// the one that finds the pieces' ends (`ends`; it has no last pieces) or the one that
+// goes through them.  h_final may be h0's buffer, and its last piece's workgroup writes
+// it in the latter: there only a piece by itself reads h0, other first pieces take the
+// copy that the former made.
+constexpr bool gdr_reads_h0(bool ends, bool first, bool last) { return first && last != ends; }
+constexpr bool gdr_writes_h_final(bool ends, bool last) { return !ends && last; }
+
 // What the chunk-parallel pass leaves for each (slot, head), in bytes: the
 // matrices N and P as operands of the matrix instructions (their 6 blocks of 16
 // x 32 that are not zero, as bfloat16 planes of 1 KB that add up to the float32
@@ -63,7 +71,7 @@ struct GdrArgs {
     float* h_final;          // nullable
     // chunk matrices (slots, H, GdrLayout::bytes)
     uint8_t* mats;
-    float* starts;           // (pieces, H, V, K) the state before a piece
+    float* starts;           // (pieces, H, V, K) the state before a piece (none for a sequence of one)
     float* moves;            // (pieces, H, K, K) what a piece makes of a state's rows, transposed
     bool train;              // with the transposes, the states and the misses:
     float* states;           // (slots, H, V, K) before every chunk; null: not kept

@@ -75,15 +75,17 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     const bool of_v = v0 < a.V, in_v = of_v || (ENDS && v0 < K);  // V and K are multiples of 16
 
     f32x4 S[CT][KM];
-    const float* start = sp.first ? a.h0 : a.starts;
-    if (ENDS && !sp.first) start = nullptr;
+    const bool initial = !PIECES || gdr_reads_h0(ENDS, sp.first, sp.last);
+    const float* start = initial ? a.h0 : ENDS ? nullptr : a.starts;
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
         const int col = state_column(m, 4 * g);
         S[0][m] = f32x4{0, 0, 0, 0};
         if (start && of_v && col < K)
-            S[0][m] = *reinterpret_cast<const f32x4*>(start + (((sp.first ? n : piece) * a.H + h) * a.V + v0 + c) * a.K + col);
+            S[0][m] = *reinterpret_cast<const f32x4*>(start + (((initial ? n : piece) * a.H + h) * a.V + v0 + c) * a.K + col);
         if constexpr (ENDS) {
+            if (initial && of_v && col < K)  // for the launch that may write h_final there
+                *reinterpret_cast<f32x4*>(a.starts + ((piece * a.H + h) * a.V + v0 + c) * a.K + col) = S[0][m];
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[1][m][r] = col + r == v0 + c ? 1.0f : 0.0f;
         }
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         return;
     }
     if (chunks) put_y(chunks - 1);
-    if (a.h_final && in_v && sp.last) {
+    if (a.h_final && in_v && gdr_writes_h_final(ENDS, sp.last)) {
 #pragma unroll
         for (int m = 0; m < KM; ++m)
             if (state_column(m, 4 * g) < K)
