@@ -38,20 +38,20 @@ struct GdrPieces {
 constexpr bool gdr_reads_h0(bool ends, bool first, bool last) { return first && last != ends; }
 constexpr bool gdr_writes_h_final(bool ends, bool last) { return !ends && last; }
 
-// What the chunk-parallel pass leaves for each (slot, head), in bytes: the
-// matrices N and P as operands of the matrix instructions (their 6 blocks of 16
-// x 32 that are not zero, as bfloat16 planes of 1 KB that add up to the float32
-// value), 5 rows of 64 factors, and for the backward the transposes of both.
+// What the chunk-parallel pass leaves for each (slot, head), in bytes: of the
+// matrices N and P their 6 blocks of 16 x 32 that are not zero, in the order of the
+// matrix instructions' operands, N as three bfloat16 planes of 1 KB that add up to
+// the float32 value, P in float32 (2 KB a block, cut into the same planes by who
+// multiplies with it), 5 rows of 64 factors, and for the backward the transposes of
+// both in planes.
 constexpr int kGdrBlocks = 6;
 constexpr int kGdrBlockBytes = 1024;
 constexpr int kGdrFactors = 5;
 struct GdrLayout {
-    int p_planes;      // of P for the forward: 2 where y is bfloat16, else 3
     int64_t pm, n, factors, nt, pt, bytes;
-    GdrLayout(int dtype, bool train) {
-        p_planes = dtype == MSSM_BF16 ? 2 : 3;
+    explicit GdrLayout(bool train) {
         pm = 0;  // the forward's P, N and factors and the backward's factors and transposes lie together
-        n = pm + p_planes * kGdrBlocks * kGdrBlockBytes;
+        n = pm + 2 * kGdrBlocks * kGdrBlockBytes;
         factors = n + 3 * kGdrBlocks * kGdrBlockBytes;
         nt = factors + kGdrFactors * kGdrChunk * 4;
         pt = nt + (train ? 3 * kGdrBlocks * kGdrBlockBytes : 0);

@@ -66,7 +66,7 @@ size_t cells(const mssm_gdr_problem* p) { return static_cast<size_t>(mssm::gdr_s
 
 // Sets the places of the forward's hand-over in `c`; train: of a ctx.
 void place_forward(const mssm_gdr_problem* p, bool train, Cut& c, GdrArgs& a) {
-    a.mats = static_cast<uint8_t*>(c.take(cells(p) * static_cast<size_t>(GdrLayout(p->dtype, train).bytes)));
+    a.mats = static_cast<uint8_t*>(c.take(cells(p) * static_cast<size_t>(GdrLayout(train).bytes)));
     a.train = train;
     const mssm::GdrPieces pieces(p->tokens, p->seqs, p->heads, p->key_dim, p->value_dim, p->dtype);
     if (pieces.shift) {

@@ -638,7 +638,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
 
 template <typename T, int KP, int NW>
 hipError_t launch_c(const GdrArgs& a, hipStream_t s) {
-    const GdrLayout l(a.dtype, true);
+    const GdrLayout l(true);
     const int64_t parts = (a.V + 16 * NW - 1) / (16 * NW);
     const AdjointArgs k{a.q, a.k, a.dy, a.offsets, a.mats, a.dh_final, a.dv, a.dh0, a.adjoints, a.pulls,
                         a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.factors, l.nt, l.pt};

@@ -34,6 +34,19 @@ __device__ __forceinline__ Planes<N> load_block(const uint8_t* mat, int block, i
     return out;
 }
 
+template <int N>
+__device__ __forceinline__ void store_block(uint8_t* mat, int block, int lane, const Planes<N>& x) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(mat + (n * kGdrBlocks + block) * kGdrBlockBytes + lane * 16) = x.p[n];
+}
+// A block kept in float32, as the rows of two accumulators (as planes it is cut by split).
+__device__ __forceinline__ Planes<2> words_of(f32x4 lo, f32x4 hi) {
+    return Planes<2>{{__builtin_bit_cast(u32x4, lo), __builtin_bit_cast(u32x4, hi)}};
+}
+__device__ __forceinline__ Planes<3> split_words(const Planes<2>& w) {
+    return split<3>(__builtin_bit_cast(f32x4, w.p[0]), __builtin_bit_cast(f32x4, w.p[1]));
+}
+
 // ---- sequences --------------------------------------------------------------
 
 struct Span {

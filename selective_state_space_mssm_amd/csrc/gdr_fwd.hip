@@ -40,10 +40,13 @@ struct FwdArgs {
 
 enum Form { kForward, kTrain, kEnds };
 
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // NW waves with a tile of 16 columns each.  While a chunk is worked on, the next
 // one's rows and matrices come in: bfloat16 straight into the other half of LDS,
-// one barrier a chunk; float32 through registers, where it is cut into planes,
-// with P from memory (the L2, mostly) as the planes leave no room for it.
+// float32 through registers, where it is cut into planes.  So is P, once by the whole
+// workgroup, and lies in LDS once: it is written behind the barrier that ends the chunk
+// before, and is there behind the next one.
 // kEnds: only the state behind a piece, and what the piece makes of any row of a state:
 // a second tile of each wave starts with unit rows (one for each key element) and sees
 // values of zero.
@@ -52,16 +55,16 @@ enum Form { kForward, kTrain, kEnds };
 template <typename T, int KP, int NW, int FORM, bool PIECES>
 __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     constexpr bool B16 = sizeof(T) == 2, TRAIN = FORM == kTrain, ENDS = FORM == kEnds;
-    constexpr int PL = kPlanes<T>, PP = B16 ? 2 : 3, KS = KP / 32, KM = KP / 16, VC = NW * 16, CT = ENDS ? 2 : 1;
+    constexpr int PL = kPlanes<T>, KS = KP / 32, KM = KP / 16, VC = NW * 16, CT = ENDS ? 2 : 1;
     typedef Tile<KP> Keys;
     typedef Tile<VC> Values;
-    constexpr int kPm = PP * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
-    constexpr bool kPhere = B16 && !ENDS;
-    constexpr int kMats = (kPhere ? kPm : 0) + kN + kF;
+    constexpr int kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4, kMats = kN + kF;
+    constexpr int kOwn = (kGdrBlocks + NW - 1) / NW;  // blocks of P that a wave cuts
     constexpr int kKeys = (ENDS ? 1 : 2) * PL * Keys::kBytes;
     constexpr int kPart = B16 ? kKeys + Values::kBytes + kMats : kMats;  // of what LDS holds twice
-    __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys)];
+    __shared__ __align__(16) uint8_t lds[2 * kPart + (B16 ? 0 : kKeys) + (ENDS ? 0 : kN)];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
+    uint8_t* lds_p = lds + 2 * kPart + (B16 ? 0 : kKeys);
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
     if (at.head >= a.pieces * a.H) return;
@@ -101,14 +104,23 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     const RowsToLds<KP, NW> key_loads(static_cast<uint32_t>(qk_stride), K, w, lane);
     const RowsToLds<VC, NW> value_loads(static_cast<uint32_t>(v_stride), static_cast<int>(a.V - vw), w, lane);
     FloatRows<KP, NW * 64> fk, fq;
+    Planes<2> pw[kOwn];
     // In four parts: a compute unit takes 1 KB into LDS in about 30 cycles, the 80 KB
     // of a bfloat16 chunk in 2,500, for which its waves would otherwise wait at once.
     constexpr int kParts = 4;
     auto fetch = [&](int64_t chunk, int half, int part) {
         const int len = length(chunk);
         uint8_t* to = lds + half * kPart;
+        if (part == 0 && !ENDS) {
+            const View<float> words(reinterpret_cast<const float*>(mats_of(chunk) + a.at_p));
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    pw[i].p[p] = words.words4((p * kGdrBlocks + i * NW + w) * 256 + lane * 4, i * NW + w < kGdrBlocks);
+        }
         if constexpr (B16) {
-            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + (ENDS ? a.at_n : a.at_p), w, lane);
+            if (part == 0) bytes_to_lds<NW, kMats>(lds_offset(to) + kKeys + Values::kBytes, mats_of(chunk) + a.at_n, w, lane);
             if (part == 1) key_loads.load(lds_offset(to), kp + chunk * kC * qk_stride, len, w);
             if (part == 2 && !ENDS) key_loads.load(lds_offset(to) + Keys::kBytes, qp + chunk * kC * qk_stride, len, w);
             if (part == 3) value_loads.load(lds_offset(to) + kKeys, vp + vw + chunk * kC * v_stride, len, w);
@@ -136,10 +148,14 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         const int half = static_cast<int>(chunk & 1), len = length(chunk);
         const uint8_t* in = lds + half * kPart;
         const uint8_t *lds_k = B16 ? in : lds + 2 * kPart, *lds_q = lds_k + PL * Keys::kBytes, *lds_v = in + kKeys;
-        const uint8_t* lds_p = B16 ? in + kKeys + Values::kBytes : in;
-        const uint8_t* lds_n = kPhere ? lds_p + kPm : lds_p;
+        const uint8_t* lds_n = B16 ? in + kKeys + Values::kBytes : in;
         const float* f = reinterpret_cast<const float*>(lds_n + kN);
-        tile_barrier();  // this half is whole, nobody reads the other one
+        tile_barrier();  // this half is whole, nobody reads the other one, nor P
+        if constexpr (!ENDS) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+                if (i * NW + w < kGdrBlocks) store_block(lds_p, i * NW + w, lane, split_words(pw[i]));
+        }
         if constexpr (!B16) {
             fk.store(lds + 2 * kPart, tid);
             if constexpr (!ENDS) fq.store(lds + 2 * kPart + PL * Keys::kBytes, tid);
@@ -148,6 +164,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         if (chunk) put_y(chunk - 1);  // here, not when it was ready: the barrier waits for stores too
         const bool more = chunk + 1 < chunks;
         if (!in_v) {
+            if constexpr (B16 && !ENDS) lds_barrier();  // as below
 #pragma unroll
             for (int q = 0; q < kParts; ++q)
                 if (more) fetch(chunk + 1, half ^ 1, q);
@@ -185,9 +202,6 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             Planes<3> st[CT];
 #pragma unroll
             for (int j = 0; j < CT; ++j) st[j] = split<3>(S[j][2 * s], S[j][2 * s + 1]);
-            Planes<PP> so;
-#pragma unroll
-            for (int i = 0; i < PP; ++i) so.p[i] = st[0].p[i];
             Planes<PL> kf[4], qf[4];
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
@@ -199,12 +213,13 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
 #pragma unroll
                 for (int j = 0; j < CT; ++j) X[j][rt] = mma(kf[rt], st[j], X[j][rt]);
 #pragma unroll
-            for (int rt = 0; rt < 4 && !ENDS; ++rt) O[rt] = mma(so, qf[rt], O[rt]);
+            for (int rt = 0; rt < 4 && !ENDS; ++rt) O[rt] = mma(st[0], qf[rt], O[rt]);
             if (more) {
 #pragma unroll
                 for (int q = s * kParts / KS; q < (s + 1) * kParts / KS; ++q) fetch(chunk + 1, half ^ 1, q);
             }
         }
+        if constexpr (B16 && !ENDS) lds_barrier();  // P is there
         // e = r + N (beta r) with r = v - exp(b) S k
         f32x4 beta[4];
 #pragma unroll
@@ -243,7 +258,6 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
         // u; y = scale exp(b) S q + P u, and the state's update
         const float last = f[4 * kC];
         Planes<3> ud[CT][2];
-        Planes<PP> u[2];
         auto cut_u = [&](int s) {
             const f32x4 d0 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 4 * g),
                         d1 = *reinterpret_cast<const f32x4*>(f + 2 * kC + 32 * s + 16 + 4 * g);
@@ -253,7 +267,6 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
                 X[j][2 * s + 1] *= beta[2 * s + 1];
                 ud[j][s] = split<3>(d0 * X[j][2 * s], d1 * X[j][2 * s + 1]);
             }
-            u[s] = split<PP>(X[0][2 * s], X[0][2 * s + 1]);
         };
         if constexpr (!ENDS) cut_u(0), cut_u(1);
 #pragma unroll
@@ -276,11 +289,13 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
             }
         }
 #pragma unroll
-        for (int s = 0; s < 2 && !ENDS; ++s)
+        for (int s = 0; s < 2 && !ENDS; ++s) {
+            const Planes<3> u = split<3>(X[0][2 * s], X[0][2 * s + 1]);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt)
                 if (block_of<true>(rt, s) >= 0)
-                    O[rt] = mma(u[s], load_block<PP>(kPhere ? lds_p : mats_of(chunk) + a.at_p, block_of<true>(rt, s), lane), O[rt]);
+                    O[rt] = mma(u, load_block<3>(lds_p, block_of<true>(rt, s), lane), O[rt]);
+        }
     }
     if constexpr (ENDS) {
         float* end = a.starts + (((piece + 1) * a.H + h) * a.V + v0 + c) * a.K;
@@ -397,8 +412,6 @@ __device__ __forceinline__ void put_half(uint8_t* area, int rt, f32x4 x, int lan
 
 // ---- few columns: the waves of a workgroup share a tile of 16 ------------------------
 
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 // One tile of 16 columns a workgroup, bfloat16.  What the next chunk waits for is
 // cut over KS waves: each has 32 key elements of the state, multiplies its part of
 // S k, and after an exchange through LDS has a part of the rows of e and u.  Four
@@ -408,15 +421,15 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // issued between each two barriers, in the order in which they are needed.
 template <int KP, bool TRAIN>
 __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdArgs a) {
-    constexpr int KS = KP / 32, RPW = 4 / KS, PP = 2;  // RPW: row tiles of a chain wave
+    constexpr int KS = KP / 32, RPW = 4 / KS;  // RPW: row tiles of a chain wave
     typedef Tile<KP> Keys;
-    constexpr int kPm = PP * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
-    constexpr int kV = kC * 32, kPart = 2 * Keys::kBytes + kPm + kN + kF + kV;
-    constexpr int kX = KS * (4 - RPW) * 1024, kS = KS * PP * 1024, kM = 2 * 3 * 1024;
-    constexpr int kU = 2 * (3 + PP) * 1024, kXU = kX > kU ? kX : kU;  // u lies where the sums were
-    __shared__ __align__(16) uint8_t lds[2 * kPart + kXU + kS + kM];
+    constexpr int kPm = 2 * kGdrBlocks * kGdrBlockBytes, kN = 3 * kGdrBlocks * kGdrBlockBytes, kF = kGdrFactors * kC * 4;
+    constexpr int kV = kC * 32, kPart = 2 * Keys::kBytes + kN + kF + kV;
+    constexpr int kX = KS * (4 - RPW) * 1024, kS = KS * 3 * 1024, kM = 2 * 3 * 1024;
+    constexpr int kU = 2 * (3 + 3) * 1024, kXU = kX > kU ? kX : kU;  // u lies where the sums were
+    __shared__ __align__(16) uint8_t lds[2 * kPart + kXU + kS + kM + kPm];
     static_assert(sizeof(lds) <= 160 * 1024, "LDS of a compute unit");
-    uint8_t *s_x = lds + 2 * kPart, *s_ud = s_x, *s_u = s_ud + 2 * 3 * 1024, *s_s = s_x + kXU, *s_m = s_s + kS;
+    uint8_t *s_x = lds + 2 * kPart, *s_ud = s_x, *s_u = s_ud + 2 * 3 * 1024, *s_s = s_x + kXU, *s_m = s_s + kS, *lds_p = s_m + kM;
     const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const HeadPart at = head_part(static_cast<uint32_t>(a.parts));
     if (at.head >= a.N * a.H) return;
@@ -441,7 +454,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
         }
         for (int64_t chunk = 0; chunk < chunks; ++chunk) {
             const uint8_t* in = lds + (chunk & 1) * kPart;
-            const uint8_t* lds_n = in + 2 * Keys::kBytes + kPm;
+            const uint8_t* lds_n = in + 2 * Keys::kBytes;
             const float* f = reinterpret_cast<const float*>(lds_n + kN);
             const uint8_t* lds_v = lds_n + kN + kF;
             const Planes<3> st = split<3>(S[0], S[1]);
@@ -460,7 +473,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) kf[rt] = Keys::template rows<1>(in, rt, w, c, g);
 #pragma unroll
-                for (int i = 0; i < PP; ++i) *piece(s_s, w * PP + i) = st.p[i];
+                for (int i = 0; i < 3; ++i) *piece(s_s, 3 * w + i) = st.p[i];
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) X[rt] = mma(kf[rt], st, X[rt]);
             }
@@ -540,7 +553,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
             for (int i = 0; i < RPW; ++i) {
                 const f32x4 u = beta[i] * e[i];
                 put_half<3>(s_ud, w * RPW + i, ed[i] * u, lane);
-                put_half<PP>(s_u, w * RPW + i, u, lane);
+                put_half<3>(s_u, w * RPW + i, u, lane);
             }
             if constexpr (TRAIN) {
                 float* to = a.misses + ((slot0 + chunk) * a.H + h) * kC * a.V + (4 * g + (c & 3)) * a.V + v0 + (c & ~3);
@@ -583,7 +596,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
         auto mats = [&](int64_t chunk) { return a.mats + ((slot0 + chunk) * a.H + h) * a.mat_bytes + a.at_p; };
         auto fetch_k = [&](int64_t chunk) { loads.load(to_half(chunk), kp + chunk * kC * qk_stride, length(chunk), rt); };
         auto fetch_n = [&](int64_t chunk) {
-            const uint32_t to = to_half(chunk) + 2 * Keys::kBytes + kPm;
+            const uint32_t to = to_half(chunk) + 2 * Keys::kBytes;
             if (rt < 2) {  // two lanes a row
                 const int row = 32 * rt + lane / 2;
                 load_to_lds(to + kN + kF + rt * 1024, buffer_words(vp + chunk * kC * v_stride, 0x7ffffff0u),
@@ -592,7 +605,9 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
             bytes_to_lds<4, kN + kF>(to, mats(chunk) + kPm, rt, lane);
         };
         auto fetch_q = [&](int64_t chunk) { loads.load(to_half(chunk) + Keys::kBytes, qp + chunk * kC * qk_stride, length(chunk), rt); };
-        auto fetch_p = [&](int64_t chunk) { bytes_to_lds<4, kPm>(to_half(chunk) + 2 * Keys::kBytes, mats(chunk), rt, lane); };
+        // it lies there once, and is read before the barrier that this comes behind
+        auto fetch_p = [&](int64_t chunk) { bytes_to_lds<4, kPm>(lds_offset(lds_p), mats(chunk), rt, lane); };
+        auto planes = [&](uint8_t* area, int i) { return Planes<3>{{*piece(area, 3 * i), *piece(area, 3 * i + 1), *piece(area, 3 * i + 2)}}; };
         f32x4 O;
         auto put_y = [&](int64_t chunk) {
             const int t = 16 * rt + c;
@@ -607,8 +622,8 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
         }
         for (int64_t chunk = 0; chunk < chunks; ++chunk) {
             const uint8_t* in = lds + (chunk & 1) * kPart;
-            const uint8_t *lds_q = in + Keys::kBytes, *lds_p = lds_q + Keys::kBytes;
-            const float* f = reinterpret_cast<const float*>(lds_p + kPm + kN);
+            const uint8_t* lds_q = in + Keys::kBytes;
+            const float* f = reinterpret_cast<const float*>(lds_q + Keys::kBytes + kN);
             const bool more = chunk + 1 < chunks;
             wait_memory<kOthers>();
             lds_barrier();
@@ -622,20 +637,15 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
             if (chunk) put_y(chunk - 1);  // not earlier: the waits above would be for it too
             if (more) fetch_q(chunk + 1);
             Planes<1> qf[KS];
-            Planes<PP> pb[2];
+            Planes<2> pb[2];
 #pragma unroll
             for (int s = 0; s < KS; ++s) qf[s] = Keys::template rows<1>(lds_q, rt, s, c, g);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) pb[s] = load_block<PP>(lds_p, rt < 2 ? rt : 2 * rt - 2 + s, lane);
+            for (int s = 0; s < 2; ++s) pb[s] = load_block<2>(lds_p, rt < 2 ? rt : 2 * rt - 2 + s, lane);
             const float eq = f[3 * kC + 16 * rt + c];
             O = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                Planes<PP> st;
-#pragma unroll
-                for (int i = 0; i < PP; ++i) st.p[i] = *piece(s_s, s * PP + i);
-                O = mma(st, qf[s], O);
-            }
+            for (int s = 0; s < KS; ++s) O = mma(planes(s_s, s), qf[s], O);
             O *= eq;
             lds_barrier();
             if (more) fetch_n(chunk + 1);
@@ -644,10 +654,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (s && rt < 2) break;
-                Planes<PP> u;
-#pragma unroll
-                for (int i = 0; i < PP; ++i) u.p[i] = *piece(s_u, s * PP + i);
-                O = mma(u, pb[s], O);
+                O = mma(planes(s_u, s), split_words(pb[s]), O);
             }
         }
         if (chunks) put_y(chunks - 1);
@@ -655,7 +662,7 @@ __global__ __launch_bounds__(64 * (KP / 32 + 4)) void gdr_fwd_narrow_kernel(FwdA
 }
 
 FwdArgs arguments(const GdrArgs& a, const GdrPieces& p, int64_t parts) {
-    const GdrLayout l(a.dtype, a.train);
+    const GdrLayout l(a.train);
     return {a.q, a.k, a.v, a.offsets, a.mats, a.h0, a.y, a.h_final, a.states, a.misses,
             a.T, a.N, a.T / a.N, a.G, a.H, a.K, a.V, parts, l.bytes, l.n, l.pm, l.factors, p.count, p.shift, a.starts, a.moves};
 }

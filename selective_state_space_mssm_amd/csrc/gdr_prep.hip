@@ -125,7 +125,7 @@ constexpr int kWaves = 4;
 
 template <typename T, int KS, bool TRAIN>
 __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && TRAIN ? 1 : 2) void gdr_prep_kernel(PrepArgs a) {
-    constexpr int PL = kPlanes<T>, PP = sizeof(T) == 2 ? 2 : 3;
+    constexpr int PL = kPlanes<T>;
     __shared__ __align__(16) float shared[kWaves][8][kC];
     const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
     const int64_t cell = static_cast<int64_t>(blockIdx.x) * kWaves + w;
@@ -241,17 +241,13 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && TRAIN ? 1 : 2) void 
             if constexpr (TRAIN) qk[i][i][r] = row >= c ? qk[i][i][r] * down * qr[r] * kc : 0.0f;
         }
     }
-    auto put = [&](int64_t to, int block, auto planes) {
-#pragma unroll
-        for (int n = 0; n < static_cast<int>(sizeof(planes.p) / sizeof(planes.p[0])); ++n)
-            *reinterpret_cast<u32x4*>(out + to + (n * kGdrBlocks + block) * kGdrBlockBytes + lane * 16) = planes.p[n];
-    };
+    auto put = [&](int64_t to, int block, auto planes) { store_block(out + to, block, lane, planes); };
     const f32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            if (block_of<true>(i, s) >= 0) put(a.at_p, block_of<true>(i, s), split<PP>(kq[2 * s][i], 2 * s + 1 <= i ? kq[2 * s + 1][i] : zero));
+            if (block_of<true>(i, s) >= 0) put(a.at_p, block_of<true>(i, s), words_of(kq[2 * s][i], 2 * s + 1 <= i ? kq[2 * s + 1][i] : zero));
             if constexpr (TRAIN)
                 if (block_of<false>(i, s) >= 0) put(a.at_pt, block_of<false>(i, s), split<3>(2 * s >= i ? qk[2 * s][i] : zero, qk[2 * s + 1][i]));
         }
@@ -301,7 +297,7 @@ void launch_t(const PrepArgs& k, bool train, uint32_t blocks, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_gdr_prep(const GdrArgs& a, hipStream_t s) {
-    const GdrLayout l(a.dtype, a.train);
+    const GdrLayout l(a.train);
     const int64_t cells = gdr_slots(a.T, a.N) * a.H;
     const PrepArgs k{a.q, a.k, a.g, a.beta, a.offsets, a.mats, a.T, a.N, a.T / a.N, cells, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.H),
                      static_cast<uint32_t>(a.K), a.scale, a.norm, l.bytes, l.n, l.pm, l.factors, l.nt, l.pt};
