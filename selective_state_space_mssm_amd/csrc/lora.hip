@@ -2,7 +2,7 @@
 // (mssm_lora): y[m] += scale[i] (x[m] A_iᵀ) B_iᵀ with i = index[m].
 //
 // Two launches, down to the rank and up again; what lies between is float32 in
-// the workspace.  Many rows: tiles of 16 or 64 rows on the matrix cores, each
+// the workspace.  Many rows: tiles of 16, 32 or 64 rows on the matrix cores, each
 // tile once for every adapter that its rows name (packed requests: one or two),
 // the other rows' results unused.  Few rows: a row for itself, by dot products,
 // since each mostly has an adapter of its own and its weights are read once.
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256, 2) void lora_down_kernel(LoraKernelArgs a) {
 // The rows' inner values are cut into planes once for the workgroup's 256 columns.
 template <typename W, typename Y, int RS, int MT>
 __global__ __launch_bounds__(256, 2) void lora_up_kernel(LoraKernelArgs a) {
-    constexpr int PT = sizeof(Y) == 2 && sizeof(W) == 2 ? 2 : 3;  // planes of the inner values
+    constexpr int PT = 3;  // planes of the inner values, which are float32 whatever y is
     constexpr int ROW = RS * 64 + 16, PLANE = 16 * MT * ROW;      // 16 bytes apart: the 16 rows of a read on different banks
     __shared__ __align__(16) uint8_t lds[PT * PLANE];
     const int lane = threadIdx.x & 63, w = wave_id(), c = lane & 15, g = lane >> 4;
