@@ -138,7 +138,8 @@ mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float
 #define MSSM_MAX_RANK 128
 
 typedef struct {
-    int64_t rows;      /* >= 1, below 2^28 */
+    int64_t rows;      /* >= 1, below 2^28; ceil(rows / 32) ceil(out_dim / 256) below 2^24, with MSSM_F32 and a
+                          rank above 64 ceil(rows / 16) ceil(out_dim / 256) (else MSSM_ERR_SHAPE) */
     int64_t in_dim;    /* >= 1, below 2^20 */
     int64_t out_dim;   /* >= 1, below 2^23 */
     int64_t rank;      /* 1 .. MSSM_MAX_RANK (else MSSM_ERR_UNSUPPORTED) */

@@ -72,7 +72,8 @@ mssm_status check_lora(const mssm_lora_problem* p) {
     if (p->rows >= (int64_t{1} << 28) || p->in_dim >= (int64_t{1} << 20) || p->out_dim >= (int64_t{1} << 23) ||
         p->adapters >= (int64_t{1} << 31))
         return MSSM_ERR_SHAPE;
-    if ((p->rows + 31) / 32 * ((p->out_dim + 255) / 256) >= (int64_t{1} << 24)) return MSSM_ERR_SHAPE;  // beyond any memory
+    const int64_t tile = mssm::plan_lora(p->rows, p->in_dim, p->rank, p->dtype == MSSM_F32).rows == 16 ? 16 : 32;  // or more
+    if ((p->rows + tile - 1) / tile * ((p->out_dim + 255) / 256) >= (int64_t{1} << 24)) return MSSM_ERR_SHAPE;
     return MSSM_OK;
 }
 
