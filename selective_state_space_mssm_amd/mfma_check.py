@@ -9,8 +9,8 @@ product wrong in the last two values of its last accumulator).  ``check_asm``
 follows every path from every matrix instruction and reports each instruction
 that reads or writes part of its result too early.  Matrix instructions that take
 it whole as their accumulator are interlocked and are not reported, nor are those
-that only write to its registers and take as long or longer: matrix instructions of
-one length end in the order in which they begin.
+that only write to its registers and are known (``PASSES``) to take as long or
+longer: matrix instructions of one length end in the order in which they begin.
 
 ``__graft_entry__.build`` runs it on the assembly of the library it builds and
 fails the build on any finding.
@@ -52,7 +52,7 @@ def _adds_to(dst, op, args):
 def _overwrites(dst, first, op, args):
     """A matrix instruction that reads nothing of the result and takes at least as long: they end in order, so what it
     writes of the result's registers is its own."""
-    if not op.startswith("v_mfma") or PASSES.get(op, 16) < PASSES.get(first, 16):
+    if not op.startswith("v_mfma") or op not in PASSES or PASSES[op] < PASSES.get(first, 16):  # unlisted: maybe a short one
         return False
     return not any(dst & _regs(p) for p in re.split(r",\s*(?![^\[]*\])", args)[1:4])
 
