@@ -12,6 +12,7 @@ remembered by the sizes they follow from.
 from __future__ import annotations
 
 import ctypes
+import operator
 from functools import lru_cache
 
 import torch
@@ -160,7 +161,7 @@ def _norm_args(x, weight, residual, residual_out, eps):
         residual_out = torch.empty_like(residual)
     if not eps >= 0.0:
         raise ValueError(f"eps = {eps} must not be negative")
-    return _norm_problem(x.numel() // D if D else 0, D, code, rcode, eps)[0], residual_out, dev
+    return _norm_problem(x.numel() // D if D else 0, D, code, rcode, float(eps))[0], residual_out, dev  # by its value
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None):
@@ -347,7 +348,7 @@ def beam_select(logits, scores, finished=None, end_token=None, scores_out=None, 
         token = torch.empty_like(parent)
     else:
         _req(token, "token", (B, K), torch.int32, dev)
-    prob, nbytes, _ = _beam_problem(B, K, V, code, -1 if end_token is None else end_token)
+    prob, nbytes, _ = _beam_problem(B, K, V, code, -1 if end_token is None else operator.index(end_token))
     ws = _workspace(nbytes, logits.device, workspace)
     if _current_device() != dev:
         with torch.cuda.device(dev):

@@ -48,9 +48,14 @@ _declare()
 
 
 @lru_cache(maxsize=1024)
-def _problem(tokens, seqs, groups, heads, kdim, vdim, code, norm, scale, size_of):
-    p = GdrProblem(tokens, seqs, groups, heads, kdim, vdim, code, norm, kdim ** -0.5 if scale is None else scale)
+def _remembered(tokens, seqs, groups, heads, kdim, vdim, code, norm, scale, size_of):
+    p = GdrProblem(tokens, seqs, groups, heads, kdim, vdim, code, norm, scale)
     return ctypes.byref(p), int(getattr(lib, size_of)(ctypes.byref(p))) if size_of else 0, p
+
+
+def _problem(tokens, seqs, groups, heads, kdim, vdim, code, norm, scale, size_of):
+    # by the scale's value: a tensor of one number is the same one when its value is another
+    return _remembered(tokens, seqs, groups, heads, kdim, vdim, code, norm, kdim ** -0.5 if scale is None else float(scale), size_of)
 
 
 def _first(t, name, dims):
