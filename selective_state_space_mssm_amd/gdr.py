@@ -124,7 +124,8 @@ def gdr_fwd(q, k, v, g, beta, h0=None, offsets=None, scale=None, norm_qk=False, 
     from token offsets[n] to offsets[n + 1] - 1 (in ascending order; tokens of
     no sequence are left as they are); N = B without.  norm_qk: q and k divided
     by their lengths; scale: K ** -0.5 by default.  h_final may be h0.
-    Returns (y, h_final) (h_final None unless requested)."""
+    Returns (y, h_final) (h_final None unless requested).  No gradient is
+    recorded, also of tensors that require one: gdr_bwd computes them."""
     return _forward(lib.mssm_gdr_fwd, "mssm_gdr_fwd_workspace_bytes", q, k, v, g, beta, h0, offsets, scale, norm_qk,
                     return_final_state, y, h_final, workspace)[:2]
 
@@ -132,7 +133,9 @@ def gdr_fwd(q, k, v, g, beta, h0=None, offsets=None, scale=None, norm_qk=False, 
 def gdr_fwd_train(q, k, v, g, beta, h0=None, offsets=None, scale=None, norm_qk=False, return_final_state=True, y=None,
                   h_final=None, ctx=None):
     """gdr_fwd that also saves the training context for gdr_bwd_saved.  Returns
-    (y, h_final, ctx); ctx is a uint8 device tensor (pass one to reuse it)."""
+    (y, h_final, ctx); ctx is a uint8 device tensor (pass one to reuse it).  No
+    gradient is recorded, also of tensors that require one: gdr_bwd_saved
+    computes them."""
     return _forward(lib.mssm_gdr_fwd_train, "mssm_gdr_ctx_bytes", q, k, v, g, beta, h0, offsets, scale, norm_qk,
                     return_final_state, y, h_final, ctx)
 
