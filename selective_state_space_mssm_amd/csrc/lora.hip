@@ -40,43 +40,9 @@ __device__ __forceinline__ void stream(void* p, V v) {
     __builtin_nontemporal_store(v, static_cast<Anywhere*>(p));
 }
 
-template <int N>
-__device__ __forceinline__ Planes<N> widen(const float (&x)[8]) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[i];
-    return split<N>(v);
-}
 __device__ __forceinline__ void to_floats(u32x4 q, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(q[i]), v[2 * i + 1] = bf16_hi(q[i]);
-}
-__device__ __forceinline__ float load_one(const float* p) { return *p; }
-__device__ __forceinline__ float load_one(const uint16_t* p) { return load_act(p, 0); }
-__device__ __forceinline__ float load_one(const uint8_t* p) { return __builtin_amdgcn_cvt_f32_fp8(*p, 0); }
-__device__ __forceinline__ void load_eight(const float* p, float (&v)[8]) {
-    const f32x4 a = reinterpret_cast<const Loose<f32x4>*>(p)->v, b = reinterpret_cast<const Loose<f32x4>*>(p + 4)->v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-}
-__device__ __forceinline__ void load_eight(const uint16_t* p, float (&v)[8]) { to_floats(reinterpret_cast<const Loose<u32x4>*>(p)->v, v); }
-__device__ __forceinline__ void load_eight(const uint8_t* p, float (&v)[8]) {
-    const u32x2 q = reinterpret_cast<const Loose<u32x2>*>(p)->v;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q[i]), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q[i]), true);
-        v[4 * i] = lo[0]; v[4 * i + 1] = lo[1]; v[4 * i + 2] = hi[0]; v[4 * i + 3] = hi[1];
-    }
-}
-// Elements k .. k + 7 of a row of `end`; zeros behind its end.
-template <typename T>
-__device__ __forceinline__ void load_part(const T* row, int64_t k, int64_t end, float (&v)[8]) {
-    if (k + 8 <= end) {
-        load_eight(row + k, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = k + i < end ? load_one(row + k + i) : 0.0f;
-    }
 }
 __device__ __forceinline__ void store_eight(float* p, const float (&v)[8]) {
     stream(p, f32x4{v[0], v[1], v[2], v[3]});
@@ -143,16 +109,27 @@ template <> struct Eight<uint8_t> {
             for (int j = 0; j < 4; ++j) v[i] |= k + 4 * i + j < end ? static_cast<uint32_t>(row[k + 4 * i + j]) << (8 * j) : 0u;
         }
     }
-    __device__ __forceinline__ Planes<1> planes() const {  // widened, which is exact
-        float x[8];
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[i]), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[i]), true);
             x[4 * i] = lo[0]; x[4 * i + 1] = lo[1]; x[4 * i + 2] = hi[0]; x[4 * i + 3] = hi[1];
         }
+    }
+    __device__ __forceinline__ Planes<1> planes() const {  // widened, which is exact
+        float x[8];
+        floats(x);
         return split<1>(x);
     }
 };
+// Elements k .. k + 7 of a row of `end`; zeros behind its end.
+template <typename T>
+__device__ __forceinline__ void floats_of(const T* row, int64_t k, int64_t end, float (&v)[8]) {
+    Eight<T> e;
+    if (k + 8 <= end) e.load(row + k);
+    else e.load_part(row, k, end);
+    e.floats(v);
+}
 
 // ---- few rows ---------------------------------------------------------------------
 
@@ -174,8 +151,8 @@ __global__ __launch_bounds__(256) void lora_row_down_kernel(LoraKernelArgs a) {
     float s = 0.0f;
     for (int64_t k = lane * 8; k < a.K; k += 512) {
         float p[8], q[8];
-        load_part(x, k, a.K, p);
-        load_part(w, k, a.K, q);
+        floats_of(x, k, a.K, p);
+        floats_of(w, k, a.K, q);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(p[j], q[j], s);
     }
@@ -197,7 +174,7 @@ __global__ __launch_bounds__(256) void lora_row_up_kernel(LoraKernelArgs a) {
     float s = 0.0f;
     for (int64_t r = 0; r < a.R; r += 8) {
         float q[8];
-        load_part(w, r, a.R, q);
+        floats_of(w, r, a.R, q);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(r + j < a.R ? t[r + j] : 0.0f, q[j], s);
     }
