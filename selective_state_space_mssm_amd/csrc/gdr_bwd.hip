@@ -358,10 +358,10 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
     };
     f32x4 dq_sum[KH] = {}, dk_sum[KH] = {};
     const int per = static_cast<int>(a.H / a.G);
-    constexpr int kItems = KP * 8 / THREADS, kTokens = 1;  // four columns of an element each; four elements of a token
-    const int to_t = tid >> 3, to_q = tid & 7;                         // and of tokens 32 further
-    float to_beta[kTokens], dbeta[kTokens];
-    f32x4 st_s[kItems], st_l[kItems], to_z[kTokens], to_e[kTokens], to_dy[kTokens];
+    constexpr int kItems = KP * 8 / THREADS;    // four columns of an element each
+    const int to_t = tid >> 3, to_q = tid & 7;  // eight lanes a token, four elements each
+    float to_beta, dbeta;
+    f32x4 st_s[kItems], st_l[kItems], to_z, to_e, to_dy;
     auto fetch = [&](int64_t h, int vb) {
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));  // addresses are computed here, not kept (and spilled) from before the loops
@@ -377,35 +377,27 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             st_l[i] = L.four(v * K + k, v < V && k < K);
         }
         const int v = vb + 4 * to_q;
-#pragma unroll
-        for (int i = 0; i < kTokens; ++i) {
-            const int t = to_t + 32 * i;
-            to_z[i] = z.four(t * V + v, v < V);
-            to_e[i] = e.four(t * V + v, v < V);
-            to_dy[i] = dy.four(t * static_cast<uint32_t>(v_stride) + v, v < V && t < ch.len);
-            if (vb == 0) to_beta[i] = View<float>(a.beta + ch.start * a.H + h).one(t * static_cast<uint32_t>(a.H), t < ch.len);
-        }
+        to_z = z.four(to_t * V + v, v < V);
+        to_e = e.four(to_t * V + v, v < V);
+        to_dy = dy.four(to_t * static_cast<uint32_t>(v_stride) + v, v < V && to_t < ch.len);
+        if (vb == 0) to_beta = View<float>(a.beta + ch.start * a.H + h).one(to_t * static_cast<uint32_t>(a.H), to_t < ch.len);
     };
     fetch(hg * per, 0);
     float g_log = View<float>(a.g + ch.start * a.H + hg * per).one(lane * static_cast<uint32_t>(a.H), lane < ch.len);
-    {   // the lengths of q and k: eight lanes a token
-        const int t = tid >> 3;
+    {   // the lengths of q and k
+        float k2 = 0.0f, q2 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 512 / THREADS; ++i) {
-            float k2 = 0.0f, q2 = 0.0f;
-#pragma unroll
-            for (int p = 0; p < KP / 64; ++p) {
-                const uint32_t col = 64 * p + 8 * (tid & 7), at = (t + 32 * i) * static_cast<uint32_t>(qk_stride) + col;
-                const bool in = t + 32 * i < ch.len && col < a.K;
-                k2 += sum_squares(k_rows.planes(at, in));
-                q2 += sum_squares(q_rows.planes(at, in));
-            }
-            k2 = group_sum<8>(k2);
-            q2 = group_sum<8>(q2);
-            if ((tid & 7) == 0) {
-                s_rk[t + 32 * i] = a.norm ? 1.0f / __builtin_sqrtf(k2 + kGdrNormEps) : 1.0f;
-                s_rq[t + 32 * i] = a.norm ? 1.0f / __builtin_sqrtf(q2 + kGdrNormEps) : 1.0f;
-            }
+        for (int p = 0; p < KP / 64; ++p) {
+            const uint32_t col = 64 * p + 8 * to_q, at = to_t * static_cast<uint32_t>(qk_stride) + col;
+            const bool in = to_t < ch.len && col < a.K;
+            k2 += sum_squares(k_rows.planes(at, in));
+            q2 += sum_squares(q_rows.planes(at, in));
+        }
+        k2 = group_sum<8>(k2);
+        q2 = group_sum<8>(q2);
+        if (to_q == 0) {
+            s_rk[to_t] = a.norm ? 1.0f / __builtin_sqrtf(k2 + kGdrNormEps) : 1.0f;
+            s_rq[to_t] = a.norm ? 1.0f / __builtin_sqrtf(q2 + kGdrNormEps) : 1.0f;
         }
     }
     if constexpr (!kShare) keep_keys();
@@ -423,11 +415,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         // (tokens i) of column block w for b > w, transposed (rows: tokens j) for b <= w, and of the diagonal both
         f32x4 yS[KH] = {}, zS[KH] = {}, uL[KH] = {}, half[5] = {};
         float both = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kTokens; ++i) {
-            dbeta[i] = 0.0f;
-            if (to_q == 0) s_beta[to_t + 32 * i] = to_beta[i];
-        }
+        dbeta = 0.0f;
+        if (to_q == 0) s_beta[to_t] = to_beta;
 #pragma unroll 1
         for (int vb = 0; vb < V; vb += 32) {
             __syncthreads();  // what is staged has been read
@@ -442,13 +431,10 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
                 put_four<3>(lds_s + at, State::kBytes, st_s[i]);
                 put_four<3>(lds_l + at, State::kBytes, st_l[i]);
             }
-#pragma unroll
-            for (int i = 0; i < kTokens; ++i) {
-                dbeta[i] = dot4(to_z[i], to_e[i], dbeta[i]);
-                Tokens::put<3>(lds_z, to_t + 32 * i, to_q, to_z[i]);
-                Tokens::put<3>(lds_u, to_t + 32 * i, to_q, to_beta[i] * to_e[i]);
-                Tokens::put<PL>(lds_dy, to_t + 32 * i, to_q, to_dy[i]);
-            }
+            dbeta = dot4(to_z, to_e, dbeta);
+            Tokens::put<3>(lds_z, to_t, to_q, to_z);
+            Tokens::put<3>(lds_u, to_t, to_q, to_beta * to_e);
+            Tokens::put<PL>(lds_dy, to_t, to_q, to_dy);
             __syncthreads();
             if (vb + 32 < V) fetch(h, vb + 32);
             int c = lane & 15, g = lane >> 4;
@@ -526,12 +512,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         const float row_hi = s_hi[row], row_lo = s_lo[row], row_beta = s_beta[row];
         const f32x4 zero = {0, 0, 0, 0};
         auto four = [&](const float* p, int b) { return *reinterpret_cast<const f32x4*>(p + 16 * b + 4 * g); };
-#pragma unroll
-        for (int i = 0; i < kTokens; ++i) {
-            const float sum = group_sum<8>(dbeta[i]);
-            const int t = to_t + 32 * i;
-            if (to_q == 0 && t < ch.len) a.dbeta[(ch.start + t) * a.H + h] = sum;
-        }
+        dbeta = group_sum<8>(dbeta);
+        if (to_q == 0 && to_t < ch.len) a.dbeta[(ch.start + to_t) * a.H + h] = dbeta;
         both = group4_sum(group_sum<16>(both));
         if (lane == 0) s_end[wave] = both;
 

@@ -150,10 +150,6 @@ struct View {
         if constexpr (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rsrc, offset(at, in), 0, 0))) << 16);
         else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, offset(at, in), 0, 0));
     }
-    __device__ __forceinline__ f32x2 two(uint32_t at, bool in) const {
-        static_assert(sizeof(T) == 4, "float32");
-        return __builtin_bit_cast(f32x2, words2(at, in));
-    }
     __device__ __forceinline__ f32x4 four(uint32_t at, bool in) const {
         if constexpr (sizeof(T) == 2) {
             const u32x2 a = words2(at, in);
@@ -234,11 +230,6 @@ __device__ __forceinline__ double decays_since_start(float gl, int lane) {
     }
     return b;
 }
-// exp(b_i - b_j) of sums kept as float32 and remainder
-__device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_j, float lo_j) {
-    return expf((hi_i - hi_j) + (lo_i - lo_j));
-}
-
 // ---- a chunk's rows in LDS --------------------------------------------------------
 
 // R rows (tokens, or value elements) of W columns, as bfloat16 planes.  A row's 16-byte pieces are
