@@ -15,8 +15,17 @@
 //     dq    = scale exp(b) dy S + (G dP) k
 //     dk    = -exp(b) dr S + M k    where a key is read with (its "row" part, decays exp(b))
 //           + D u L + (G dP)ᵀ q + Mᵀ k    where it is written with (exp(-b))
-//     db    = q . dq + k . dk_row - k . dk_column, and for the chunk's last token
-//             exp(b_C) <L, S> + sum_t D_t k_t . (L u_t) more;   dg_i = sum_{t >= i} db_t
+//
+// and of the decay of token i what passes it: the state to a token from i on or to the
+// chunk's end, a token before i to that end, and a token before i to one from i on,
+//
+//     dg_i  = sum_{t >= i} s_t + exp(b_C) <L, S> + sum_{j < i} w_j + sum_{j < i <= t} c_tj
+//     s_t   = q_t . scale exp(b_t) dy_t S - k_t . exp(b_t) dr_t S        w_j = k_j . D_j u_j L
+//
+// The pairs are the sum of d_t = (q . dq + k . dk_row - k . dk_column)_t - s_t + w_t over
+// t >= i, or the negative one over t < i: of all tokens it is zero, as all that is read
+// was written.  The sum over fewer tokens is taken, and where no state goes in (S = 0)
+// the first token's is exactly 0, as it has to be.
 //
 // Measured: 8,192 packed tokens, 32 heads of 128 x 128, bfloat16: the chain 370 us,
 // the chunks' gradients 528 us (921 MB, 1.7 TB/s; vector instructions busy for 38 %,
@@ -308,8 +317,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
     constexpr int kExchange = WAVES * 5 * 1024;
     constexpr bool kShare = kKeys + kStaged > 150 * 1024;  // q and k come after the sums, in the same place
     __shared__ __align__(16) uint8_t lds[kKeys + (kShare ? kExchange : kStaged)];
-    __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_dots[4][kC], s_end[16];
-    static_assert(sizeof(lds) + 3500 <= 160 * 1024 && kStaged >= kExchange && (!kShare || kKeys >= kStaged), "LDS of a compute unit, and its parts");
+    __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_states[2][kC], s_writes[2][kC], s_dots[4][kC], s_end[8];
+    static_assert(sizeof(lds) + 4500 <= 160 * 1024 && kStaged >= kExchange && (!kShare || kKeys >= kStaged), "LDS of a compute unit, and its parts");
     uint8_t *lds_k = lds, *lds_q = lds_k + PL * Keys::kBytes;
     uint8_t *lds_s = lds + (kShare ? 0 : kKeys), *lds_l = lds_s + 3 * State::kBytes, *lds_z = lds_l + 3 * State::kBytes,
             *lds_u = lds_z + 3 * Tokens::kBytes, *lds_dy = lds_u + 3 * Tokens::kBytes;
@@ -406,10 +415,12 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         const int64_t h = hg * per + hh;
         __syncthreads();  // the head before is done with LDS
         if (wave == 0) {
-            const double b = decays_since_start(g_log, lane);
+            int token = lane;
+            asm volatile("" : "+v"(token));  // what the sum needs of it is computed here, not kept (and spilled)
+            const double b = decays_since_start(g_log, token);
             const float hi = static_cast<float>(b);
-            s_hi[lane] = hi;
-            s_lo[lane] = static_cast<float>(b - hi);
+            s_hi[token] = hi;
+            s_lo[token] = static_cast<float>(b - hi);
         }
         // sums over the value elements; X: dy . u, or in the waves of the second half M: Z . u, of block b the rows
         // (tokens i) of column block w for b > w, transposed (rows: tokens j) for b <= w, and of the diagonal both
@@ -523,16 +534,22 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         const double end = static_cast<double>(s_hi[kC - 1]) + s_lo[kC - 1];
         const float to_end = whole_exp(end - (static_cast<double>(row_hi) + row_lo));
         const float fy = a.scale * in_chunk, fz = -in_chunk * row_beta;
-        float wrote = 0.0f, db = 0.0f;
+        float wrote = 0.0f, read = 0.0f, db = 0.0f;
         const int token = 16 * w + c;
 #pragma unroll
         for (int m = 0; m < KH; ++m) {
-            const f32x4 k4 = rk * from_tile(lds_k, token, state_column(kh * KH + m, 4 * g));
+            const int col = state_column(kh * KH + m, 4 * g);
+            const f32x4 k4 = rk * from_tile(lds_k, token, col), q4 = rq * from_tile(lds_q, token, col);
             yS[m] *= fy;
             zS[m] *= fz;
             uL[m] *= to_end;
+            read = dot4(q4, yS[m], read);
+            read = dot4(k4, zS[m], read);
             wrote = dot4(k4, uL[m], wrote);
         }
+        read = group4_sum(read);
+        wrote = group4_sum(wrote);
+        if (g == 0) s_states[kh][token] = read, s_writes[kh][token] = wrote;
         // summed over the tokens of blocks 2 s and 2 s + 1: the lane's row of X and M, and its column
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -571,23 +588,32 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         __builtin_amdgcn_sched_barrier(0);
         db = group4_sum(db);
         if (g == 0) s_db[kh][row] = db;
-        wrote = group4_sum(group_sum<16>(wrote));
-        if (lane == 0) s_end[8 + wave] = wrote;
         __syncthreads();
         if (wave == 0) {
-            double v = static_cast<double>(s_db[0][lane]) + s_db[1][lane];
-            if (lane == kC - 1) {
-                double states = 0.0, writes = 0.0;
+            int token = lane;
+            asm volatile("" : "+v"(token));  // as above
+            const double read = static_cast<double>(s_states[0][token]) + s_states[1][token];
+            const double wrote = static_cast<double>(s_writes[0][token]) + s_writes[1][token];
+            const double pairs = static_cast<double>(s_db[0][token]) + s_db[1][token] - read + wrote;
+            constexpr int kHalf = kC / 2;
+            const int in_half = token % kHalf;
+            const bool early = token < kHalf;  // fewer tokens before it
+            double from_here = early ? read : read + pairs, up_to_here = early ? wrote - pairs : wrote;
+            double other = early ? wrote : read;  // of the whole half: what the tokens of the other one lack
 #pragma unroll
-                for (int i = 0; i < WAVES; ++i) states += s_end[i], writes += s_end[8 + i];
-                v += static_cast<double>(whole_exp(end)) * states + writes;
+            for (int d = 1; d < kHalf; d *= 2) {
+                const double after = of_lane(from_here, token + d), before = of_lane(up_to_here, token - d);
+                if (in_half + d < kHalf) from_here += after;
+                if (in_half >= d) up_to_here += before;
+                other += of_lane(other, token ^ d);
             }
+            const double before = of_lane(up_to_here, token - 1);
+            double v = from_here + (in_half ? before : 0.0) + of_lane(other, token ^ kHalf);
+            double states = 0.0;
 #pragma unroll
-            for (int d = 1; d < kC; d *= 2) {  // from the last token on
-                const double o = __shfl_down(v, d);
-                if (lane + d < kC) v += o;
-            }
-            if (lane < ch.len) a.dg[(ch.start + lane) * a.H + h] = static_cast<float>(v);
+            for (int i = 0; i < WAVES; ++i) states += s_end[i];
+            v += static_cast<double>(whole_exp(end)) * states;
+            if (token < ch.len) a.dg[(ch.start + token) * a.H + h] = static_cast<float>(v);
         }
     }
     // through the division by their lengths

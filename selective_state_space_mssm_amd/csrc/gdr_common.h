@@ -220,12 +220,18 @@ __device__ __forceinline__ float whole_exp(double x) {
     const float f = static_cast<float>(x), e = expf(f);
     return __builtin_fmaf(e, static_cast<float>(x - f), e);
 }
+// Lane `from`'s value (of the 64, modulo 64).
+__device__ __forceinline__ double of_lane(double v, int from) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_ds_bpermute(from * 4, static_cast<int>(b)), hi = __builtin_amdgcn_ds_bpermute(from * 4, static_cast<int>(b >> 32));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
 // One wave, a token a lane: the sum of the chunk's log decays up to the lane's token.
 __device__ __forceinline__ double decays_since_start(float gl, int lane) {
     double b = gl < kGdrLeast ? kGdrLeast : gl;
 #pragma unroll
     for (int d = 1; d < kC; d *= 2) {
-        const double o = __shfl_up(b, d);
+        const double o = of_lane(b, lane - d);
         if (lane >= d) b += o;
     }
     return b;
