@@ -131,7 +131,9 @@ mssm_status mssm_linear(const mssm_linear_problem* p, const void* x, const float
  *   y (rows, out_dim)             in p->out_dtype: MSSM_F32, or MSSM_BF16 (not with
  *                                 MSSM_F32 operands); read and written in place,
  *                                 rounded once.  No input's buffer.
- * The inner sums stay float32 (in the workspace).  Many rows go by tiles, each
+ * The inner sums stay float32 (in the workspace).  A NaN or an infinity in a row,
+ * or in the weights of its adapter, spoils that row only (an infinity may come out
+ * as NaN).  Many rows go by tiles, each
  * computed once for every adapter that its rows name: rows of one adapter are
  * best neighbours, as the tokens of packed requests are.
  */

@@ -32,6 +32,8 @@
  * g is a log decay, g <= 0: values below -200 count as -200 (exp is 0 there).
  * The products of decays are taken of differences of their float64 sums, so that
  * long sums cost no accuracy.
+ * Sums of products and of squares of q and k (with norm_qk too) have to stay in
+ * float32's range: lengths below 1e19.
  * Offsets have to be in ascending order within 0 .. tokens.  They are read on
  * the device, clamped to that range: others give wrong results, but no access
  * out of bounds.  Tokens that belong to no sequence are neither read nor
@@ -70,7 +72,8 @@ typedef struct {
  * (tokens / 64 + seqs) has to be below 2^23, heads * seqs at most 2^20, heads *
  * value_dim and qk_heads * key_dim at most 2^22 (MSSM_ERR_SHAPE).  A NaN or an
  * infinity in a token spoils its chunk of 64 tokens and what follows it in its
- * sequence, in the heads that read it, and nothing else.
+ * sequence, in the heads that read it, and nothing else (as NaN: an infinity is cut
+ * into operands, which leaves none).
  */
 size_t mssm_gdr_fwd_workspace_bytes(const mssm_gdr_problem* p);
 

@@ -27,10 +27,10 @@
 // was written.  The sum over fewer tokens is taken, and where no state goes in (S = 0)
 // the first token's is exactly 0, as it has to be.
 //
-// Measured: 8,192 packed tokens, 32 heads of 128 x 128, bfloat16: the chain 370 us,
-// the chunks' gradients 528 us (921 MB, 1.7 TB/s; vector instructions busy for 38 %,
-// matrix instructions for 19 %); 16,384 tokens, 24 heads of 64 x 64, float32: 349 and
-// 484 us.
+// Measured: 8,192 packed tokens, 32 heads of 128 x 128, bfloat16: the chain 375 us,
+// the chunks' gradients 535 us (637 MB, 1.2 TB/s; vector instructions busy for 45 %,
+// matrix instructions for 21 %); 16,384 tokens, 24 heads of 64 x 64, float32: 350 and
+// 503 us.
 #include "gdr_common.h"
 
 namespace mssm {
@@ -662,8 +662,8 @@ template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
     // As the forward: chains of 128 columns once those of 64 are more than the compute
     // units.  1,024 tokens, the whole backward in us with 64 / 128 columns: key and value
-    // dim 128, 128 heads 411 / 448; 128 and 256, 72 heads 452 / 408; float32, 64 and 128,
-    // 128 heads 363 / 417, 64 and 256, 72 heads 477 / 390.  Eight waves have too few
+    // dim 128, 128 heads 375 / 407; 128 and 256, 72 heads 440 / 395; float32, 64 and 128,
+    // 128 heads 365 / 420, 64 and 256, 72 heads 480 / 393.  Eight waves have too few
     // registers for the float32 planes of a key dim of 128.
     if constexpr (sizeof(T) == 2 || KP == 64) {
         if (a.V > 64 && a.N * a.H * ((a.V + 63) / 64) > 256) return launch_c<T, KP, 8>(a, s);

@@ -9,11 +9,11 @@
 // shared by the waves of a workgroup.
 //
 // Measured, key and value dim 128, bfloat16: 4 sequences of 4,096 tokens, 40 heads,
-// 310 us, 4.8 us a chunk (matrix instructions busy for 50 % of the time on the
-// compute units in use, vector instructions for 53 %); 16 columns a workgroup, 1.7 us
+// 390 us, 6.1 us a chunk (matrix instructions busy for 50 % of the time on the
+// compute units in use, vector instructions for 51 %); 16 columns a workgroup, 1.8 us
 // a chunk.  For the backward the states and e are written too, 96 KB a chunk and
-// head: 8,192 packed tokens of 32 heads 332 us, 2.0 TB/s, the longest sequences alone
-// at the end.  float32, 64 and 64: 7 us a chunk, 4 waves a compute unit.
+// head: 8,192 packed tokens of 32 heads 389 us, 680 MB at 1.7 TB/s, the longest
+// sequences alone at the end.  float32, 64 and 64: 6.8 us a chunk, 4 waves a compute unit.
 #include "gdr_common.h"
 
 namespace mssm {
@@ -50,8 +50,8 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // kEnds: only the state behind a piece, and what the piece makes of any row of a state:
 // a second tile of each wave starts with unit rows (one for each key element) and sees
 // values of zero.
-// Whole sequences are a form of their own (with both in one, 364 us for 326 of 8,192
-// packed tokens of 32 heads with what the backward needs).
+// Whole sequences are a form of their own: with both in one, 8,192 packed tokens of 32
+// heads with what the backward needs took a tenth longer.
 template <typename T, int KP, int NW, int FORM, bool PIECES>
 __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     constexpr bool B16 = sizeof(T) == 2, TRAIN = FORM == kTrain, ENDS = FORM == kEnds;
@@ -696,17 +696,17 @@ template <typename T, int KP>
 hipError_t launch_k(const GdrArgs& a, hipStream_t s) {
     // A tile of 16 columns a workgroup while there are at most 512 (of key dim up to 64:
     // 256) of them.  1,024 tokens, with the chunks' own pass, us of this form / of the
-    // wide one: key and value dim 128, 64 heads (512 tiles) 81 / 86, 96 heads 118 / 97;
-    // 128 and 64, 128 heads (512) 94 / 100, 192 heads 137 / 117; dim 64, 64 heads (256)
-    // 45 / 66, 96 heads 75 / 72; 64 and 128, 32 heads (256) 44 / 64, 64 heads 70 / 67.
+    // wide one: key and value dim 128, 64 heads (512 tiles) 92 / 100, 96 heads 131 / 107;
+    // 128 and 64, 128 heads (512) 102 / 110, 192 heads 149 / 128; dim 64, 64 heads (256)
+    // 47 / 75, 96 heads 80 / 82; 64 and 128, 32 heads (256) 47 / 74, 64 heads 76 / 76.
     const GdrPieces p(a.T, a.N, a.H, a.K, a.V, a.dtype);
     if constexpr (sizeof(T) == 2) {
         if (!p.shift && a.N * a.H * (a.V / 16) <= (KP == 128 ? 512 : 256)) return launch_narrow<KP>(a, p, s);
     }
     // Workgroups of 128 columns once those of 64 are more than the 256 compute units; as
-    // above, us with 64 / 128 columns: 128 and 128, 128 heads 105 / 118, 160 heads 171 /
-    // 128; 128 and 256, 48 heads 83 / 100, 72 heads 153 / 109; float32, 64 and 128, 128
-    // heads 125 / 157, 160 heads 229 / 180.  Their eight waves have 256 registers each,
+    // above, us with 64 / 128 columns: 128 and 128, 128 heads 114 / 130, 160 heads 195 /
+    // 142; 128 and 256, 48 heads 97 / 115, 72 heads 178 / 125; float32, 64 and 128, 128
+    // heads 123 / 138, 160 heads 230 / 162.  Their eight waves have 256 registers each,
     // too few for the float32 planes of a key dim of 128.
     if constexpr (sizeof(T) == 2 || KP == 64) {
         if (a.V > 64 && p.count * a.H * ((a.V + 63) / 64) > 256) return launch_c<T, KP, 8>(a, p, s);
@@ -721,13 +721,14 @@ hipError_t launch_t(const GdrArgs& a, hipStream_t s) {
 }  // namespace
 
 // Pieces of 512 tokens or more, so long that their workgroups are at most the 256
-// compute units, if a sequence then has at least 8 of them (float32: 4).  What they
-// cost is the pass over all but the last for their ends and moves, with twice the
-// columns, and the join, 3 us a piece.  us in pieces / through whole sequences (bfloat16
-// by the form for few columns), key and value dim 128: bfloat16, 16 heads, 32,768
-// tokens (16 pieces) 595 / 998, 8,192 (16) 194 / 239, 32 heads, 16,384 (8) 568 / 603,
-// 4 heads, 4,096 (8) 125 / 126, 1 head, 65,536 (128) 470 / 1,552; float32, 16 heads,
-// 2,048 tokens (4) 171 / 255, 8,192 (8) 345 / 959.
+// compute units, if a sequence of the mean length (their own are known on the device
+// only) then has at least 8 of them (float32: 4).  What they cost is the pass over all
+// but the last for their ends and moves, with twice the columns, and the join, 3 us a
+// piece.  us in pieces / through whole sequences (bfloat16 by the form for few columns),
+// key and value dim 128: bfloat16, 16 heads, 32,768 tokens (16 pieces) 650 / 1,085,
+// 8,192 (16) 210 / 285, 32 heads, 16,384 (8) 620 / 618, 4 heads, 4,096 (8) 123 / 140,
+// 1 head, 65,536 (128) 479 / 1,917; float32, 16 heads, 2,048 tokens (4) 171 / 269,
+// 8,192 (8) 366 / 1,010.
 GdrPieces::GdrPieces(int64_t T, int64_t N, int64_t H, int64_t K, int64_t V, int dtype) : count(N) {
     const int64_t columns = V > 64 && (dtype == MSSM_BF16 || K <= 64) ? 128 : 64, least = dtype == MSSM_BF16 ? 8 : 4;
     const int64_t units = N * H * (((K > V ? K : V) + columns - 1) / columns), each = (T + N - 1) / N;

@@ -8,9 +8,9 @@
 // since each mostly has an adapter of its own and its weights are read once.
 // y is read and written once, rounded once.
 //
-// Measured: 16,384 8-bit rows, 2560 -> 10240, rank 64, 16 adapters in runs: down 48 us,
-// up 202 us (y, 671 MB, at 3.3 TB/s; bound by memory and its latency); 32 rows of an
-// adapter each, rank 16: 5.9 and 5.2 us.
+// Measured: 16,384 8-bit rows, 2560 -> 10240, rank 64, 16 adapters in runs: down 47 us,
+// up 206 us (y, 671 MB, at 3.3 TB/s; bound by memory and its latency); 32 rows of an
+// adapter each, rank 16: 3.8 and 3.9 us, launches.
 #include "block.h"
 #include "planes.h"
 
@@ -430,9 +430,19 @@ LoraPlan plan_lora(int64_t M, int64_t K, int64_t R, bool f32) {
     p.rank = (R + 15) / 16 * 16;
     if (p.rank == 48) p.rank = 64;
     if (p.rank > 64) p.rank = 128;
-    // the rank's and the rows' accumulators of a tile have to fit the registers, and float32 has three planes of each operand
+    // Rows for themselves up to 64: the index is on the device, and where each row has an adapter of its own a tile
+    // computes 16 rows for every one.  us by rows / by tiles of 16, bfloat16, 2560 -> 10240, rank 16: 32 rows of 32
+    // adapters 14 / 35, 64 of 64 13 / 35, 64 of 2 in runs 13 / 11; rank 64: 64 rows of 64 67 / 58, of 2 in runs 27 / 11,
+    // 128 of 2 in runs 48 / 12.
+    // Tiles of 16 up to 2,048, then larger ones, whose weights are read less often.  us by 16 / 64, bfloat16, in runs of
+    // 8 adapters: rank 64, 2,048 rows 46 / 48, 4,096 75 / 68; by 16 / 32: rank 128, 2,048 rows 67 / 60, 4,096 118 / 91;
+    // float32, 1536 -> 1536, rank 16, 2,048 rows 16 / 17, 4,096 25 / 23.  Rows of many adapters in any order lose by
+    // larger tiles (4,096 of 64, rank 16: 243 / 449).
+    // The rank's and the rows' accumulators of a tile have to fit the registers, and float32 has three planes of each operand.
     p.rows = M <= 64 ? 1 : M <= 2048 || (f32 && R > 64) ? 16 : f32 || R > 64 ? 32 : 64;
     const int64_t tiles = (M + p.rows - 1) / p.rows;
+    // Parts of K of at least 256, while there are fewer workgroups than compute units.  us in one part / in several:
+    // 300 rows (19 tiles) of rank 16 18 / 12 (8 parts), 1,000 26 / 21 (4); 2,000 of rank 64 60 / 51 (2).
     int64_t splits = 1;
     if (p.rows > 1)
         while (splits < 8 && tiles * splits < 256 && K / (splits * 2) >= 256) splits *= 2;
