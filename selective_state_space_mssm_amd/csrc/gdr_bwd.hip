@@ -22,10 +22,15 @@
 //     dg_i  = sum_{t >= i} s_t + exp(b_C) <L, S> + sum_{j < i} w_j + sum_{j < i <= t} c_tj
 //     s_t   = q_t . scale exp(b_t) dy_t S - k_t . exp(b_t) dr_t S        w_j = k_j . D_j u_j L
 //
-// The pairs are the sum of d_t = (q . dq + k . dk_row - k . dk_column)_t - s_t + w_t over
-// t >= i, or the negative one over t < i: of all tokens it is zero, as all that is read
-// was written.  The sum over fewer tokens is taken, and where no state goes in (S = 0)
-// the first token's is exactly 0, as it has to be.
+// Of the pairs of different tokens, c_tj, row t has r_t = q . dq + k . dk_row - s_t and
+// column j l_j = k . dk_column - w_j, and those of (j < i <= t) are sum_{m < i} l_m - r_m:
+//
+//     dg_i  = sum_{t >= i} s_t + exp(b_C) <L, S> + sum_{m < i} (s - q . dq - k . dk_row + k . dk_column)_m
+//
+// Nothing is added here and taken away there but what is part of some token's dg (a
+// token with itself, dP_ii, comes to dq and dk behind that): strong decays, which make
+// all of it small, cost no accuracy, and where no state goes in (S = 0) the first
+// token's is 0.
 //
 // Measured: 8,192 packed tokens, 32 heads of 128 x 128, bfloat16: the chain 375 us,
 // the chunks' gradients 535 us (637 MB, 1.2 TB/s; vector instructions busy for 45 %,
@@ -317,8 +322,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
     constexpr int kExchange = WAVES * 5 * 1024;
     constexpr bool kShare = kKeys + kStaged > 150 * 1024;  // q and k come after the sums, in the same place
     __shared__ __align__(16) uint8_t lds[kKeys + (kShare ? kExchange : kStaged)];
-    __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_states[2][kC], s_writes[2][kC], s_dots[4][kC], s_end[8];
-    static_assert(sizeof(lds) + 4500 <= 160 * 1024 && kStaged >= kExchange && (!kShare || kKeys >= kStaged), "LDS of a compute unit, and its parts");
+    __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_beta[kC], s_rk[kC], s_rq[kC], s_db[2][kC], s_states[2][kC], s_diag[kC], s_dots[4][kC], s_end[8];
+    static_assert(sizeof(lds) + 4300 <= 160 * 1024 && kStaged >= kExchange && (!kShare || kKeys >= kStaged), "LDS of a compute unit, and its parts");
     uint8_t *lds_k = lds, *lds_q = lds_k + PL * Keys::kBytes;
     uint8_t *lds_s = lds + (kShare ? 0 : kKeys), *lds_l = lds_s + 3 * State::kBytes, *lds_z = lds_l + 3 * State::kBytes,
             *lds_u = lds_z + 3 * Tokens::kBytes, *lds_dy = lds_u + 3 * Tokens::kBytes;
@@ -489,7 +494,8 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         }
         __syncthreads();  // what was staged has been read
         f32x4* exchange = reinterpret_cast<f32x4*>(lds + kKeys) + wave * 5 * 64 + lane;  // read from there: they would not fit the registers
-        {   // with their decays: X_ij = scale G_ij dP_ij (j <= i), M_ij = -G_ij beta_i Z_i . u_j (j < i)
+        {   // with their decays: X_ij = scale G_ij dP_ij, M_ij = -G_ij beta_i Z_i . u_j (j < i); X_ii apart
+            float diagonal = 0.0f;
             const float row_hi = s_hi[row], row_lo = s_lo[row], row_beta = s_beta[row];
 #pragma unroll
             for (int n = 0; n < 5; ++n) {
@@ -501,11 +507,13 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
                 for (int r = 0; r < 4; ++r) {
                     const int other = 16 * b + 4 * g + r, ahead = columns ? other - row : row - other;  // i - j
                     const float sum = (hi[r] - row_hi) + (lo[r] - row_lo);
-                    const float d = fast_exp2(ahead >= 0 ? (columns ? sum : -sum) * kLog2e : -1000.0f);  // 0 there
-                    half[n][r] *= kh == 0 ? a.scale * d : ahead > 0 ? -d * (columns ? beta[r] : row_beta) : 0.0f;
+                    const float d = fast_exp2(ahead > 0 ? (columns ? sum : -sum) * kLog2e : -1000.0f);  // 0 there
+                    if (n < 4) diagonal = ahead == 0 ? half[n][r] : diagonal;
+                    half[n][r] *= kh == 0 ? a.scale * d : -d * (columns ? beta[r] : row_beta);
                 }
                 exchange[n * 64] = half[n];
             }
+            if (kh == 0 && g == c >> 2) s_diag[row] = a.scale * diagonal;
         }
         __syncthreads();
         if constexpr (kShare) {
@@ -534,7 +542,7 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
         const double end = static_cast<double>(s_hi[kC - 1]) + s_lo[kC - 1];
         const float to_end = whole_exp(end - (static_cast<double>(row_hi) + row_lo));
         const float fy = a.scale * in_chunk, fz = -in_chunk * row_beta;
-        float wrote = 0.0f, read = 0.0f, db = 0.0f;
+        float read = 0.0f, db = 0.0f;
         const int token = 16 * w + c;
 #pragma unroll
         for (int m = 0; m < KH; ++m) {
@@ -545,11 +553,9 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             uL[m] *= to_end;
             read = dot4(q4, yS[m], read);
             read = dot4(k4, zS[m], read);
-            wrote = dot4(k4, uL[m], wrote);
         }
         read = group4_sum(read);
-        wrote = group4_sum(wrote);
-        if (g == 0) s_states[kh][token] = read, s_writes[kh][token] = wrote;
+        if (g == 0) s_states[kh][token] = read;
         // summed over the tokens of blocks 2 s and 2 s + 1: the lane's row of X and M, and its column
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -576,14 +582,15 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             }
         }
         __builtin_amdgcn_sched_barrier(0);
+        const float diagonal = s_diag[token];
 #pragma unroll
         for (int m = 0; m < KH; ++m) {
             const int col = state_column(kh * KH + m, 4 * g);
             const f32x4 k4 = rk * from_tile(lds_k, token, col), q4 = rq * from_tile(lds_q, token, col);
             db = dot4(q4, yS[m], db);
             db = dot4(k4, zS[m] - uL[m], db);
-            dq_sum[m] += yS[m];
-            dk_sum[m] += zS[m] + uL[m];
+            dq_sum[m] += yS[m] + diagonal * k4;
+            dk_sum[m] += zS[m] + uL[m] + diagonal * q4;
         }
         __builtin_amdgcn_sched_barrier(0);
         db = group4_sum(db);
@@ -593,22 +600,15 @@ __global__ __launch_bounds__(512, 2) void gdr_grad_kernel(GradArgs a) {
             int token = lane;
             asm volatile("" : "+v"(token));  // as above
             const double read = static_cast<double>(s_states[0][token]) + s_states[1][token];
-            const double wrote = static_cast<double>(s_writes[0][token]) + s_writes[1][token];
-            const double pairs = static_cast<double>(s_db[0][token]) + s_db[1][token] - read + wrote;
-            constexpr int kHalf = kC / 2;
-            const int in_half = token % kHalf;
-            const bool early = token < kHalf;  // fewer tokens before it
-            double from_here = early ? read : read + pairs, up_to_here = early ? wrote - pairs : wrote;
-            double other = early ? wrote : read;  // of the whole half: what the tokens of the other one lack
+            double from_here = read, up_to_here = read - s_db[0][token] - s_db[1][token];
 #pragma unroll
-            for (int d = 1; d < kHalf; d *= 2) {
+            for (int d = 1; d < kC; d *= 2) {
                 const double after = of_lane(from_here, token + d), before = of_lane(up_to_here, token - d);
-                if (in_half + d < kHalf) from_here += after;
-                if (in_half >= d) up_to_here += before;
-                other += of_lane(other, token ^ d);
+                if (token + d < kC) from_here += after;
+                if (token >= d) up_to_here += before;
             }
             const double before = of_lane(up_to_here, token - 1);
-            double v = from_here + (in_half ? before : 0.0) + of_lane(other, token ^ kHalf);
+            double v = from_here + (token ? before : 0.0);
             double states = 0.0;
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) states += s_end[i];
