@@ -32,10 +32,10 @@
 // all of it small, cost no accuracy, and where no state goes in (S = 0) the first
 // token's is 0.
 //
-// Measured: 8,192 packed tokens, 32 heads of 128 x 128, bfloat16: the chain 375 us,
-// the chunks' gradients 535 us (637 MB, 1.2 TB/s; vector instructions busy for 45 %,
-// matrix instructions for 21 %); 16,384 tokens, 24 heads of 64 x 64, float32: 350 and
-// 503 us.
+// Measured: 8,192 packed tokens, 32 heads of 128 x 128, bfloat16: the chain 370 us,
+// the chunks' gradients 503 us (628 MB, 1.2 TB/s; vector instructions busy for 45 %,
+// matrix instructions for 21 %); 16,384 tokens, 24 heads of 64 x 64, float32: 342 and
+// 464 us.
 #include "gdr_common.h"
 
 namespace mssm {

@@ -12,7 +12,7 @@
 // 390 us, 6.1 us a chunk (matrix instructions busy for 50 % of the time on the
 // compute units in use, vector instructions for 51 %); 16 columns a workgroup, 1.8 us
 // a chunk.  For the backward the states and e are written too, 96 KB a chunk and
-// head: 8,192 packed tokens of 32 heads 389 us, 680 MB at 1.7 TB/s, the longest
+// head: 8,192 packed tokens of 32 heads 378 us, 681 MB at 1.8 TB/s, the longest
 // sequences alone at the end.  float32, 64 and 64: 6.8 us a chunk, 4 waves a compute unit.
 #include "gdr_common.h"
 

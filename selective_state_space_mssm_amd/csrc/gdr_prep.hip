@@ -24,7 +24,7 @@
 // Measured: 16,384 tokens, 40 heads, key dim 128, bfloat16, 124 us: 431 MB at 3.5
 // TB/s, 76 % of them written (N and P, 30 KB a chunk and head); vector instructions
 // are busy for half of it, matrix instructions for a fifth.  8,192 tokens of 32
-// heads take 57 us, 83 us with the transposes for the backward.
+// heads take 57 us, 82 us with the transposes for the backward.
 #include "gdr_common.h"
 
 namespace mssm {
