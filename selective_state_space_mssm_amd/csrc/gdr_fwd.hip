@@ -105,8 +105,8 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void gdr_fwd_kernel(FwdArgs a) {
     const RowsToLds<VC, NW> value_loads(static_cast<uint32_t>(v_stride), static_cast<int>(a.V - vw), w, lane);
     FloatRows<KP, NW * 64> fk, fq;
     Planes<2> pw[kOwn];
-    // In four parts: a compute unit takes 1 KB into LDS in about 30 cycles, the 80 KB
-    // of a bfloat16 chunk in 2,500, for which its waves would otherwise wait at once.
+    // In four parts: a compute unit takes 1 KB into LDS in about 30 cycles, the 67 KB
+    // of a bfloat16 chunk in 2,000, for which its waves would otherwise wait at once.
     constexpr int kParts = 4;
     auto fetch = [&](int64_t chunk, int half, int part) {
         const int len = length(chunk);
